@@ -15,3 +15,7 @@ from ._binding import (  # noqa: F401
     EP_ERRBIT_TIMEOUT, selftest_bounded_wait, ep_combine_backward, ep_dispatch_backward,
     ep_dispatch_fp8, alloc_recv_planned, ep_layout_dispatch, plan_layout,
 )
+from ._ops import (  # noqa: F401
+    alloc_fp8, alloc_rmsnorm, ep_combine_weighted_backward, ep_rmsnorm, ep_rmsnorm_backward,
+    ep_swiglu, ep_swiglu_backward, sf_layout,
+)

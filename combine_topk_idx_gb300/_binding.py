@@ -134,6 +134,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_layout_dispatch.argtypes = [ctypes.POINTER(EpConfigC), vp, vp, vp, vp, vp, vp, vp, vp,
                                        ctypes.POINTER(vp), ctypes.POINTER(EpLayoutInfoC)]
     lib.ep_layout_dispatch.restype = ctypes.c_int
+    pi64 = ctypes.POINTER(i64)
+    lib.ep_sf_layout.argtypes = [vp, i32, pi64, pi64, pi64, pi64]
+    lib.ep_sf_layout.restype = ctypes.c_int
+    lib.ep_rmsnorm.argtypes = [i32, i32, vp, i64, vp, i64, vp, i32, ctypes.c_float, vp, vp, vp, vp,
+                               i64, i64, vp, vp]
+    lib.ep_rmsnorm.restype = ctypes.c_int
+    lib.ep_rmsnorm_backward.argtypes = [i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.ep_rmsnorm_backward.restype = ctypes.c_int
+    lib.ep_swiglu.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.ep_swiglu.restype = ctypes.c_int
+    lib.ep_swiglu_backward.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.ep_swiglu_backward.restype = ctypes.c_int
+    lib.ep_combine_weighted_backward.argtypes = [vp] * 11
+    lib.ep_combine_weighted_backward.restype = ctypes.c_int
     if lib.ep_abi_version() != EP_ABI_VERSION:
         raise RuntimeError("libep.so ABI version does not match this binding")
     _lib = lib

@@ -9,18 +9,7 @@
 #include <thread>
 #include <vector>
 
-#include "ep_internal.cuh"
-
-struct ep_handle {
-  ep_config cfg;
-  int device;
-  cudaStream_t stream;
-  void *dmem;
-  ep::LayoutParams lp;
-  int64_t rows_alloc;
-  int64_t sf_hidden_stride, sf_token_stride, sf_numel, sf_expert_stride;
-  float *tok_scale;
-};
+#include "ep_host.cuh"
 
 namespace ep {
 
@@ -93,10 +82,6 @@ namespace {
 // Host waits poll without yielding the CPU for this long, then yield between
 // polls.
 constexpr int kTightPollMs = 2;
-
-inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Bounds {
   int64_t per_rank, global, rows;
@@ -197,6 +182,8 @@ SyncPool &sync_pool() {
   return *p;
 }
 
+}  // namespace
+
 // A memory pool per device for handle metadata: freed blocks are kept for
 // reuse (release threshold = max), so steady-state ep_layout calls do not map
 // new device memory.  Lives until process exit.
@@ -229,20 +216,36 @@ ep_status cuda_status(cudaError_t e) {
   return EP_ERR_CUDA;
 }
 
-}  // namespace
+cudaError_t workspace_alloc(size_t bytes, cudaStream_t s, void **out) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &cs);
+  if (e != cudaSuccess) return e;
+  if (cs != cudaStreamCaptureStatusNone) return cudaMallocAsync(out, bytes, s);
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaMemPool_t pool = nullptr;
+  e = handle_pool(dev, &pool);
+  if (e != cudaSuccess) return e;
+  return cudaMallocFromPoolAsync(out, bytes, pool, s);
+}
+
+cudaError_t workspace_free(void *p, cudaStream_t s) { return cudaFreeAsync(p, s); }
+
 }  // namespace ep
 
 using ep::align_up;
 using ep::aligned;
 
 namespace ep {
-namespace {
 
 ep_status check_device(const ep_handle *h) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return EP_ERR_CUDA;
   return dev == h->device ? EP_OK : EP_ERR_INVALID_ARG;
 }
+
+namespace {
 
 DispatchParams dispatch_params(const ep_handle *h, const void *x, const float *topk_weights,
                                void *recv_x, float *recv_sf, float *recv_topk_weights,

@@ -42,6 +42,8 @@
 
 #include "ep_internal.cuh"
 #include "ep_ptx.cuh"
+#include "ep_quant.cuh"
+#include "ep_rows.cuh"
 
 namespace ep {
 namespace {
@@ -71,16 +73,6 @@ struct TokenMeta {
   int n;
   int t;  // source token, or -1: no more tokens for this CTA
 };
-
-// Expert whose padding range holds padding row q: the last e with psum_pad[e] <= q.
-__device__ __forceinline__ int padding_expert(const int32_t *psum_pad, int E, int q) {
-  int lo = 0, hi = E;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(psum_pad + mid) <= q) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
 
 // One work item of alignment padding: up to kPadRowsPerItem consecutive
 // padding rows (numbered across all experts): zero payload, scales, weight.
@@ -125,41 +117,6 @@ struct Routing {
   int d, e;
   float w;
 };
-
-// e4m3 bytes of x / sc for eight elements (f: x as fp32), equal to the
-// round-to-nearest-even, saturating conversion of the IEEE fp32 quotients.
-// With r the reciprocal of sc within 2 ulp (relative error 2^-22), the
-// products x * r * (1 -+ 2^-17), each rounded, bracket the rounded quotient
-// strictly (every rounding error is below 2^-21 of the 2^-17 margin).  The
-// conversion is monotonic in the magnitude, so where both ends of the
-// bracket convert to the same byte, the quotient does too; where they differ
-// -- a rounding boundary of the e4m3 grid inside the bracket, about 1 element
-// in 200 of BF16 data, mostly exact ties -- that pair of quotients is taken
-// by IEEE division (per pair, so a warp runs the divisions only for pairs
-// where some lane needs them).  Outside sc in [2^-120, 2^120) the reciprocal
-// loses its accuracy and every quotient is a division.
-__device__ __forceinline__ uint2 e4m3_block8(const float *f, float sc) {
-  const uint32_t sb = __float_as_uint(sc);
-  uint32_t c[4];
-  if (sb >= 0x03800000u && sb < 0x7B800000u) {
-    const float r = __fdividef(1.0f, sc);
-    const float rl = r * 0.99999237060546875f, rh = r * 1.00000762939453125f;  // 1 -+ 2^-17
-    const uint64_t rl2 = f32x2_pack(rl, rl), rh2 = f32x2_pack(rh, rh);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t x2 = f32x2_pack(f[2 * q], f[2 * q + 1]);
-      const uint64_t lo = f32x2_mul_rn(x2, rl2), hi = f32x2_mul_rn(x2, rh2);
-      c[q] = cvt_e4m3x2(f32x2_lo(lo), f32x2_hi(lo));
-      if (c[q] != cvt_e4m3x2(f32x2_lo(hi), f32x2_hi(hi)))
-        c[q] = cvt_e4m3x2(__fdiv_rn(f[2 * q], sc), __fdiv_rn(f[2 * q + 1], sc));
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      c[q] = cvt_e4m3x2(__fdiv_rn(f[2 * q], sc), __fdiv_rn(f[2 * q + 1], sc));
-  }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
 
 __device__ __forceinline__ Routing load_routing(const DispatchParams &p, int t, int lane) {
   Routing r{-1, -1, 0.f};

@@ -140,6 +140,102 @@ struct CombineWeightsParams {
   int do_expand;
 };
 
+// Root-mean-square norm with the residual's addition (rows of x and residual
+// may be strided; everything else is dense).
+struct NormParams {
+  const uint16_t *x, *residual;  // bf16 [T, H] with row strides; residual or nullptr
+  int64_t x_stride, res_stride;
+  const void *gamma;             // [H] bf16, or fp32 with gamma_f32
+  int gamma_f32;
+  float eps;
+  int T, H;
+  uint16_t *res_out;             // [T, H] x + residual, or nullptr
+  uint16_t *y;                   // [T, H] bf16 result, or nullptr
+  uint8_t *q;                    // [T, H] e4m3 result, or nullptr (then sf too)
+  float *sf;                     // scale (t, j) at sf[t * sf_ts + j * sf_hs]
+  int64_t sf_ts, sf_hs;
+  float *rstd;                   // [T] or nullptr
+};
+
+struct NormBackwardParams {
+  const uint16_t *gy;            // [T, H] gradient of the normalised rows
+  const uint16_t *r;             // [T, H] what the forward normalised (bf16)
+  const uint16_t *gres;          // [T, H] gradient of r from elsewhere, or nullptr
+  const void *gamma;
+  int gamma_f32;
+  const float *rstd;             // [T]
+  int T, H;
+  uint16_t *gx;                  // [T, H]
+  float *ggamma;                 // [H] or nullptr
+  float *part;                   // [parts, H] workspace of the column sums
+  int parts;
+};
+
+// Rows of a layout, for kernels that work on rows in place: which rows are in
+// use, and where a row's scales lie.
+struct RowsParams {
+  const int32_t *num_rows;  // device total rows, or nullptr: `rows` rows, all in use
+  const int32_t *meta;      // [rows, 2] source (token, slot); token -1: padding
+  const int32_t *psum_e, *cnt_e;  // fixed-capacity layout: item i of expert e is row
+  int E, fixed_cap;               // e * fixed_cap + i - psum_e[e], rows past cnt_e unused
+  int zero_padding;         // padding rows of the outputs are zeroed
+  int64_t rows;             // rows allocated
+};
+
+// Where the scale of (row, block j) lies: sf[row * ts + j * hs], or with
+// es > 0 (fixed-capacity slabs) sf[(row / cap) * es + (row % cap) * ts + j * hs].
+struct SfLayout {
+  int64_t ts, hs, es, numel;
+  int cap;
+};
+
+struct SwigluParams {
+  RowsParams r;
+  const uint16_t *h;        // [rows, 2F] gate | up
+  const float *row_w;       // [rows] or nullptr
+  int F;
+  uint16_t *act;            // [rows, F] bf16, or nullptr
+  uint8_t *q;               // [rows, F] e4m3, or nullptr
+  float *sf;
+  SfLayout sfl;
+  uint8_t *ckpt;            // [rows, 2F] e4m3, or nullptr
+  float *ckpt_sf;           // [rows, 2F / 128]
+};
+
+struct SwigluBackwardParams {
+  RowsParams r;
+  const uint16_t *ga;       // [rows, F]
+  const uint8_t *ckpt;
+  const float *ckpt_sf;
+  const float *row_w;
+  int F;
+  uint16_t *gh;             // [rows, 2F] bf16, or nullptr
+  uint8_t *q;               // [rows, 2F] e4m3, or nullptr
+  float *sf;
+  SfLayout sfl;
+  float *gw;                // [rows] or nullptr
+};
+
+struct CombineGradParams {
+  const uint16_t *g;        // [T, H] gradient of the combined tokens
+  const uint16_t *y;        // [rows_alloc, H]
+  const float *topk_w;      // [T, K]
+  const int32_t *topk32, *dst;   // [T, K]
+  const uint16_t *ebias;    // [E, H] or nullptr
+  const int32_t *psum_e, *cnt_e, *psum_pad;
+  int T, K, E, H;
+  int zero_padding;
+  int64_t rows_alloc;
+  uint16_t *gy;             // [rows_alloc, H] bf16, or nullptr
+  uint8_t *q;               // [rows_alloc, H] e4m3, or nullptr
+  float *sf;
+  SfLayout sfl;
+  float *gw;                // [T, K] or nullptr
+  float *gbias;             // [E, H] or nullptr
+  float *part;              // [parts, E, H] workspace of the bias sums
+  int parts;
+};
+
 // Dynamic shared memory above which a kernel must opt in with
 // cudaFuncAttributeMaxDynamicSharedMemorySize: the 48 KB default window less
 // a margin for the kernels' static shared memory (all below 8 KB).
@@ -156,6 +252,17 @@ cudaError_t launch_dispatch(const DispatchParams &p, int mode, int col_major,
 cudaError_t launch_combine(const CombineParams &p, int sm_cap, cudaStream_t s);
 cudaError_t launch_combine_weights(const CombineWeightsParams &p, cudaStream_t s);
 
+// out[c] = sum over i < parts of part[i * n + c], in a fixed order.
+cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
+                              cudaStream_t s);
+cudaError_t launch_norm(const NormParams &p, cudaStream_t s);
+int norm_backward_parts(const NormBackwardParams &p);
+cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s);
+cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s);
+cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s);
+int combine_grad_parts(const CombineGradParams &p);
+cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s);
+
 // Device facts, cached per device.
 int device_sm_count(int device);
 
@@ -167,5 +274,23 @@ int device_sm_count(int device);
 // applies the opt-in only.
 cudaError_t launch_geometry(const void *func, int threads, size_t smem, int *device,
                             int *per_sm);
+
+// Launch with programmatic dependent launch: the kernel may start while its
+// predecessor drains and calls griddep_wait() before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, int threads, size_t smem,
+                       cudaStream_t s, A... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(grid);
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, args...);
+}
 
 }  // namespace ep

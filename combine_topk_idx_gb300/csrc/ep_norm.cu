@@ -1,0 +1,260 @@
+// Root-mean-square norm with the residual's addition, and its gradient.
+//
+// Forward, per row of H elements:
+//   s = x + residual (fp32), r = bf16(s), k = 1 / sqrt(mean(s^2) + eps),
+//   v = s * k * gamma; written as bf16(v) and/or as e4m3 bytes with one fp32
+//   scale per 1x128 block (amax / 448), the input of a pre-quantised dispatch.
+// Backward, with xh = r * k:
+//   m = mean(gy * gamma * xh), gx = k * (gy * gamma - xh * m) + gres,
+//   ggamma = sum over rows of gy * xh.
+//
+// Both read each input once and write each output once: a row stays in
+// registers between the sum and the result, one 16-byte vector of eight
+// elements per thread and step, so 16 neighbouring lanes hold one scale block.
+#include <algorithm>
+
+#include "ep_internal.cuh"
+#include "ep_ptx.cuh"
+#include "ep_quant.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+
+// Sum over the threads of a row: a warp, or the whole CTA (`red` then holds
+// one value per warp; one barrier per call, the caller alternates buffers).
+template <bool WARP_ROW>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (WARP_ROW) return v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < nw ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void load_gamma(const void *gamma, int f32, int v, float *f) {
+  if (f32) {
+    const float4 a = __ldg(static_cast<const float4 *>(gamma) + 2 * v);
+    const float4 b = __ldg(static_cast<const float4 *>(gamma) + 2 * v + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    bf16x8_to_f32(ld_cached_v4(static_cast<const uint4 *>(gamma) + v), f);
+  }
+}
+
+// NV vectors per thread; WARP_ROW: one warp per row, else one CTA per row.
+template <int NV, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads)
+    norm_kernel(NormParams p) {
+  __shared__ float red[32];
+  const int tpr = WARP_ROW ? 32 : blockDim.x;  // threads per row
+  const int tid = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t t = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                             : (int64_t)blockIdx.x;
+  if (WARP_ROW && t >= p.T) return;
+  const int nvec = p.H / 8;
+  const float inv_h = 1.0f / (float)p.H;
+  griddep_wait();
+  float f[NV][8];
+  float ss = 0.f;
+  uint4 xv[NV], rv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * tpr + tid;
+    xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+    if (v < nvec) {
+      xv[i] = ld_stream_v4(p.x + t * p.x_stride + v * 8);
+      // a plain load: the sum may be written over the residual
+      if (p.residual != nullptr) rv[i] = ld_plain_v4(p.residual + t * p.res_stride + v * 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * tpr + tid;
+    bf16x8_to_f32(xv[i], f[i]);
+    if (p.residual != nullptr) {
+      float r[8];
+      bf16x8_to_f32(rv[i], r);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] += r[q];
+    }
+    if (v < nvec && p.res_out != nullptr)
+      st_stream_v4(p.res_out + t * (int64_t)p.H + v * 8, f32_to_bf16x8(f[i]));
+#pragma unroll
+    // each term over H before the sum: the mean then fits fp32 as long as it
+    // does itself, although the sum of squares may not
+    for (int q = 0; q < 8; ++q) ss = fmaf(f[i][q] * inv_h, f[i][q], ss);
+  }
+  ss = row_sum<WARP_ROW>(ss, red);
+  const float k = rsqrtf(ss + p.eps);
+  if (tid == 0 && p.rstd != nullptr) p.rstd[t] = k;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * tpr + tid;
+    if (v - (tid & 31) >= nvec) break;  // whole warps only: the scale blocks shuffle
+    const bool valid = v < nvec;
+    if (valid) {
+      float g[8];
+      load_gamma(p.gamma, p.gamma_f32, v, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] = f[i][q] * k * g[q];
+      if (p.y != nullptr) st_stream_v4(p.y + t * (int64_t)p.H + v * 8, f32_to_bf16x8(f[i]));
+    }
+    if (p.q != nullptr) {
+      float sc;
+      const uint2 b = quantise_block(f[i], &sc);
+      if (valid) {
+        *reinterpret_cast<uint2 *>(p.q + t * (int64_t)p.H + v * 8) = b;
+        if ((v & 15) == 0) p.sf[t * p.sf_ts + (v >> 4) * p.sf_hs] = sc;
+      }
+    }
+  }
+}
+
+template <int NV, bool WARP_ROW>
+cudaError_t launch_forward(const NormParams &p, int threads, cudaStream_t s) {
+  const int rows = WARP_ROW ? threads / 32 : 1;
+  return launch_pdl(norm_kernel<NV, WARP_ROW>, (unsigned)((p.T + (int64_t)rows - 1) / rows),
+                    threads, 0, s, p);
+}
+
+// Persistent CTAs take rows blockIdx.x, + gridDim.x, ...; every thread keeps
+// its columns, so the gradient of gamma is summed in registers and leaves as
+// one row of partial sums per CTA.
+template <int NV>
+__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(NormBackwardParams p) {
+  __shared__ float red[2][32];
+  const int nvec = p.H / 8;
+  const float inv_h = 1.0f / (float)p.H;
+  griddep_wait();
+  float acc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i][q] = 0.f;
+  int par = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
+    uint4 gv[NV], rv[NV], av[NV];
+    const float k = __ldg(p.rstd + t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * blockDim.x + threadIdx.x;
+      gv[i] = rv[i] = av[i] = make_uint4(0, 0, 0, 0);
+      if (v < nvec) {
+        const int64_t at = t * p.H + v * 8;
+        gv[i] = ld_stream_v4(p.gy + at);
+        rv[i] = ld_stream_v4(p.r + at);
+        if (p.gres != nullptr) av[i] = ld_plain_v4(p.gres + at);  // gx may be written over it
+      }
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * blockDim.x + threadIdx.x;
+      if (v < nvec) {
+        float g[8], r[8], w[8];
+        bf16x8_to_f32(gv[i], g);
+        bf16x8_to_f32(rv[i], r);
+        load_gamma(p.gamma, p.gamma_f32, v, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float gx = g[q] * (r[q] * k);
+          acc[i][q] += gx;
+          m = fmaf(gx, w[q], m);
+        }
+      }
+    }
+    m = row_sum<false>(m, red[par]) * inv_h;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * blockDim.x + threadIdx.x;
+      if (v < nvec) {
+        float g[8], r[8], w[8], a[8], o[8];
+        bf16x8_to_f32(gv[i], g);
+        bf16x8_to_f32(rv[i], r);
+        bf16x8_to_f32(av[i], a);
+        load_gamma(p.gamma, p.gamma_f32, v, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] = k * (g[q] * w[q] - r[q] * k * m) + a[q];
+        st_stream_v4(p.gx + t * (int64_t)p.H + v * 8, f32_to_bf16x8(o));
+      }
+    }
+  }
+  if (p.ggamma == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * blockDim.x + threadIdx.x;
+    if (v < nvec) {
+      float4 *o = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.H + v * 8);
+      o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
+}
+
+// out[c] = sum over i < parts of part[i, c], in a fixed order: 8 threads of a
+// column sum every eighth row, then one adds the eight.
+constexpr int kSumCols = 32, kSumSplit = 8;
+__global__ void __launch_bounds__(kSumCols *kSumSplit)
+    column_sum_kernel(const float *part, int parts, int64_t n, float *out) {
+  __shared__ float s[kSumSplit][kSumCols];
+  const int c = threadIdx.x & (kSumCols - 1), k = threadIdx.x / kSumCols;
+  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+  griddep_wait();
+  float v = 0.f;
+  if (col < n)
+    for (int i = k; i < parts; i += kSumSplit) v += part[(int64_t)i * n + col];
+  s[k][c] = v;
+  __syncthreads();
+  if (k == 0 && col < n) {
+    for (int i = 1; i < kSumSplit; ++i) v += s[i][c];
+    out[col] = v;
+  }
+}
+
+int backward_threads(int H) {
+  const int nvec = H / 8;
+  return std::min(kMaxThreads, std::max(32, ((nvec + 3) / 4 + 31) / 32 * 32));
+}
+
+template <int NV>
+cudaError_t launch_backward(const NormBackwardParams &p, int threads, cudaStream_t s) {
+  return launch_pdl(norm_backward_kernel<NV>, (unsigned)p.parts, threads, 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
+                              cudaStream_t s) {
+  return launch_pdl(column_sum_kernel, (unsigned)((n + kSumCols - 1) / kSumCols),
+                    kSumCols * kSumSplit, 0, s, part, parts, n, out);
+}
+
+cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
+  const int nvec = p.H / 8;
+  if (nvec <= 32) return launch_forward<1, true>(p, 128, s);
+  if (nvec <= 128) return launch_forward<4, true>(p, 128, s);
+  const int threads = ((nvec + 3) / 4 + 31) / 32 * 32;
+  return launch_forward<4, false>(p, threads, s);
+}
+
+int norm_backward_parts(const NormBackwardParams &p) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return (int)std::min<int64_t>(p.T, (int64_t)device_sm_count(dev) * 2);
+}
+
+cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s) {
+  const cudaError_t e = launch_backward<4>(p, backward_threads(p.H), s);
+  if (e != cudaSuccess || p.ggamma == nullptr) return e;
+  return launch_column_sum(p.part, p.parts, p.H, p.ggamma, s);
+}
+
+}  // namespace ep

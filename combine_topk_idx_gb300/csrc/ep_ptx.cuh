@@ -23,11 +23,34 @@ __device__ __forceinline__ uint4 ld_cached_v4(const void *p) {
   return r;
 }
 
+// 16-byte load of data that this thread may write later in the same kernel
+// (in-place updates): not the read-only path.
+__device__ __forceinline__ uint4 ld_plain_v4(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// 8-byte read-only streaming load.
+__device__ __forceinline__ uint2 ld_stream_v2(const void *p) {
+  uint2 r;
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
 // 16-byte streaming store (written once, not re-read by this kernel).
 __device__ __forceinline__ void st_stream_v4(void *p, uint4 v) {
   asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
                : "memory");
+}
+
+// 8-byte streaming store.
+__device__ __forceinline__ void st_stream_v2(void *p, uint2 v) {
+  asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Bulk (TMA engine) copy shared::cta -> global, tracked in the issuing thread's bulk group.

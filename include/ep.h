@@ -337,6 +337,137 @@ EP_API ep_status ep_combine_backward(ep_handle *h, const void *grad_combined_x,
  */
 EP_API void ep_handle_free(ep_handle *h);
 
+/* ---- operators around dispatch and combine ------------------------------ */
+
+/*
+ * Rows, scales and padding of the calls below that take a handle: they work on
+ * the rows of its layout (expanded, rank or fixed capacity), whatever
+ * cfg->use_fp8 says.  FP8 rows are e4m3 bytes with one fp32 scale per 1x128
+ * block, quantised as in ep_dispatch; a row of n elements has its scales where
+ * ep_sf_layout says.  Rows past the real total (or past an expert's count, in
+ * the fixed-capacity layout) are neither read nor written.  Alignment padding
+ * rows are not read; outputs there are zeroed when cfg->do_zero_padding, else
+ * left as they are.
+ */
+
+/*
+ * ep_sf_layout -- where the scales of rows of n elements (n a multiple of 128)
+ * lie in the handle's layout: row-major, or column-major with
+ * cfg->use_tma_aligned_col_major_sf, as ep_layout_info says for n = hidden:
+ *   sf[row * token_stride + j * hidden_stride], or with expert_stride > 0
+ *   sf[e * expert_stride + i * token_stride + j * hidden_stride] for row
+ *   e * expert_capacity + i.
+ * numel: fp32 values to allocate.  Host only.
+ */
+EP_API ep_status ep_sf_layout(const ep_handle *h, int32_t n, int64_t *numel,
+                              int64_t *token_stride, int64_t *hidden_stride,
+                              int64_t *expert_stride);
+
+/*
+ * ep_rmsnorm -- root-mean-square norm with the residual's addition.
+ *
+ * Per row: s = x + residual (fp32; s = x without a residual),
+ *   rstd = 1 / sqrt(mean(s^2) + eps), v = s * rstd * gamma, all in fp32.
+ * x, residual: device BF16 [num_tokens, hidden] with row strides (elements,
+ *   multiples of 8, >= hidden), 16-byte aligned; residual may be NULL (its
+ *   stride is then ignored).
+ * gamma: [hidden] BF16, or fp32 with gamma_is_fp32; 16-byte aligned.
+ * Outputs, each NULL or dense and 16-byte aligned (rstd, y_sf: 4), at least one given:
+ *   residual_out BF16 [T, H]: s, rounded; may be `residual` itself if that is dense;
+ *   y BF16 [T, H]: v, rounded;
+ *   y_fp8 e4m3 [T, H] with y_sf: v quantised by 1x128 blocks (hidden a multiple of 128), the
+ *     scale of token t and block j at y_sf[t * y_sf_token_stride + j * y_sf_hidden_stride]
+ *     (strides >= 1), the input of ep_dispatch_fp8;
+ *   rstd fp32 [T]: for ep_rmsnorm_backward.
+ * Otherwise outputs overlap neither each other nor an input.
+ */
+EP_API ep_status ep_rmsnorm(int32_t num_tokens, int32_t hidden, const void *x, int64_t x_stride,
+                            const void *residual, int64_t residual_stride, const void *gamma,
+                            int32_t gamma_is_fp32, float eps, void *residual_out, void *y,
+                            void *y_fp8, float *y_sf, int64_t y_sf_token_stride,
+                            int64_t y_sf_hidden_stride, float *rstd, ep_stream_t stream);
+
+/*
+ * ep_rmsnorm_backward -- gradient of ep_rmsnorm.
+ *
+ * grad_y: BF16 [T, H], gradient of v.  normed: BF16 [T, H], what the forward
+ *   normalised (residual_out, or x).  rstd: fp32 [T] of the forward.
+ * grad_residual: NULL, or BF16 [T, H], the gradient of residual_out from elsewhere.
+ * With xh = normed * rstd, m = mean(grad_y * gamma * xh):
+ *   grad_x = rstd * (grad_y * gamma - xh * m) + grad_residual  (BF16 [T, H]; the
+ *     gradient of x and of residual alike; may be grad_residual itself);
+ *   grad_gamma = sum over rows of grad_y * xh  (fp32 [H], or NULL), summed in a
+ *     fixed order.
+ * Dense, 16-byte aligned (rstd: 4).  Uses a stream-ordered workspace.
+ */
+EP_API ep_status ep_rmsnorm_backward(int32_t num_tokens, int32_t hidden, const void *grad_y,
+                                     const void *normed, const void *gamma, int32_t gamma_is_fp32,
+                                     const float *rstd, const void *grad_residual, void *grad_x,
+                                     float *grad_gamma, ep_stream_t stream);
+
+/*
+ * ep_swiglu -- gated activation between the experts' two products.
+ *
+ * h: the handle whose rows these are, or NULL: `rows` rows, all in use, scales
+ *   row-major.  With a handle `rows` must be its rows_alloc.
+ * gate_up: BF16 [rows, 2 * ffn], gate then up; row_weights: NULL or fp32 [rows].
+ *   a = row_weight * gate * sigmoid(gate) * up, in fp32.
+ * Outputs, each NULL or 16-byte aligned (scales: 4), at least one given:
+ *   act BF16 [rows, ffn]; act_fp8 e4m3 [rows, ffn] with act_sf (ep_sf_layout of
+ *   ffn); ckpt_fp8 e4m3 [rows, 2 * ffn] with ckpt_sf fp32 [rows, 2 * ffn / 128]
+ *   row-major: gate_up itself quantised, kept for ep_swiglu_backward (rows in
+ *   use only: its padding rows are never written).
+ * ffn: a multiple of 128 (of 8 if only `act` is given), at most EP_MAX_HIDDEN.
+ */
+EP_API ep_status ep_swiglu(const ep_handle *h, int64_t rows, int32_t ffn, const void *gate_up,
+                           const float *row_weights, void *act, void *act_fp8, float *act_sf,
+                           void *ckpt_fp8, float *ckpt_sf, ep_stream_t stream);
+
+/*
+ * ep_swiglu_backward -- gradient of ep_swiglu from its 8-bit checkpoint.
+ *
+ * grad_act: BF16 [rows, ffn]; ckpt_fp8, ckpt_sf, row_weights as given to and
+ *   written by the forward; h, rows, ffn as there.
+ * With g, u the checkpoint's values, sg = sigmoid(g), t = row_weight * grad_act:
+ *   gradient of gate = t * u * sg * (1 + g * (1 - sg)), of up = t * g * sg,
+ *   grad_row_weights = sum over ffn of grad_act * g * sg * u.
+ * Outputs, each NULL or 16-byte aligned (fp32: 4), at least one given:
+ *   grad_gate_up BF16 [rows, 2 * ffn]; grad_fp8 e4m3 [rows, 2 * ffn] with grad_sf
+ *   (ep_sf_layout of 2 * ffn); grad_row_weights fp32 [rows] (0 on zeroed padding).
+ */
+EP_API ep_status ep_swiglu_backward(const ep_handle *h, int64_t rows, int32_t ffn,
+                                    const void *grad_act, const void *ckpt_fp8,
+                                    const float *ckpt_sf, const float *row_weights,
+                                    void *grad_gate_up, void *grad_fp8, float *grad_sf,
+                                    float *grad_row_weights, ep_stream_t stream);
+
+/*
+ * ep_combine_weighted_backward -- gradient of ep_combine with topk_weights.
+ *
+ * grad_out: BF16 [T, H].  y: BF16 [rows_alloc, H], topk_weights: fp32 [T, K],
+ *   expert_bias: NULL or BF16 [E, H], as given to ep_combine.  y may be NULL if
+ *   grad_topk_weights is.
+ * Outputs, each NULL or 16-byte aligned (fp32 [T, K] and scales: 4), at least one given:
+ *   grad_y BF16 [rows_alloc, H]: (sum of the weights of the token's slots on the
+ *     row, in slot order) * grad_out of its token;
+ *   grad_y_fp8 e4m3 [rows_alloc, H] with grad_y_sf (ep_sf_layout of hidden, a
+ *     multiple of 128): the same rows in 8 bits -- the bytes are grad_out
+ *     quantised once per token, negated for a negative weight, the scale is the
+ *     token's scale times |weight| (weight 0: zero bytes and scales);
+ *   grad_topk_weights fp32 [T, K]: <grad_out[t], y[row] + expert_bias[e]>, 0 for
+ *     a slot without a row;
+ *   grad_expert_bias fp32 [E, H]: sum over the slots routed to e of weight *
+ *     grad_out, in a fixed order; 0 for an expert without slots.
+ * The gradient of bias_0 and bias_1 is grad_out.  Uses a stream-ordered
+ * workspace if grad_expert_bias is given.
+ */
+EP_API ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out,
+                                              const void *y, const float *topk_weights,
+                                              const void *expert_bias, void *grad_y,
+                                              void *grad_y_fp8, float *grad_y_sf,
+                                              float *grad_topk_weights, float *grad_expert_bias,
+                                              ep_stream_t stream);
+
 /* ---- layout without any allocation ------------------------------------- */
 
 /*
