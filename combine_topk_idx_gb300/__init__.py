@@ -16,6 +16,6 @@ from ._binding import (  # noqa: F401
     ep_dispatch_fp8, alloc_recv_planned, ep_layout_dispatch, plan_layout,
 )
 from ._ops import (  # noqa: F401
-    alloc_fp8, alloc_rmsnorm, ep_combine_weighted_backward, ep_rmsnorm, ep_rmsnorm_backward,
-    ep_swiglu, ep_swiglu_backward, sf_layout,
+    alloc_fp8, alloc_rmsnorm, ep_combine_weighted_backward, ep_expert_gemm, ep_rmsnorm,
+    ep_rmsnorm_backward, ep_swiglu, ep_swiglu_backward, sf_layout,
 )

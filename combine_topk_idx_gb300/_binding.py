@@ -148,6 +148,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_swiglu_backward.restype = ctypes.c_int
     lib.ep_combine_weighted_backward.argtypes = [vp] * 11
     lib.ep_combine_weighted_backward.restype = ctypes.c_int
+    lib.ep_expert_gemm.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.ep_expert_gemm.restype = ctypes.c_int
     if lib.ep_abi_version() != EP_ABI_VERSION:
         raise RuntimeError("libep.so ABI version does not match this binding")
     _lib = lib

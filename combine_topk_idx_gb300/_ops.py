@@ -1,6 +1,6 @@
 """Binding of the operators around dispatch and combine: the norm before the
-dispatch, the gated activation between the experts' products, and the gradient
-of the weighted combine.
+dispatch, the experts' products and the gated activation between them, and the
+gradient of the weighted combine.
 
 Like the rest of the binding this only checks and marshals arguments.  Every
 call is ordered on the current torch stream, or on ``stream=``; a tensor that
@@ -247,3 +247,28 @@ def ep_combine_weighted_backward(handle: Handle, grad_out: torch.Tensor,
                                            (sf_layout(handle, H)[0],)),
       c.ptr(grad_topk_weights, "grad_topk_weights", _F32, (T, K)),
       c.ptr(grad_expert_bias, "grad_expert_bias", _F32, (E, H)))
+
+
+def ep_expert_gemm(handle: Handle, a: torch.Tensor, a_sf: torch.Tensor, w: torch.Tensor,
+                   w_sf: torch.Tensor, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The experts' FP8 product over the handle's expanded rows (``ep_expert_gemm``):
+    ``a`` e4m3 [rows_alloc, k] with flat scales in the handle's layout, ``w`` e4m3
+    [E, n, k] with ``w_sf`` fp32 [E, ceil(n / 128), k / 128]; returns BF16
+    [rows_alloc, n]."""
+    c = _Call("ep_expert_gemm", stream)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, n, k]")
+    E, n, k = w.shape
+    if E != handle.E:
+        raise ValueError(f"w has {E} experts, the handle {handle.E}")
+    if k % 128 or k == 0:
+        raise ValueError(f"k = {k} is not a multiple of 128")
+    rows = handle.rows_alloc
+    if out is None:
+        out = c.empty(rows, n, dtype=_BF16)
+    c(ctypes.c_void_p(handle.ptr), n, k, c.ptr(a, "a", _FP8, (rows, k)),
+      c.ptr(a_sf, "a_sf", _F32, (sf_layout(handle, k)[0],)), c.ptr(w, "w", _FP8),
+      c.ptr(w_sf, "w_sf", _F32, (E, -(-n // 128), k // 128)),
+      c.ptr(out, "out", _BF16, (rows, n)))
+    return out

@@ -236,6 +236,22 @@ struct CombineGradParams {
   int parts;
 };
 
+struct ExpertGemmParams {
+  const uint8_t *a;         // [rows_alloc, K] e4m3
+  const float *sf;          // its scales, sfl
+  SfLayout sfl;
+  const uint8_t *w;         // [E, N, K] e4m3
+  const float *w_sf;        // [E, ceil(N / 128), K / 128]
+  uint16_t *out;            // [rows_alloc, N] bf16
+  int out32;                // every row of out starts on a 32-byte boundary
+  const int32_t *psum_e, *cnt_e;
+  int E, N, K;
+  int fixed_cap, zero_padding;
+  int64_t rows_alloc;
+  int64_t max_slots;        // T * K of the layout
+  unsigned *err;            // the handle's error word (EP_ERRBIT_TIMEOUT)
+};
+
 // Dynamic shared memory above which a kernel must opt in with
 // cudaFuncAttributeMaxDynamicSharedMemorySize: the 48 KB default window less
 // a margin for the kernels' static shared memory (all below 8 KB).
@@ -262,6 +278,8 @@ cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s);
 cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s);
 int combine_grad_parts(const CombineGradParams &p);
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s);
+
+cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream_t s);
 
 // Device facts, cached per device.
 int device_sm_count(int device);

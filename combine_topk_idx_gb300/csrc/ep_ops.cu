@@ -74,6 +74,7 @@ ep_status check_norm(int32_t num_tokens, int32_t hidden) {
 }  // namespace
 }  // namespace ep
 
+using ep::aligned;
 using ep::have;
 using ep::maybe;
 
@@ -302,6 +303,42 @@ ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out,
     if (e == cudaSuccess) e = f;
   }
   return ep::cuda_status(e);
+}
+
+ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const void *a_fp8,
+                         const float *a_sf, const void *w_fp8, const float *w_sf, void *out,
+                         ep_stream_t stream) {
+  if (h == nullptr) return EP_ERR_INVALID_ARG;
+  const ep_config &c = h->cfg;
+  if (n < 8 || n % 8 != 0 || k < ep::kFp8Block || k % ep::kFp8Block != 0)
+    return EP_ERR_INVALID_ARG;
+  if (!c.do_expand || n > EP_MAX_GEMM || k > EP_MAX_GEMM ||
+      (int64_t)c.num_experts * n > 0x7fffffffLL)
+    return EP_ERR_UNSUPPORTED;
+  if (!have(w_fp8, 16) || !have(w_sf, 4)) return EP_ERR_INVALID_ARG;
+  if (const ep_status st = ep::check_device(h); st != EP_OK) return st;
+  if (h->rows_alloc == 0) return EP_OK;
+  if (!have(a_fp8, 16) || !have(a_sf, 4) || !have(out, 16)) return EP_ERR_INVALID_ARG;
+  ep::ExpertGemmParams p{};
+  p.a = static_cast<const uint8_t *>(a_fp8);
+  p.sf = a_sf;
+  p.sfl = ep::sf_layout(h, k);
+  p.w = static_cast<const uint8_t *>(w_fp8);
+  p.w_sf = w_sf;
+  p.out = static_cast<uint16_t *>(out);
+  p.out32 = aligned(out, 32) && n % 16 == 0;
+  p.psum_e = h->lp.psum_e;
+  p.cnt_e = h->lp.cnt_e;
+  p.E = c.num_experts;
+  p.N = n;
+  p.K = k;
+  p.fixed_cap = h->lp.fixed_cap;
+  p.zero_padding = c.do_zero_padding;
+  p.rows_alloc = h->rows_alloc;
+  p.max_slots = (int64_t)c.num_tokens * c.num_topk;
+  p.err = reinterpret_cast<unsigned *>(h->lp.ctrl + ep::kCtrlError);
+  return ep::cuda_status(
+      ep::launch_expert_gemm(p, c.num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

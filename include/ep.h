@@ -468,6 +468,27 @@ EP_API ep_status ep_combine_weighted_backward(const ep_handle *h, const void *gr
                                               float *grad_topk_weights, float *grad_expert_bias,
                                               ep_stream_t stream);
 
+/*
+ * ep_expert_gemm -- the experts' product over the rows of an expanded layout
+ * (do_expand, fixed capacity too; else EP_ERR_UNSUPPORTED).
+ *
+ * a_fp8: e4m3 [rows_alloc, k] with scales a_sf (ep_sf_layout of k), as
+ *   ep_dispatch, ep_swiglu or the backward calls write them.
+ * w_fp8: e4m3 [E, n, k], one matrix per expert; w_sf: fp32
+ *   [E, ceil(n / 128), k / 128], one scale per 128x128 block.
+ * out: BF16 [rows_alloc, n].  For a row of expert e:
+ *   out[r, c] = sum over blocks j of a_sf[r, j] * w_sf[e, c / 128, j] *
+ *               sum over i in block j of a[r, i] * w[e, c, i]
+ *   with fp32 sums, rounded once.  The data gradient is the same call on the
+ *   transposed weights [E, k, n], whose scales are transposed likewise.
+ * k: a multiple of 128; n: a multiple of 8; both at most EP_MAX_GEMM.
+ * 16-byte aligned (scales: 4); out overlaps no input.
+ */
+#define EP_MAX_GEMM 65536
+EP_API ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const void *a_fp8,
+                                const float *a_sf, const void *w_fp8, const float *w_sf,
+                                void *out, ep_stream_t stream);
+
 /* ---- layout without any allocation ------------------------------------- */
 
 /*

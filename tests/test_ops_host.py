@@ -79,3 +79,7 @@ def test_without_a_handle(lib):
     r = ctypes.byref(v)
     assert lib.ep_sf_layout(None, 128, r, r, r, r) == INVALID
     assert lib.ep_combine_weighted_backward(*[None] * 11) == INVALID
+
+
+def test_expert_gemm_without_a_handle(lib):
+    assert lib.ep_expert_gemm(None, 256, 256, P, P, P, P, P, None) == INVALID
