@@ -14,45 +14,49 @@ from typing import Optional
 
 import torch
 
-from ._binding import EP_OK, EpError, Handle, _ptr, load_library
+from ._binding import EP_OK, EpError, Handle, load_library
 
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
-_BF16 = torch.bfloat16
-_F32 = torch.float32
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
 
 
 class _Call:
     """One call's stream, device check and tensor pointers."""
 
+    __slots__ = ("fn", "name", "raw", "other", "device")
+
     def __init__(self, name: str, stream):
         self.name = name
-        self.lib = load_library()
-        current = torch.cuda.current_stream()
-        self.stream = current if stream is None else stream
-        if not hasattr(self.stream, "cuda_stream"):
-            self.stream = torch.cuda.ExternalStream(int(self.stream))
-        self.other = self.stream if self.stream != current else None
-        self.device = current.device_index
+        self.fn = getattr(load_library(), name)
+        self.device = torch.cuda.current_device()
+        # the raw handle: making a torch Stream of the current one takes 2.8 us, most of a launch
+        current = torch._C._cuda_getCurrentRawStream(self.device)
+        self.other = None
+        if stream is None:
+            self.raw = current
+        else:
+            self.raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+            if self.raw != current:
+                self.other = torch.cuda.ExternalStream(self.raw)
 
-    def ptr(self, t: Optional[torch.Tensor], what: str, dtype, shape=None, strided=False):
-        """Pointer of an optional tensor of the expected dtype and shape (None in a shape: any)."""
+    def ptr(self, t: Optional[torch.Tensor], what: str, dtypes: tuple, shape=None, strided=False):
+        """Pointer of an optional tensor of the expected type and shape."""
         if t is None:
             return None
-        if strided:
+        if t.get_device() != self.device:
             if not t.is_cuda:
                 raise ValueError(f"{what} must be a CUDA tensor")
-            if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-                raise ValueError(f"{what} has dtype {t.dtype}, expected {dtype}")
-            p = t.data_ptr() if t.numel() > 0 else None
-        else:
-            p = _ptr(t, what, dtype)
+            raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{self.device}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{what} has dtype {t.dtype}, expected {dtypes}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{what} shape {tuple(t.shape)} != {tuple(shape)}")
-        if t.device.index != self.device:
-            raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{self.device}")
+        if not strided and not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
         if self.other is not None:
             t.record_stream(self.other)
-        return p
+        return t.data_ptr() or None
 
     def empty(self, *shape, dtype):
         """An output tensor of the call's stream."""
@@ -62,7 +66,7 @@ class _Call:
             return torch.empty(shape, dtype=dtype, device="cuda")
 
     def __call__(self, *args):
-        st = getattr(self.lib, self.name)(*args, self.stream.cuda_stream)
+        st = self.fn(*args, self.raw)
         if st != EP_OK:
             raise EpError(st, self.name)
 
@@ -81,7 +85,7 @@ def alloc_fp8(handle: Handle, n: int, zero: bool = False):
     """(e4m3 bytes [rows_alloc, n], flat fp32 scales) in the handle's layout."""
     mk = torch.zeros if zero else torch.empty
     return (mk((handle.rows_alloc, n), dtype=torch.uint8, device="cuda"),
-            mk((sf_layout(handle, n)[0],), dtype=_F32, device="cuda"))
+            mk((sf_layout(handle, n)[0],), dtype=torch.float32, device="cuda"))
 
 
 def alloc_rmsnorm(x: torch.Tensor, residual: bool = False, bf16: bool = False, fp8: bool = True,
@@ -91,17 +95,17 @@ def alloc_rmsnorm(x: torch.Tensor, residual: bool = False, bf16: bool = False, f
     forms are what :func:`ep_dispatch_fp8` takes."""
     T, H = x.shape
     dev = x.device
-    out = {"residual_out": torch.empty((T, H), dtype=_BF16, device=dev) if residual else None,
-           "y": torch.empty((T, H), dtype=_BF16, device=dev) if bf16 else None,
+    out = {"residual_out": torch.empty((T, H), dtype=torch.bfloat16, device=dev) if residual else None,
+           "y": torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
            "y_fp8": None, "y_sf": None,
-           "rstd": torch.empty((T,), dtype=_F32, device=dev) if rstd else None}
+           "rstd": torch.empty((T,), dtype=torch.float32, device=dev) if rstd else None}
     if fp8:
         out["y_fp8"] = torch.empty((T, H), dtype=torch.uint8, device=dev)
         if col_major_sf:
-            sf = torch.empty((H // 128, -(-T // 4) * 4), dtype=_F32, device=dev)
+            sf = torch.empty((H // 128, -(-T // 4) * 4), dtype=torch.float32, device=dev)
             out["y_sf"] = sf[:, :T].t()
         else:
-            out["y_sf"] = torch.empty((T, H // 128), dtype=_F32, device=dev)
+            out["y_sf"] = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
     return out
 
 
@@ -115,7 +119,7 @@ def _row_stride(t: torch.Tensor, what: str) -> int:
 
 
 def _gamma(c: _Call, gamma: torch.Tensor, H: int):
-    return c.ptr(gamma, "gamma", (_BF16, _F32), (H,)), int(gamma.dtype == _F32)
+    return c.ptr(gamma, "gamma", _BF16 + _F32, (H,)), int(gamma.dtype == torch.float32)
 
 
 def ep_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float,
@@ -160,9 +164,9 @@ def ep_rmsnorm_backward(grad_y: torch.Tensor, normed: torch.Tensor, gamma: torch
         raise ValueError("normed must be [T, H]")
     T, H = normed.shape
     if grad_x is None:
-        grad_x = c.empty(T, H, dtype=_BF16)
+        grad_x = c.empty(T, H, dtype=torch.bfloat16)
     if grad_gamma is None and need_gamma:
-        grad_gamma = c.empty(H, dtype=_F32)
+        grad_gamma = c.empty(H, dtype=torch.float32)
     gp, f32 = _gamma(c, gamma, H)
     c(T, H, c.ptr(grad_y, "grad_y", _BF16, normed.shape), c.ptr(normed, "normed", _BF16), gp, f32,
       c.ptr(rstd, "rstd", _F32, (T,)),
@@ -266,7 +270,7 @@ def ep_expert_gemm(handle: Handle, a: torch.Tensor, a_sf: torch.Tensor, w: torch
         raise ValueError(f"k = {k} is not a multiple of 128")
     rows = handle.rows_alloc
     if out is None:
-        out = c.empty(rows, n, dtype=_BF16)
+        out = c.empty(rows, n, dtype=torch.bfloat16)
     c(ctypes.c_void_p(handle.ptr), n, k, c.ptr(a, "a", _FP8, (rows, k)),
       c.ptr(a_sf, "a_sf", _F32, (sf_layout(handle, k)[0],)), c.ptr(w, "w", _FP8),
       c.ptr(w_sf, "w_sf", _F32, (E, -(-n // 128), k // 128)),

@@ -35,12 +35,13 @@ struct Slots {       // a token's slots, one per lane
   int d, e;
   float w;           // weight of the slot
   float ws;          // weight of its row (sum over the slots sharing it, in slot order)
+  int64_t sf;        // where its row's first scale lies (FP8 output)
   unsigned first;    // lanes holding the first slot of their row
   int lead;          // lane of the first slot of this slot's row
 };
 
 __device__ __forceinline__ Slots load_slots(const CombineGradParams &p, int64_t t, int lane) {
-  Slots s{-1, -1, 0.f, 0.f, 0u, 0};
+  Slots s{-1, -1, 0.f, 0.f, 0, 0u, 0};
   if (lane < p.K) {
     s.d = __ldg(p.dst + t * p.K + lane);
     s.w = __ldg(p.topk_w + t * p.K + lane);
@@ -49,115 +50,165 @@ __device__ __forceinline__ Slots load_slots(const CombineGradParams &p, int64_t 
   const unsigned peers = __match_any_sync(0xffffffffu, s.d);
   s.lead = __ffs(peers) - 1;
   s.first = __ballot_sync(0xffffffffu, s.d >= 0 && s.lead == lane);
-  s.ws = 0.f;
-  for (int k = 0; k < p.K; ++k) {
-    const float w = __shfl_sync(0xffffffffu, s.w, k);
-    if ((peers >> k) & 1) s.ws += w;
+  s.ws = s.w;
+  if (!p.do_expand) {  // several slots may share a row
+    s.ws = 0.f;
+    for (int k = 0; k < p.K; ++k) {
+      const float w = __shfl_sync(0xffffffffu, s.w, k);
+      if ((peers >> k) & 1) s.ws += w;
+    }
   }
+  if (p.q != nullptr && s.d >= 0) s.sf = sf_at(p.sfl, s.d, 0);
   return s;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sums of a and of b over the warp: lanes 0..15 get a's, lanes 16..31 b's.
+__device__ __forceinline__ float warp_sum2(float a, float b) {
+  const bool hi = (threadIdx.x & 16) != 0;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 8; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-template <int NV, int MAXT>
+// A thread's share of a row: NV units of U vectors, blockDim.x units apart.
+template <int U, int NV>
+struct Share {
+  uint4 v[NV][U];
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const uint16_t *row, int H, bool any) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * 8 * U;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const uint16_t *a = row + c + 8 * k;
+        v[i][k] = any && c < H ? (STREAM ? ld_stream_v4(a) : ld_cached_v4(a))
+                               : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  // This thread's part of the inner product with another share: each product
+  // of two BF16 values is exact, each sum rounded once.
+  __device__ __forceinline__ float dot(const Share &o) const {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        s = fma2_bf16_f32(v[i][k].x, o.v[i][k].x, s);
+        s = fma2_bf16_f32(v[i][k].y, o.v[i][k].y, s);
+        s = fma2_bf16_f32(v[i][k].z, o.v[i][k].z, s);
+        s = fma2_bf16_f32(v[i][k].w, o.v[i][k].w, s);
+      }
+    return s;
+  }
+};
+
+// The token's gradient as FP8 bytes and scales, a thread's share of them.
+template <int U, int NV>
+struct ShareFp8 {
+  uint32_t b[NV][2 * U];
+  float s[NV];
+};
+
+// Writes w * g to `row` of the outputs; sf0: where the row's scales begin.
+template <int U, int NV>
+__device__ __forceinline__ void write_row(const CombineGradParams &p, const Share<U, NV> &g,
+                                          const ShareFp8<U, NV> &q, int64_t row, float w,
+                                          int64_t sf0) {
+  constexpr int N = 8 * U;
+  const int64_t at = row * p.H;
+  if (p.gy != nullptr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * N;
+      float f[N];
+      bf16_to_f32<U>(g.v[i], f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) f[k] *= w;
+      if (c < p.H) store_bf16<U>(p.gy + at + c, f);
+    }
+  }
+  if (U == 2 && p.q != nullptr) {
+    const uint32_t flip = w < 0.f ? 0x80808080u : 0u;
+    const uint32_t keep = w != 0.f ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * blockDim.x + threadIdx.x;
+      if (v * N < p.H) {
+        uint32_t b[2 * U];
+#pragma unroll
+        for (int k = 0; k < 2 * U; ++k) b[k] = (q.b[i][k] ^ flip) & keep;
+        store_bytes<U>(p.q + at + v * N, b);
+        if ((v & 7) == 0) p.sf[sf0 + (v >> 3) * p.sfl.hs] = fabsf(w) * q.s[i];
+      }
+    }
+  }
+}
+
+// U = 2 where H is a multiple of 16: eight neighbouring lanes then hold a
+// scale block.
+template <int U, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p) {
+  constexpr int N = 8 * U;
   __shared__ float red_y[2][EP_MAX_TOPK][kMaxWarps + 1];
   __shared__ float red_b[2][EP_MAX_TOPK][kMaxWarps + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int nvec = p.H / 8;
   const int64_t H = p.H;
   griddep_wait();
   int par = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
-    uint4 gv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = i * blockDim.x + threadIdx.x;
-      gv[i] = v < nvec ? ld_stream_v4(p.g + t * H + v * 8) : make_uint4(0, 0, 0, 0);
-    }
+    Share<U, NV> g;
+    g.template load<true>(p.g + t * H, p.H, true);
     const Slots s = load_slots(p, t, lane);
-    uint2 gq[NV];
-    float gs[NV];
-    if (p.q != nullptr) {
+    ShareFp8<U, NV> q;
+    if (U == 2 && p.q != nullptr) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float f[8];
-        bf16x8_to_f32(gv[i], f);
-        gq[i] = quantise_block(f, &gs[i]);
+        float f[N];
+        bf16_to_f32<U>(g.v[i], f);
+        quantise_block<N>(f, q.b[i], &q.s[i]);
       }
     }
-    unsigned slots = __ballot_sync(0xffffffffu, s.d >= 0);
-    for (; slots; slots &= slots - 1) {
-      const int k = __ffs(slots) - 1;
-      const int64_t row = __shfl_sync(0xffffffffu, s.d, k);
-      const float w = __shfl_sync(0xffffffffu, s.ws, k);
-      if ((s.first >> k) & 1) {
-        uint4 yv[NV];
-        if (p.gw != nullptr) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int v = i * blockDim.x + threadIdx.x;
-            yv[i] = v < nvec ? ld_stream_v4(p.y + row * H + v * 8) : make_uint4(0, 0, 0, 0);
-          }
-        }
-        if (p.gy != nullptr) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int v = i * blockDim.x + threadIdx.x;
-            float f[8];
-            bf16x8_to_f32(gv[i], f);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) f[q] *= w;
-            if (v < nvec) st_stream_v4(p.gy + row * H + v * 8, f32_to_bf16x8(f));
-          }
-        }
-        if (p.q != nullptr) {
-          const uint32_t flip = w < 0.f ? 0x80808080u : 0u;
-          const uint32_t keep = w != 0.f ? 0xffffffffu : 0u;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int v = i * blockDim.x + threadIdx.x;
-            if (v < nvec) {
-              st_stream_v2(p.q + row * H + v * 8,
-                           make_uint2((gq[i].x ^ flip) & keep, (gq[i].y ^ flip) & keep));
-              if ((v & 15) == 0) p.sf[sf_at(p.sfl, row, v >> 4)] = fabsf(w) * gs[i];
-            }
-          }
-        }
-        if (p.gw != nullptr) {
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            float f[8], y[8];
-            bf16x8_to_f32(gv[i], f);
-            bf16x8_to_f32(yv[i], y);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dot = fmaf(f[q], y[q], dot);
-          }
-          dot = warp_sum(dot);
-          if (lane == 0) red_y[par][k][warp] = dot;
-        }
+    // the token's rows, two at a time
+    for (unsigned m = s.first; m;) {
+      const int k0 = __ffs(m) - 1;
+      m &= m - 1;
+      const bool two = m != 0;
+      const int k1 = two ? __ffs(m) - 1 : k0;
+      m &= m - 1;
+      const int64_t row0 = __shfl_sync(0xffffffffu, s.d, k0);
+      const int64_t row1 = __shfl_sync(0xffffffffu, s.d, k1);
+      Share<U, NV> y0, y1;
+      if (p.gw != nullptr) {
+        y0.template load<true>(p.y + row0 * H, p.H, true);
+        y1.template load<true>(p.y + row1 * H, p.H, two);
       }
-      if (p.gw != nullptr && p.ebias != nullptr) {
-        const int e = __shfl_sync(0xffffffffu, s.e, k);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int v = i * blockDim.x + threadIdx.x;
-          if (v < nvec) {
-            float f[8], b[8];
-            bf16x8_to_f32(gv[i], f);
-            bf16x8_to_f32(ld_cached_v4(p.ebias + e * H + v * 8), b);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dot = fmaf(f[q], b[q], dot);
-          }
-        }
-        dot = warp_sum(dot);
-        if (lane == 0) red_b[par][k][warp] = dot;
+      write_row<U, NV>(p, g, q, row0, __shfl_sync(0xffffffffu, s.ws, k0),
+                       __shfl_sync(0xffffffffu, s.sf, k0));
+      if (two)
+        write_row<U, NV>(p, g, q, row1, __shfl_sync(0xffffffffu, s.ws, k1),
+                         __shfl_sync(0xffffffffu, s.sf, k1));
+      if (p.gw != nullptr) {
+        const float v = warp_sum2(g.dot(y0), g.dot(y1));
+        if (lane == 0) red_y[par][k0][warp] = v;
+        if (lane == 16 && two) red_y[par][k1][warp] = v;
+      }
+    }
+    if (p.gw != nullptr && p.ebias != nullptr) {
+      for (unsigned m = __ballot_sync(0xffffffffu, s.d >= 0); m;) {
+        const int k0 = __ffs(m) - 1;
+        m &= m - 1;
+        const bool two = m != 0;
+        const int k1 = two ? __ffs(m) - 1 : k0;
+        m &= m - 1;
+        Share<U, NV> b0, b1;
+        b0.template load<false>(p.ebias + __shfl_sync(0xffffffffu, s.e, k0) * H, p.H, true);
+        b1.template load<false>(p.ebias + __shfl_sync(0xffffffffu, s.e, k1) * H, p.H, two);
+        const float v = warp_sum2(g.dot(b0), g.dot(b1));
+        if (lane == 0) red_b[par][k0][warp] = v;
+        if (lane == 16 && two) red_b[par][k1][warp] = v;
       }
     }
     if (p.gw != nullptr) {
@@ -179,16 +230,19 @@ __global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p)
   }
   if (!p.zero_padding || (p.gy == nullptr && p.q == nullptr)) return;
   const int npad = __ldg(p.psum_pad + p.E);
-  for (int64_t q = blockIdx.x; q < npad; q += gridDim.x) {
-    const int e = padding_expert(p.psum_pad, p.E, (int)q);
+  for (int64_t i = blockIdx.x; i < npad; i += gridDim.x) {
+    const int e = padding_expert(p.psum_pad, p.E, (int)i);
     const int64_t row =
-        (int64_t)__ldg(p.psum_e + e) + __ldg(p.cnt_e + e) + (q - __ldg(p.psum_pad + e));
+        (int64_t)__ldg(p.psum_e + e) + __ldg(p.cnt_e + e) + (i - __ldg(p.psum_pad + e));
     if (row >= p.rows_alloc) continue;
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-      if (p.gy != nullptr) st_stream_v4(p.gy + row * H + v * 8, make_uint4(0, 0, 0, 0));
-      if (p.q != nullptr) {
-        st_stream_v2(p.q + row * H + v * 8, make_uint2(0, 0));
-        if ((v & 15) == 0) p.sf[sf_at(p.sfl, row, v >> 4)] = 0.f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (p.gy != nullptr)
+      for (int c = threadIdx.x * 8; c < p.H; c += blockDim.x * 8)
+        st_stream_v4(p.gy + row * H + c, zero);
+    if (p.q != nullptr) {
+      for (int c = threadIdx.x * 16; c < p.H; c += blockDim.x * 16) {
+        st_stream_v4(p.q + row * H + c, zero);
+        if (c % kFp8Block == 0) p.sf[sf_at(p.sfl, row, c / kFp8Block)] = 0.f;
       }
     }
   }
@@ -236,9 +290,9 @@ __global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p, int 
 
 int bias_experts(int E) { return std::min(E, kBiasExperts); }
 
-template <int NV, int MAXT>
+template <int U, int NV, int MAXT>
 cudaError_t launch_rows(const CombineGradParams &p, int threads, int sm_cap, cudaStream_t s) {
-  auto kern = combine_grad_kernel<NV, MAXT>;
+  auto kern = combine_grad_kernel<U, NV, MAXT>;
   int dev = 0, per_sm = 0;
   const cudaError_t e =
       launch_geometry(reinterpret_cast<const void *>(kern), threads, 0, &dev, &per_sm);
@@ -265,13 +319,17 @@ int combine_grad_parts(const CombineGradParams &p) {
 }
 
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s) {
-  const int nvec = p.H / 8;
   cudaError_t e = cudaSuccess;
   if (p.T > 0 && (p.gy != nullptr || p.q != nullptr || p.gw != nullptr)) {
-    const int threads = std::max(32, ((nvec + 3) / 4 + 31) / 32 * 32);
-    e = threads <= 256   ? launch_rows<4, 256>(p, threads, sm_cap, s)
-        : threads <= 512 ? launch_rows<4, 512>(p, threads, sm_cap, s)
-                         : launch_rows<4, 1024>(p, threads, sm_cap, s);
+    // 32 elements per thread
+    const int threads = std::max(32, ((p.H + 31) / 32 + 31) / 32 * 32);
+    if (p.H % 16 == 0)
+      e = threads <= 256   ? launch_rows<2, 2, 256>(p, threads, sm_cap, s)
+          : threads <= 512 ? launch_rows<2, 2, 512>(p, threads, sm_cap, s)
+                           : launch_rows<2, 2, 1024>(p, threads, sm_cap, s);
+    else
+      e = threads <= 512 ? launch_rows<1, 4, 512>(p, threads, sm_cap, s)
+                         : launch_rows<1, 4, 1024>(p, threads, sm_cap, s);
   }
   if (e != cudaSuccess || p.gbias == nullptr) return e;
   const int experts = bias_experts(p.E);

@@ -224,7 +224,7 @@ struct CombineGradParams {
   const uint16_t *ebias;    // [E, H] or nullptr
   const int32_t *psum_e, *cnt_e, *psum_pad;
   int T, K, E, H;
-  int zero_padding;
+  int do_expand, zero_padding;
   int64_t rows_alloc;
   uint16_t *gy;             // [rows_alloc, H] bf16, or nullptr
   uint8_t *q;               // [rows_alloc, H] e4m3, or nullptr
@@ -272,7 +272,8 @@ cudaError_t launch_combine_weights(const CombineWeightsParams &p, cudaStream_t s
 cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
                               cudaStream_t s);
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s);
-int norm_backward_parts(const NormBackwardParams &p);
+// Rows of partial sums (CTAs) a backward call will write.
+cudaError_t norm_backward_parts(const NormBackwardParams &p, int *parts);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s);
 cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s);
 cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s);

@@ -49,87 +49,96 @@ __device__ __forceinline__ void load_gamma(const void *gamma, int f32, int v, fl
   }
 }
 
-// NV vectors per thread; WARP_ROW: one warp per row, else one CTA per row.
-template <int NV, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : kMaxThreads)
-    norm_kernel(NormParams p) {
+// A thread holds NV units of U vectors; WARP_ROW: one warp per row, else one
+// CTA per row of at most MAXT threads.  FP8 output needs U = 2: eight
+// neighbouring lanes then hold one scale block.
+template <int U, int NV, bool WARP_ROW, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_kernel(NormParams p) {
+  constexpr int N = 8 * U;
   __shared__ float red[32];
   const int tpr = WARP_ROW ? 32 : blockDim.x;  // threads per row
   const int tid = WARP_ROW ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t t = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
                              : (int64_t)blockIdx.x;
   if (WARP_ROW && t >= p.T) return;
-  const int nvec = p.H / 8;
   const float inv_h = 1.0f / (float)p.H;
   griddep_wait();
-  float f[NV][8];
+  float f[NV][N];
   float ss = 0.f;
-  uint4 xv[NV], rv[NV];
+  uint4 xv[NV][U], rv[NV][U];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * tpr + tid;
-    xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-    if (v < nvec) {
-      xv[i] = ld_stream_v4(p.x + t * p.x_stride + v * 8);
-      // a plain load: the sum may be written over the residual
-      if (p.residual != nullptr) rv[i] = ld_plain_v4(p.residual + t * p.res_stride + v * 8);
+    const int c = (i * tpr + tid) * N;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      xv[i][k] = rv[i][k] = make_uint4(0, 0, 0, 0);
+      if (c < p.H) {
+        xv[i][k] = ld_stream_v4(p.x + t * p.x_stride + c + 8 * k);
+        // a plain load: the sum may be written over the residual
+        if (p.residual != nullptr) rv[i][k] = ld_plain_v4(p.residual + t * p.res_stride + c + 8 * k);
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * tpr + tid;
-    bf16x8_to_f32(xv[i], f[i]);
+    const int c = (i * tpr + tid) * N;
+    bf16_to_f32<U>(xv[i], f[i]);
     if (p.residual != nullptr) {
-      float r[8];
-      bf16x8_to_f32(rv[i], r);
+      float r[N];
+      bf16_to_f32<U>(rv[i], r);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[i][q] += r[q];
+      for (int q = 0; q < N; ++q) f[i][q] += r[q];
     }
-    if (v < nvec && p.res_out != nullptr)
-      st_stream_v4(p.res_out + t * (int64_t)p.H + v * 8, f32_to_bf16x8(f[i]));
-#pragma unroll
+    if (c < p.H && p.res_out != nullptr) store_bf16<U>(p.res_out + t * (int64_t)p.H + c, f[i]);
     // each term over H before the sum: the mean then fits fp32 as long as it
     // does itself, although the sum of squares may not
-    for (int q = 0; q < 8; ++q) ss = fmaf(f[i][q] * inv_h, f[i][q], ss);
+#pragma unroll
+    for (int q = 0; q < N; ++q) ss = fmaf(f[i][q] * inv_h, f[i][q], ss);
   }
   ss = row_sum<WARP_ROW>(ss, red);
   const float k = rsqrtf(ss + p.eps);
   if (tid == 0 && p.rstd != nullptr) p.rstd[t] = k;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * tpr + tid;
-    if (v - (tid & 31) >= nvec) break;  // whole warps only: the scale blocks shuffle
-    const bool valid = v < nvec;
+    const int v = i * tpr + tid, c = v * N;
+    if ((v - (tid & 31)) * N >= p.H) break;  // whole warps only: the scale blocks shuffle
+    const bool valid = c < p.H;
     if (valid) {
-      float g[8];
-      load_gamma(p.gamma, p.gamma_f32, v, g);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[i][q] = f[i][q] * k * g[q];
-      if (p.y != nullptr) st_stream_v4(p.y + t * (int64_t)p.H + v * 8, f32_to_bf16x8(f[i]));
+      for (int j = 0; j < U; ++j) {
+        float g[8];
+        load_gamma(p.gamma, p.gamma_f32, v * U + j, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[i][8 * j + q] = f[i][8 * j + q] * k * g[q];
+      }
+      if (p.y != nullptr) store_bf16<U>(p.y + t * (int64_t)p.H + c, f[i]);
     }
-    if (p.q != nullptr) {
-      float sc;
-      const uint2 b = quantise_block(f[i], &sc);
-      if (valid) {
-        *reinterpret_cast<uint2 *>(p.q + t * (int64_t)p.H + v * 8) = b;
-        if ((v & 15) == 0) p.sf[t * p.sf_ts + (v >> 4) * p.sf_hs] = sc;
+    if constexpr (U == 2) {
+      if (p.q != nullptr) {
+        float sc;
+        uint32_t b[4];
+        quantise_block<N>(f[i], b, &sc);
+        if (valid) {
+          store_bytes<U>(p.q + t * (int64_t)p.H + c, b);
+          if ((v & 7) == 0) p.sf[t * p.sf_ts + (v >> 3) * p.sf_hs] = sc;
+        }
       }
     }
   }
 }
 
-template <int NV, bool WARP_ROW>
+template <int U, int NV, bool WARP_ROW, int MAXT>
 cudaError_t launch_forward(const NormParams &p, int threads, cudaStream_t s) {
   const int rows = WARP_ROW ? threads / 32 : 1;
-  return launch_pdl(norm_kernel<NV, WARP_ROW>, (unsigned)((p.T + (int64_t)rows - 1) / rows),
+  return launch_pdl(norm_kernel<U, NV, WARP_ROW, MAXT>, (unsigned)((p.T + (int64_t)rows - 1) / rows),
                     threads, 0, s, p);
 }
 
 // Persistent CTAs take rows blockIdx.x, + gridDim.x, ...; every thread keeps
 // its columns, so the gradient of gamma is summed in registers and leaves as
 // one row of partial sums per CTA.
-template <int NV>
-__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(NormBackwardParams p) {
+template <int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_backward_kernel(NormBackwardParams p) {
   __shared__ float red[2][32];
   const int nvec = p.H / 8;
   const float inv_h = 1.0f / (float)p.H;
@@ -224,9 +233,10 @@ int backward_threads(int H) {
   return std::min(kMaxThreads, std::max(32, ((nvec + 3) / 4 + 31) / 32 * 32));
 }
 
-template <int NV>
-cudaError_t launch_backward(const NormBackwardParams &p, int threads, cudaStream_t s) {
-  return launch_pdl(norm_backward_kernel<NV>, (unsigned)p.parts, threads, 0, s, p);
+auto backward_kernel(int threads) {
+  return threads <= 256   ? norm_backward_kernel<4, 256>
+         : threads <= 512 ? norm_backward_kernel<4, 512>
+                          : norm_backward_kernel<4, 1024>;
 }
 
 }  // namespace
@@ -238,21 +248,31 @@ cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *ou
 }
 
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
-  const int nvec = p.H / 8;
-  if (nvec <= 32) return launch_forward<1, true>(p, 128, s);
-  if (nvec <= 128) return launch_forward<4, true>(p, 128, s);
-  const int threads = ((nvec + 3) / 4 + 31) / 32 * 32;
-  return launch_forward<4, false>(p, threads, s);
+  // 32 elements per thread; rows of up to 1024 elements take a warp each
+  const int threads = ((p.H + 31) / 32 + 31) / 32 * 32;
+  if (p.H % 16 == 0) {
+    if (p.H <= 512) return launch_forward<2, 1, true, 128>(p, 128, s);
+    if (p.H <= 1024) return launch_forward<2, 2, true, 128>(p, 128, s);
+    return threads <= 256 ? launch_forward<2, 2, false, 256>(p, threads, s)
+                          : launch_forward<2, 2, false, 1024>(p, threads, s);
+  }
+  if (p.H <= 1024) return launch_forward<1, 4, true, 128>(p, 128, s);
+  return launch_forward<1, 4, false, 1024>(p, threads, s);
 }
 
-int norm_backward_parts(const NormBackwardParams &p) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return (int)std::min<int64_t>(p.T, (int64_t)device_sm_count(dev) * 2);
+cudaError_t norm_backward_parts(const NormBackwardParams &p, int *parts) {
+  const int threads = backward_threads(p.H);
+  int dev = 0, per_sm = 0;
+  const cudaError_t e = launch_geometry(reinterpret_cast<const void *>(backward_kernel(threads)),
+                                        threads, 0, &dev, &per_sm);
+  if (e != cudaSuccess) return e;
+  *parts = (int)std::min<int64_t>(p.T, (int64_t)device_sm_count(dev) * std::max(per_sm, 1));
+  return cudaSuccess;
 }
 
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s) {
-  const cudaError_t e = launch_backward<4>(p, backward_threads(p.H), s);
+  const int threads = backward_threads(p.H);
+  const cudaError_t e = launch_pdl(backward_kernel(threads), (unsigned)p.parts, threads, 0, s, p);
   if (e != cudaSuccess || p.ggamma == nullptr) return e;
   return launch_column_sum(p.part, p.parts, p.H, p.ggamma, s);
 }

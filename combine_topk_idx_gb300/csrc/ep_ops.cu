@@ -163,10 +163,9 @@ ep_status ep_rmsnorm_backward(int32_t num_tokens, int32_t hidden, const void *gr
   p.H = hidden;
   p.gx = static_cast<uint16_t *>(grad_x);
   p.ggamma = grad_gamma;
-  p.parts = ep::norm_backward_parts(p);
-  if (p.parts < 1) return EP_ERR_CUDA;
   void *ws = nullptr;
-  cudaError_t e = cudaSuccess;
+  cudaError_t e = ep::norm_backward_parts(p, &p.parts);
+  if (e != cudaSuccess) return ep::cuda_status(e);
   if (grad_gamma != nullptr) {
     e = ep::workspace_alloc(sizeof(float) * (size_t)p.parts * hidden, s, &ws);
     if (e != cudaSuccess) return ep::cuda_status(e);
@@ -275,6 +274,7 @@ ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out,
   p.K = c.num_topk;
   p.E = c.num_experts;
   p.H = c.hidden;
+  p.do_expand = c.do_expand;
   p.zero_padding = c.do_expand && c.do_zero_padding;
   p.rows_alloc = h->rows_alloc;
   if (h->rows_alloc > 0) {

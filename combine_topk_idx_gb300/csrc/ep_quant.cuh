@@ -71,21 +71,70 @@ __device__ __forceinline__ void e4m3x8_to_f32(const uint2 &v, float *f) {
   }
 }
 
-// Quantises a 1x128 block held by 16 consecutive lanes, eight fp32 values
-// each: scale = amax / 448 (fp32 division), bytes = e4m3(value / scale).
-// Every lane of the warp calls it.  An all-zero block has scale 0 and zero
-// bytes; a block holding a NaN a NaN scale and the NaN code in every byte.
-__device__ __forceinline__ uint2 quantise_block(const float *f, float *scale) {
-  float amax = 0.f;
+// Largest magnitude of N values; NaN if any is one.
+template <int N>
+__device__ __forceinline__ float amax_of(const float *f) {
+  float m = 0.f;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) amax = fmax_nan(amax, fabsf(f[q]));
+  for (int q = 0; q < N; q += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f[q]), "f"(f[q + 1]));
+  return m;
+}
+
+// Quantises a 1x128 block held by 128 / N consecutive lanes, N = 8 or 16 fp32
+// values each: scale = amax / 448, bytes = e4m3(value * (1 / scale)) in fp32,
+// to nearest even, saturating.  The inputs are fp32 results with errors of
+// their own, so unlike the dispatch, whose BF16 inputs meet exact ties, a
+// product by the reciprocal (2 ulp) serves instead of the division.  Every
+// lane of the warp calls it.  An all-zero block, or one whose scale rounds to
+// 0, has scale 0 and zero bytes; a block holding a NaN a NaN scale and the NaN
+// code in every byte; one holding an infinity scale +inf, zeros for its finite
+// values and the NaN code for the infinite ones.
+template <int N>
+__device__ __forceinline__ void quantise_block(const float *f, uint32_t *bytes, float *scale) {
+  float amax = amax_of<N>(f);
 #pragma unroll
-  for (int o = 1; o < 16; o *= 2) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float sc = __fdiv_rn(amax, 448.0f);
+  for (int o = 1; o < 128 / N; o *= 2)
+    amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float sc = amax * (1.0f / 448.0f);
   *scale = sc;
-  if (amax != amax) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  // a block so small that its scale rounds to 0 counts as zero
-  return sc != 0.f ? e4m3_block8(f, sc) : make_uint2(0, 0);
+  if (amax < 0x1p-100f) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint2 b = sc != 0.f ? e4m3_block8(f + 8 * i, sc) : make_uint2(0, 0);
+      bytes[2 * i] = b.x;
+      bytes[2 * i + 1] = b.y;
+    }
+    return;
+  }
+  const float r = rcp_approx(sc);  // sc in [2^-109, 2^120), infinite or NaN
+  const uint64_t r2 = f32x2_pack(r, r);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint64_t v = f32x2_mul_rn(f32x2_pack(f[4 * i], f[4 * i + 1]), r2);
+    const uint64_t w = f32x2_mul_rn(f32x2_pack(f[4 * i + 2], f[4 * i + 3]), r2);
+    bytes[i] = cvt_e4m3x4(f32x2_lo(v), f32x2_hi(v), f32x2_lo(w), f32x2_hi(w));
+  }
+}
+
+// A thread's U vectors of eight BF16 values, and U * 8 e4m3 bytes.
+template <int U>
+__device__ __forceinline__ void bf16_to_f32(const uint4 *v, float *f) {
+#pragma unroll
+  for (int i = 0; i < U; ++i) bf16x8_to_f32(v[i], f + 8 * i);
+}
+template <int U>
+__device__ __forceinline__ void store_bf16(void *p, const float *f) {
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    st_stream_v4(static_cast<uint8_t *>(p) + 16 * i, f32_to_bf16x8(f + 8 * i));
+}
+template <int U>
+__device__ __forceinline__ void store_bytes(void *p, const uint32_t *b) {
+  if constexpr (U == 2)
+    st_stream_v4(p, make_uint4(b[0], b[1], b[2], b[3]));
+  else
+    st_stream_v2(p, make_uint2(b[0], b[1]));
 }
 
 }  // namespace ep
