@@ -4,17 +4,21 @@
 // for the rows r of expert e; a and w are e4m3, a scaled by 1x128 blocks, w by
 // 128x128 blocks.
 //
-// One persistent CTA per SM takes output tiles of kTileM rows x kTileN
-// columns of one expert, found on the device from the layout's counts.  Warp 0
-// copies the operands (tiled TMA, 128-byte swizzle) into a ring of stages of
-// one 128-element block each; one thread of warp 1 issues the tcgen05 products
-// of a block into one of two TMEM accumulators; the epilogue warps (4..11)
-// read a finished block's accumulator and add it, times its scales, to fp32
-// sums in registers (a thread holds one row and 128 columns), while the next
-// block is multiplied into the other accumulator.  Each block's sum has its
-// own scales, so it cannot stay in TMEM: per block the tensor cores need
-// kTileN * 2 cycles (8192 multiply-adds a cycle), reading the accumulator half
-// of that and its multiply-adds as much again, on other units.
+// One persistent CTA per SM takes tiles of up to kTileR rows and kTileC columns
+// of one expert, found on the device from the layout's counts.  The rows are the
+// tensor cores' M operand, the weights their N operand.
+//   warp 0       copies the operands, a 128-element block per stage, into a
+//                ring of stages (tiled TMA, 128-byte swizzle)
+//   warp 1       issues the products of a block into one of two TMEM
+//                accumulators of kTileC columns
+//   warps 4..11  four for each half of the columns: read a finished accumulator
+//                and add it, times the scales of its rows and of its weights,
+//                to fp32 sums in registers (a thread holds one row and 128
+//                columns) while the next block is multiplied
+// Each block's sum has its own scales, so it cannot stay in TMEM.  With the
+// rows in TMEM lanes a block's scale is one register per thread; with the
+// columns there it would be one per accumulator column, and fetching those from
+// shared memory takes longer than the products.
 //
 // Every mbarrier wait is bounded: one that gives up sets EP_ERRBIT_TIMEOUT in
 // the handle's error word, and the CTA waits (bounded) for what it has in
@@ -29,25 +33,38 @@
 namespace ep {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
+constexpr int kTileR = 128, kTileC = 256, kBlockK = 128;
+constexpr int kRowStep = 16;              // a tile's rows are rounded up to this
+constexpr int kRowMaps = 4;               // TMA boxes of 16, 32, 64 and 128 rows
 constexpr int kStages = 4;
-constexpr int kABytes = kTileM * kBlockK, kBBytes = kTileN * kBlockK;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kABytes = kTileR * kBlockK;
+constexpr int kStageBytes = kABytes + kTileC * kBlockK;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kTmemColumns = 512;         // two accumulators of kTileN columns
-// registers of a control and of an epilogue thread: 128 * 88 + 256 * 208 are
+constexpr int kTmemColumns = 2 * kTileC;  // two accumulators
+constexpr int kWarpC = kTileC / 2;        // columns of an epilogue warp
+constexpr int kChunk = 64;                // accumulator columns per TMEM load
+constexpr int kGroup = 2;                 // blocks whose scales are loaded together
+constexpr int kSlice = 32;                // columns of out staged at a time: 64 bytes a row
+// registers of a control and of an epilogue thread: 128 * 40 + 256 * 232 are
 // the 168 * 384 of the launch
-constexpr int kControlRegs = 88, kEpilogueRegs = 208;
+constexpr int kControlRegs = 40, kEpilogueRegs = 232;
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
 
 struct Tile {
-  int e;             // expert
-  int64_t row0;      // first row
+  int e;               // expert
+  int64_t row0;        // first row
   int rows, out_rows;  // rows in use from row0, and rows to write (then zeros)
-  int n0;            // first column
+  int height;          // rows multiplied: out_rows up to a multiple of kRowStep
+  int c0;              // first column
 };
+
+// Height of the row tiles of an expert with n rows to write: all about the same.
+__device__ __forceinline__ int tile_height(int n) {
+  const int m = max(1, (n + kTileR - 1) / kTileR);
+  return max(1, ((n + m - 1) / m + kRowStep - 1) / kRowStep) * kRowStep;
+}
 
 // Rows of expert e: first, in use, and to write (alignment padding zeroed).
 __device__ __forceinline__ void expert_rows(const ExpertGemmParams &p, int e, int64_t *first,
@@ -76,7 +93,8 @@ __device__ __forceinline__ void count_tiles(const ExpertGemmParams &p, int *cum,
       int64_t first;
       int used, write;
       expert_rows(p, e, &first, &used, &write);
-      m = (write + kTileM - 1) / kTileM;
+      const int th = tile_height(write);
+      m = (write + th - 1) / th;
     }
     int v = m;
 #pragma unroll
@@ -102,36 +120,65 @@ __device__ __forceinline__ void count_tiles(const ExpertGemmParams &p, int *cum,
 // Tile i of the experts' tiles: row tiles first, so that the CTAs at work
 // share a weight tile through L2.
 __device__ __forceinline__ Tile find_tile(const ExpertGemmParams &p, const int *cum, int64_t i,
-                                          int tiles_n) {
-  int lo = 0, hi = p.E - 1;  // the last expert with cum[e] * tiles_n <= i
+                                          int tiles_c) {
+  int lo = 0, hi = p.E - 1;  // the last expert with cum[e] * tiles_c <= i
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)cum[mid] * tiles_n <= i) lo = mid; else hi = mid - 1;
+    if ((int64_t)cum[mid] * tiles_c <= i) lo = mid; else hi = mid - 1;
   }
-  const int tm = cum[lo + 1] - cum[lo];
-  const int k = (int)(i - (int64_t)cum[lo] * tiles_n);
-  const int n = k / tm, m = k - n * tm;
+  const int tr = cum[lo + 1] - cum[lo];
+  const int k = (int)(i - (int64_t)cum[lo] * tiles_c);
+  const int c = k / tr, r = k - c * tr;
   Tile t;
   int used, write;
   int64_t first;
   expert_rows(p, lo, &first, &used, &write);
+  const int th = tile_height(write);
   t.e = lo;
-  t.row0 = first + (int64_t)m * kTileM;
-  t.rows = max(0, min(kTileM, used - m * kTileM));
-  t.out_rows = min(kTileM, write - m * kTileM);
-  t.n0 = n * kTileN;
+  t.row0 = first + (int64_t)r * th;
+  t.rows = max(0, min(th, used - r * th));
+  t.out_rows = min(th, write - r * th);
+  t.height = (t.out_rows + kRowStep - 1) / kRowStep * kRowStep;
+  t.c0 = c * kTileC;
   return t;
 }
 
 struct __align__(8) Barriers {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kStages];   // a stage's copies landed
+  uint64_t empty[kStages];  // the products that read a stage are done
+  uint64_t acc_full[2];     // an accumulator is complete
+  uint64_t acc_empty[2];    // an accumulator is read
+  uint64_t drain;
+};
+
+struct Maps {
+  CUtensorMap a[kRowMaps], w;
+};
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t phase) {
+  return mbar_wait_bounded(bar, phase, kWaitIters, kWaitHintNs);
+}
+
+// Position in a ring of N slots: slot and the parity of the current round.  A
+// consumer waits for `phase`, a producer for the round before (`phase ^ 1`,
+// which a fresh barrier passes at once).
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_b, ExpertGemmParams p) {
+    expert_gemm_kernel(const __grid_constant__ Maps maps, ExpertGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
+  __shared__ uint4 slices[kEpilogueWarps][32 * kSlice / 8];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[kThreads / 32];
   // stages on 1024-byte boundaries (the swizzle's period), then cum[E + 1]
@@ -150,151 +197,191 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar.drain, 1);
     fence_mbar_init();
-    tma_prefetch_map(&map_a);
-    tma_prefetch_map(&map_b);
+    for (int i = 0; i < kRowMaps; ++i) tma_prefetch_map(&maps.a[i]);
+    tma_prefetch_map(&maps.w);
   }
-  if (warp == 1) {
-    tmem_alloc(&tmem_slot, kTmemColumns);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc(&tmem_slot, kTmemColumns);
   griddep_wait();
   count_tiles(p, cum, warp_sum);  // ends with a barrier
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int tiles_n = (p.N + kTileN - 1) / kTileN;
-  const int64_t tiles = (int64_t)cum[p.E] * tiles_n;
+  const int tiles_c = (p.N + kTileC - 1) / kTileC;
+  const int64_t tiles = (int64_t)cum[p.E] * tiles_c;
   const int nk = p.K / kBlockK;
 
   if (warp < 4) {
     setmaxnreg_dec<kControlRegs>();
     if (warp == 0 && lane == 0) {
       // ---------------- copies ----------------
-      int64_t it = 0;
+      Ring<kStages> st;
+      int issued = 0;  // stages filled, counted up to kStages
       bool ok = true;
       for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-        const Tile t = find_tile(p, cum, i, tiles_n);
+        const Tile t = find_tile(p, cum, i, tiles_c);
         if (t.rows == 0) continue;  // padding only: nothing to multiply
-        const int b_row = t.e * p.N + t.n0;
-        for (int k = 0; k < nk; ++k, ++it) {
-          const int s = (int)(it % kStages);
-          if (it >= kStages &&
-              !mbar_wait_bounded(&bar.empty[s], (uint32_t)((it / kStages - 1) & 1), kWaitIters,
-                                 kWaitHintNs)) {
+        const uint32_t bytes = (uint32_t)((t.height + kTileC) * kBlockK);
+        const int w_row = t.e * p.N + t.c0;
+        for (int k = 0; k < nk; ++k) {
+          if (!wait(&bar.empty[st.slot], st.phase ^ 1)) {
             ok = false;
             break;
           }
-          uint8_t *a = smem + s * kStageBytes;
-          mbar_arrive_expect_tx(&bar.full[s], kStageBytes);
-          tma_load_2d(a, &map_a, k * kBlockK, (int)t.row0, &bar.full[s]);
-          tma_load_2d(a + kABytes, &map_b, k * kBlockK, b_row, &bar.full[s]);
+          uint8_t *a = smem + st.slot * kStageBytes;
+          uint64_t *const full = &bar.full[st.slot];
+          mbar_arrive_expect_tx(full, bytes);
+          tma_load_2d(a + kABytes, &maps.w, k * kBlockK, w_row, full);
+          int r = 0;
+#pragma unroll
+          for (int b = kRowMaps - 1; b >= 0; --b)  // height = 16 * (sum of 2^b)
+            if (t.height & (kRowStep << b)) {
+              tma_load_2d(a + r * kBlockK, &maps.a[b], k * kBlockK, (int)t.row0 + r, full);
+              r += kRowStep << b;
+            }
+          st.next();
+          if (issued < kStages) ++issued;
         }
       }
       if (!ok) {
         atomicOr(p.err, EP_ERRBIT_TIMEOUT);
-        for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)  // copies in flight
-          mbar_wait_bounded(&bar.full[j % kStages], (uint32_t)((j / kStages) & 1), kWaitIters,
-                            kWaitHintNs);
+        // copies in flight: slots below st.slot in this round, the others in
+        // the round before
+        for (int s = 0; s < kStages; ++s)
+          if (s < st.slot || issued == kStages)
+            wait(&bar.full[s], s < st.slot ? st.phase : st.phase ^ 1);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------- products ----------------
-      constexpr uint32_t idesc = idesc_e4m3(kTileM, kTileN);
-      int64_t it = 0;
+      // the lanes poll the two barriers of a block side by side
+      constexpr uint32_t idesc = idesc_e4m3(kTileR, kTileC);
+      Ring<kStages> st;
+      Ring<2> acc;
+      const uint32_t smem0 = smem_u32(smem);
       bool ok = true;
       for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-        if (find_tile(p, cum, i, tiles_n).rows == 0) continue;
-        for (int k = 0; k < nk; ++k, ++it) {
-          const int s = (int)(it % kStages), b = (int)(it & 1);
-          if ((it >= 2 && !mbar_wait_bounded(&bar.acc_empty[b], (uint32_t)((it / 2 - 1) & 1),
-                                             kWaitIters, kWaitHintNs)) ||
-              !mbar_wait_bounded(&bar.full[s], (uint32_t)((it / kStages) & 1), kWaitIters,
-                                 kWaitHintNs)) {
-            ok = false;
-            break;
-          }
+        if (find_tile(p, cum, i, tiles_c).rows == 0) continue;
+        for (int k = 0; k < nk; ++k) {
+          uint64_t *b = lane & 1 ? &bar.acc_empty[acc.slot] : &bar.full[st.slot];
+          ok = __all_sync(0xffffffffu, wait(b, lane & 1 ? acc.phase ^ 1 : st.phase));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * kStageBytes);
-          const uint64_t da = smem_desc_k128(a), db = smem_desc_k128(a + kABytes);
+          const uint64_t da = smem_desc_k128(smem0 + st.slot * kStageBytes);
+          const uint64_t dw = smem_desc_k128(smem0 + st.slot * kStageBytes + kABytes);
+          if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < kBlockK / 32; ++q)
-            mma_fp8(tmem + b * kTileN, da + q * 2, db + q * 2, idesc, q > 0);
-          mma_commit(&bar.empty[s]);
-          mma_commit(&bar.acc_full[b]);
+            for (int q = 0; q < kBlockK / 32; ++q)
+              mma_fp8(tmem + acc.slot * kTileC, da + q * 2, dw + q * 2, idesc, q > 0);
+            mma_commit(&bar.acc_full[acc.slot]);
+            mma_commit(&bar.empty[st.slot]);
+          }
+          __syncwarp();
+          acc.next();
+          st.next();
         }
       }
       if (!ok) {
-        atomicOr(p.err, EP_ERRBIT_TIMEOUT);
-        mma_commit(&bar.drain);
-        mbar_wait_bounded(&bar.drain, 0, kWaitIters, kWaitHintNs);
+        if (elect_one()) {
+          atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+          mma_commit(&bar.drain);
+        }
+        __syncwarp();
+        wait(&bar.drain, 0);
       }
     }
   } else {
     // ---------------- scaled sums and output ----------------
     setmaxnreg_inc<kEpilogueRegs>();
     const int quarter = warp & 3;           // TMEM lanes of this warp
-    const int half = (warp - 4) >> 2;       // columns half * 128 ..
-    const int m = quarter * 32 + lane;
-    const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u + half * 128;
-    const int nb = (p.N + 127) / 128;
-    int64_t it = 0;
+    const int j = (warp - 4) >> 2;          // quarter of the columns
+    const int m = quarter * 32 + lane;      // row of the tile
+    const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u + j * kWarpC;
+    const int nc = (p.N + 127) / 128;
+    Ring<2> acc;
+    // After a wait that gave up, the rest of the tile is walked without waiting.
     bool ok = true;
     for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-      const Tile t = find_tile(p, cum, i, tiles_n);
-      const int64_t row = t.row0 + m;
-      const int col = t.n0 + half * 128;
-      float acc[128];
+      const Tile t = find_tile(p, cum, i, tiles_c);
+      const bool mine = m < t.rows;
+      const bool work = quarter * 32 < t.out_rows;  // any row of the warp
+      const int blocks = t.rows > 0 ? nk : 0;
+      const float *sa = p.sf + (mine ? sf_at(p.sfl, t.row0 + m, 0) : 0);
+      const float *sw =
+          p.w_sf + ((int64_t)t.e * nc + min(t.c0 / 128 + j, nc - 1)) * nk;
+      uint64_t sum[kWarpC / 2];             // pairs of columns
 #pragma unroll
-      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      if (t.rows > 0) {
-        const bool mine = m < t.rows;
-        const float *sa = p.sf + (mine ? sf_at(p.sfl, row, 0) : 0);
-        const float *sb =
-            p.w_sf + ((int64_t)t.e * nb + min(col / 128, nb - 1)) * nk;
-        float a_next = mine ? __ldg(sa) : 0.f, b_next = __ldg(sb);
-        for (int k = 0; k < nk; ++k, ++it) {
-          const float scale = a_next * b_next;
-          if (k + 1 < nk) {
-            a_next = mine ? __ldg(sa + (int64_t)(k + 1) * p.sfl.hs) : 0.f;
-            b_next = __ldg(sb + k + 1);
-          }
-          const int b = (int)(it & 1);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar.acc_full[b], (uint32_t)((it / 2) & 1),
-                                                         kWaitIters, kWaitHintNs));
-          if (!ok) break;
-          tc_fence_after();
-          float d[2][16];
-          tmem_load16(taddr + b * kTileN, d[0]);
+      for (int c = 0; c < kWarpC / 2; ++c) sum[c] = 0;
+      // scales of the next kGroup blocks, loaded together a group ahead
+      float na[kGroup], nw[kGroup];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_load_wait16(d[c & 1]);
-            if (c < 7) {
-              tmem_load16(taddr + b * kTileN + (c + 1) * 16, d[(c + 1) & 1]);
-            } else {  // the accumulator is read: the next block may overwrite it
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bar.acc_empty[b]);
+      for (int u = 0; u < kGroup; ++u) {
+        na[u] = mine && u < blocks ? __ldg(sa + u * p.sfl.hs) : 0.f;
+        nw[u] = u < blocks ? __ldg(sw + u) : 0.f;
+      }
+      for (int k0 = 0; k0 < blocks; k0 += kGroup) {
+        float s[kGroup];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) s[u] = na[u] * nw[u];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+          const int k = k0 + kGroup + u;
+          na[u] = mine && k < blocks ? __ldg(sa + k * p.sfl.hs) : 0.f;
+          nw[u] = k < blocks ? __ldg(sw + k) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+          if (k0 + u < blocks) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
+            tc_fence_after();
+            const uint32_t ta = taddr + acc.slot * kTileC;
+            if (work) {
+              const uint64_t s2 = f32x2_pack(s[u], s[u]);
+#pragma unroll
+              for (int c = 0; c < kWarpC / kChunk; ++c) {
+                uint32_t d[kChunk];
+                tmem_load64(ta + c * kChunk, d);
+                tmem_load_wait64(d);
+                if (c + 1 == kWarpC / kChunk) {  // read: a later block may overwrite it
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&bar.acc_empty[acc.slot]);
+                }
+#pragma unroll
+                for (int q = 0; q < kChunk / 2; ++q)
+                  sum[c * kChunk / 2 + q] = f32x2_fma_rn(
+                      f32x2_pack(__uint_as_float(d[2 * q]), __uint_as_float(d[2 * q + 1])), s2,
+                      sum[c * kChunk / 2 + q]);
+              }
+            } else if (lane == 0) {
+              mbar_arrive(&bar.acc_empty[acc.slot]);
             }
-#pragma unroll
-            for (int q = 0; q < 16; ++q) acc[c * 16 + q] = fmaf(d[c & 1][q], scale, acc[c * 16 + q]);
+            acc.next();
           }
         }
       }
-      if (ok && m < t.out_rows) {
-        const bool in = m < t.rows;
-        uint16_t *o = p.out + row * p.N + col;
+      if (!ok || !work) continue;
+      // out: 64 bytes of each row at a time through shared memory, so that a
+      // store covers eight rows with four lanes each instead of 32 rows
+      uint4 *const slice = slices[warp - 4];
+      const int row_r = lane >> 2, row_c = lane & 3;  // as stored: row, 16 bytes of it
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          uint32_t v[8];
+      for (int c0 = 0; c0 < kWarpC; c0 += kSlice) {
+        __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            v[q] = in ? cvt_bf16x2(acc[c + 2 * q], acc[c + 2 * q + 1]) : 0u;
-          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]);
-          const uint4 hi = make_uint4(v[4], v[5], v[6], v[7]);
-          if (p.out32 && col + c + 16 <= p.N) {
-            st_stream_v8(o + c, lo, hi);
-          } else {
-            if (col + c + 8 <= p.N) st_stream_v4(o + c, lo);
-            if (col + c + 16 <= p.N) st_stream_v4(o + c + 8, hi);
+        for (int h = 0; h < kSlice / 8; ++h) {
+          uint32_t v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t x = sum[c0 / 2 + 4 * h + q];
+            v[q] = mine ? cvt_bf16x2(f32x2_lo(x), f32x2_hi(x)) : 0u;
           }
+          slice[lane * 4 + (h ^ (lane >> 1 & 3))] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        __syncwarp();
+        const int col = t.c0 + j * kWarpC + c0 + row_c * 8;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int l = h * 8 + row_r, r = quarter * 32 + l;
+          if (r < t.out_rows && col < p.N)
+            st_stream_v4(p.out + (t.row0 + r) * p.N + col, slice[l * 4 + (row_c ^ (l >> 1 & 3))]);
         }
       }
     }
@@ -340,22 +427,23 @@ bool make_map(CUtensorMap *map, const void *base, int64_t rows, int K, int box_r
 }  // namespace
 
 cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream_t s) {
-  CUtensorMap map_a, map_b;
-  if (!make_map(&map_a, p.a, p.rows_alloc, p.K, kTileM) ||
-      !make_map(&map_b, p.w, (int64_t)p.E * p.N, p.K, kTileN))
-    return cudaErrorInvalidValue;
+  Maps maps;
+  bool ok = make_map(&maps.w, p.w, (int64_t)p.E * p.N, p.K, kTileC);
+  for (int i = 0; i < kRowMaps; ++i)
+    ok = ok && make_map(&maps.a[i], p.a, p.rows_alloc, p.K, kRowStep << i);
+  if (!ok) return cudaErrorInvalidValue;
   const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(int) * (p.E + 1);
-  const void *func = reinterpret_cast<const void *>(expert_gemm_kernel);
   int dev = 0;
-  const cudaError_t e = launch_geometry(func, kThreads, smem, &dev, nullptr);
+  const cudaError_t e = launch_geometry(reinterpret_cast<const void *>(expert_gemm_kernel),
+                                        kThreads, smem, &dev, nullptr);
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count(dev);
   const int use = (sm_cap > 0 && sm_cap < sms) ? sm_cap : sms;
   // at most this many row tiles hold rows (every expert's last one may be partial)
-  const int64_t tiles_m = std::min<int64_t>(p.max_slots, p.E) + p.rows_alloc / kTileM;
-  const int64_t tiles = tiles_m * ((p.N + kTileN - 1) / kTileN);
-  return launch_pdl(expert_gemm_kernel, (unsigned)std::min<int64_t>(use, std::max<int64_t>(tiles, 1)),
-                    kThreads, smem, s, map_a, map_b, p);
+  const int64_t tiles_r = std::min<int64_t>(p.max_slots, p.E) + 2 * (p.rows_alloc / kTileR);
+  const int64_t tiles = std::max<int64_t>(1, tiles_r * ((p.N + kTileC - 1) / kTileC));
+  return launch_pdl(expert_gemm_kernel, (unsigned)std::min<int64_t>(use, tiles), kThreads, smem, s,
+                    maps, p);
 }
 
 }  // namespace ep

@@ -243,7 +243,6 @@ struct ExpertGemmParams {
   const uint8_t *w;         // [E, N, K] e4m3
   const float *w_sf;        // [E, ceil(N / 128), K / 128]
   uint16_t *out;            // [rows_alloc, N] bf16
-  int out32;                // every row of out starts on a 32-byte boundary
   const int32_t *psum_e, *cnt_e;
   int E, N, K;
   int fixed_cap, zero_padding;

@@ -1,5 +1,5 @@
-// Inline-PTX wrappers of the 5th-generation tensor cores and their operands'
-// copies (sm_103a): TMEM, tcgen05.mma, tiled TMA loads.
+// Inline-PTX wrappers of the 5th-generation tensor cores and of their operands'
+// copies (sm_103a).
 #pragma once
 
 #include <cuda.h>
@@ -9,39 +9,45 @@
 
 namespace ep {
 
-// ---- TMEM ----
-__device__ __forceinline__ void tmem_alloc(uint32_t *smem_dst, uint32_t columns) {  // one warp
+// ---- TMEM (allocated and freed by the same warp) ----
+__device__ __forceinline__ void tmem_alloc(uint32_t *smem_dst, uint32_t columns) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(smem_dst)),
                "r"(columns)
                : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t columns) {  // the same warp
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns)
                : "memory");
 }
 
-// 16 columns of this warp's 32 lanes: lane l gets (l, column 0..15) from addr.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, float *d) {
-  uint32_t r[16];
+// 64 columns of this warp's 32 lanes: lane l gets (l, column 0..63) from addr.
+__device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t *r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) d[i] = __uint_as_float(r[i]);
 }
-// Waits for this thread's TMEM loads and orders the uses of d after them.
-__device__ __forceinline__ void tmem_load_wait16(float *d) {
+// Waits for this thread's TMEM loads and orders the uses of r after them.
+__device__ __forceinline__ void tmem_load_wait64(uint32_t *r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(d[i]));
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -62,6 +68,17 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t addr) {
 // Instruction descriptor: e4m3 x e4m3 -> fp32, both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+
+// True in one lane of the (converged) warp.  Products and commits are issued
+// under it by warps that are otherwise uniform: their descriptors then stay in
+// uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // D (TMEM) = A B^T (+ D if accumulate); K = 32 bytes; one thread issues it.
@@ -103,13 +120,6 @@ __device__ __forceinline__ void setmaxnreg_inc() {
 template <int N>
 __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// 32-byte streaming store.
-__device__ __forceinline__ void st_stream_v8(void *p, const uint4 &a, const uint4 &b) {
-  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
-               "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
 }
 
 }  // namespace ep
