@@ -16,9 +16,14 @@
 // the scale of g times |w|, so K rows cost one quantisation.  gy's alignment
 // padding is zeroed by the same CTAs afterwards.
 //
-// Bias kernel: each warp owns 64 columns and a part of the tokens and adds
-// w * g to shared-memory sums of up to kBiasExperts experts, in token order;
-// the parts are added afterwards in a fixed order (no atomics).
+// Bias gradient: a sum over tokens per expert, so the slots of each chunk of
+// kChunkTokens tokens are first sorted by expert (stably, once for all columns);
+// then each warp owns 128 columns, a range of experts and a part of the chunks
+// and walks an expert's slots with its sums in registers, which meet the sums in
+// shared memory once per chunk and expert.  The parts are added afterwards in a
+// fixed order.  (No atomics, and no dense product with the mostly empty
+// weight matrix: there 0 * inf of one token's gradient would reach experts that
+// the token never chose.)
 #include <algorithm>
 
 #include "ep_internal.cuh"
@@ -248,47 +253,132 @@ __global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p)
   }
 }
 
-constexpr int kBiasCols = 64;      // columns of a warp, two per lane
-constexpr int kBiasExperts = 256;  // experts of a warp's sums (64 KB of shared memory)
+constexpr int kChunkTokens = 128;
+constexpr int kSortWarps = 8;
+constexpr int kBiasCols = 128;     // columns of a warp, four per lane
+constexpr int kBiasExperts = 64;   // experts of a warp: 32 KB of sums
+constexpr int kBiasAhead = 8;      // slots whose rows are in flight
+
+// Sorts a chunk's slots by expert: entries (token, weight) in (token, slot)
+// order within an expert, off[e] the first entry of expert e.  Each warp takes
+// consecutive tokens, 32 slots at a step.
+__global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradParams p) {
+  extern __shared__ int cnt[];  // [kSortWarps, E]
+  __shared__ int warp_sum[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nt = kSortWarps * 32;
+  int *const mine = cnt + warp * p.E;
+  for (int i = threadIdx.x; i < kSortWarps * p.E; i += nt) cnt[i] = 0;
+  griddep_wait();
+  __syncthreads();
+  constexpr int per = kChunkTokens / kSortWarps;
+  const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens + warp * per;
+  const int64_t s0 = min(t0, (int64_t)p.T) * p.K, s1 = min(t0 + per, (int64_t)p.T) * p.K;
+  auto expert = [&](int64_t s) {
+    return s < s1 && __ldg(p.dst + s) >= 0 ? __ldg(p.topk32 + s) : -1;
+  };
+  for (int64_t s = s0 + lane; s - lane < s1; s += 32) {
+    const int e = expert(s);
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  // counts -> first entry of each (expert, warp)
+  int32_t *off = p.off + (int64_t)blockIdx.x * (p.E + 1);
+  int base = 0;
+  for (int e0 = 0; e0 < p.E; e0 += nt) {
+    const int e = e0 + threadIdx.x;
+    int n = 0;
+    if (e < p.E)
+      for (int w = 0; w < kSortWarps; ++w) n += cnt[w * p.E + e];
+    int v = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    int first = base + v - n, all = base;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) first += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (e < p.E) {
+      off[e] = first;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = cnt[w * p.E + e];
+        cnt[w * p.E + e] = first;
+        first += c;
+      }
+    }
+    base = all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) off[p.E] = base;
+  int2 *ent = p.ent + (int64_t)blockIdx.x * kChunkTokens * p.K;
+  for (int64_t s = s0 + lane; s - lane < s1; s += 32) {
+    const int e = expert(s);
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    const int at = e >= 0 ? mine[e] : 0;
+    __syncwarp();
+    if (e >= 0) {
+      ent[at + __popc(peers & lanemask_lt())] =
+          make_int2((int)(s / p.K), __float_as_int(__ldg(p.topk_w + s)));
+      if (lane == __ffs(peers) - 1) mine[e] = at + __popc(peers);
+    }
+    __syncwarp();
+  }
+}
 
 __global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p, int experts) {
-  extern __shared__ float2 sum[];  // [experts, 32]
+  extern __shared__ float4 sum[];  // [experts, 32]
   const int lane = threadIdx.x;
   const int e0 = blockIdx.y * experts, ne = min(experts, p.E - e0);
-  const int col = blockIdx.x * kBiasCols + lane * 2;
+  const int col = blockIdx.x * kBiasCols + lane * 4;
   const bool in = col < p.H;
-  for (int e = 0; e < ne; ++e) sum[e * 32 + lane] = make_float2(0.f, 0.f);
+  for (int e = 0; e < ne; ++e) sum[e * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
   griddep_wait();
-  const int64_t per = ((int64_t)p.T + p.parts - 1) / p.parts;
-  const int64_t t0 = blockIdx.z * per, t1 = min((int64_t)p.T, t0 + per);
-  for (int64_t t = t0; t < t1; ++t) {
-    int e = -1;
-    float w = 0.f;
-    if (lane < p.K) {
-      e = __ldg(p.dst + t * p.K + lane) >= 0 ? __ldg(p.topk32 + t * p.K + lane) - e0 : -1;
-      w = __ldg(p.topk_w + t * p.K + lane);
-    }
-    unsigned m = __ballot_sync(0xffffffffu, e >= 0 && e < ne);
-    if (m == 0) continue;
-    const uint32_t gv = in ? __ldg(reinterpret_cast<const uint32_t *>(p.g + t * p.H + col)) : 0u;
-    const float g0 = bf16_lo(gv), g1 = bf16_hi(gv);
-    for (; m; m &= m - 1) {
-      const int k = __ffs(m) - 1;
-      const int ek = __shfl_sync(0xffffffffu, e, k);
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      float2 a = sum[ek * 32 + lane];
-      a.x = fmaf(wk, g0, a.x);
-      a.y = fmaf(wk, g1, a.y);
-      sum[ek * 32 + lane] = a;
+  const int chunks = (p.T + kChunkTokens - 1) / kChunkTokens;
+  const uint16_t *g = p.g + (in ? col : 0);
+  for (int c = blockIdx.z; c < chunks; c += p.parts) {
+    const int32_t *off = p.off + (int64_t)c * (p.E + 1) + e0;
+    const int2 *ent = p.ent + (int64_t)c * kChunkTokens * p.K;
+    int first = __ldg(off);
+    for (int e = 0; e < ne; ++e) {
+      const int end = __ldg(off + e + 1);
+      if (first == end) continue;
+      float4 a = sum[e * 32 + lane];
+      for (; first < end; first += kBiasAhead) {
+        uint2 v[kBiasAhead];
+        float w[kBiasAhead];
+#pragma unroll
+        for (int i = 0; i < kBiasAhead; ++i) {
+          const int2 x = first + i < end ? __ldg(ent + first + i) : make_int2(-1, 0);
+          w[i] = __int_as_float(x.y);
+          v[i] = x.x >= 0 ? __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)x.x * p.H))
+                          : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kBiasAhead; ++i) {
+          a.x = fmaf(w[i], bf16_lo(v[i].x), a.x);
+          a.y = fmaf(w[i], bf16_hi(v[i].x), a.y);
+          a.z = fmaf(w[i], bf16_lo(v[i].y), a.z);
+          a.w = fmaf(w[i], bf16_hi(v[i].y), a.w);
+        }
+      }
+      first = end;
+      sum[e * 32 + lane] = a;
     }
   }
   if (!in) return;
   float *o = p.part + ((int64_t)blockIdx.z * p.E + e0) * p.H + col;
   for (int e = 0; e < ne; ++e)
-    *reinterpret_cast<float2 *>(o + (int64_t)e * p.H) = sum[e * 32 + lane];
+    *reinterpret_cast<float4 *>(o + (int64_t)e * p.H) = sum[e * 32 + lane];
 }
 
 int bias_experts(int E) { return std::min(E, kBiasExperts); }
+int bias_chunks(const CombineGradParams &p) { return (p.T + kChunkTokens - 1) / kChunkTokens; }
 
 template <int U, int NV, int MAXT>
 cudaError_t launch_rows(const CombineGradParams &p, int threads, int sm_cap, cudaStream_t s) {
@@ -306,16 +396,33 @@ cudaError_t launch_rows(const CombineGradParams &p, int threads, int sm_cap, cud
 
 }  // namespace
 
-int combine_grad_parts(const CombineGradParams &p) {
-  // enough warps to fill the GPU once, at least 64 tokens each
+cudaError_t combine_grad_workspace(CombineGradParams *p, size_t *bytes, void *base) {
+  // enough warps for about five on each SM, at least a chunk each
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const int experts = bias_experts(p.E);
-  const int per_sm = std::max(1, std::min(14, (int)(220 * 1024 / (experts * 256))));
-  const int64_t blocks = (int64_t)((p.H + kBiasCols - 1) / kBiasCols) *
-                         ((p.E + experts - 1) / experts);
-  const int64_t want = ((int64_t)device_sm_count(dev) * per_sm + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, ((int64_t)p.T + 63) / 64));
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t experts = bias_experts(p->E), chunks = bias_chunks(*p);
+  const int64_t blocks = (int64_t)((p->H + kBiasCols - 1) / kBiasCols) *
+                         ((p->E + experts - 1) / experts);
+  const int64_t want = (5 * (int64_t)device_sm_count(dev) + blocks - 1) / blocks;
+  p->parts = (int)std::max<int64_t>(1, std::min(want, chunks));
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return o;
+  };
+  const size_t o_ent = take(sizeof(int2) * (size_t)chunks * kChunkTokens * p->K);
+  const size_t o_off = take(sizeof(int32_t) * (size_t)chunks * (p->E + 1));
+  const size_t o_part = take(p->parts > 1 ? sizeof(float) * (size_t)p->parts * p->E * p->H : 0);
+  *bytes = std::max<size_t>(at, 256);
+  if (base != nullptr) {
+    uint8_t *b = static_cast<uint8_t *>(base);
+    p->ent = reinterpret_cast<int2 *>(b + o_ent);
+    p->off = reinterpret_cast<int32_t *>(b + o_off);
+    p->part = p->parts > 1 ? reinterpret_cast<float *>(b + o_part) : p->gbias;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s) {
@@ -333,21 +440,21 @@ cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStre
   }
   if (e != cudaSuccess || p.gbias == nullptr) return e;
   const int experts = bias_experts(p.E);
+  const size_t sort_smem = sizeof(int) * kSortWarps * (size_t)p.E;
   const size_t smem = (size_t)experts * kBiasCols * sizeof(float);
   int dev = 0;
+  e = launch_geometry(reinterpret_cast<const void *>(bias_sort_kernel), kSortWarps * 32, sort_smem,
+                      &dev, nullptr);
+  if (e != cudaSuccess) return e;
   e = launch_geometry(reinterpret_cast<const void *>(bias_grad_kernel), 32, smem, &dev, nullptr);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((p.H + kBiasCols - 1) / kBiasCols, (p.E + experts - 1) / experts, p.parts);
-  lc.blockDim = dim3(32);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, bias_grad_kernel, p, experts);
+  if (p.T > 0) {
+    e = launch_pdl(bias_sort_kernel, dim3((unsigned)bias_chunks(p)), kSortWarps * 32, sort_smem, s,
+                   p);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid((p.H + kBiasCols - 1) / kBiasCols, (p.E + experts - 1) / experts, p.parts);
+  e = launch_pdl(bias_grad_kernel, grid, 32, smem, s, p, experts);
   if (e != cudaSuccess || p.part == p.gbias) return e;
   return launch_column_sum(p.part, p.parts, (int64_t)p.E * p.H, p.gbias, s);
 }

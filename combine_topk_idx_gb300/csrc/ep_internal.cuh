@@ -232,8 +232,11 @@ struct CombineGradParams {
   SfLayout sfl;
   float *gw;                // [T, K] or nullptr
   float *gbias;             // [E, H] or nullptr
-  float *part;              // [parts, E, H] workspace of the bias sums
+  // workspace of the bias sums: partial sums, the slots sorted by expert
+  float *part;              // [parts, E, H]
   int parts;
+  int2 *ent;
+  int32_t *off;
 };
 
 struct ExpertGemmParams {
@@ -276,7 +279,8 @@ cudaError_t norm_backward_parts(const NormBackwardParams &p, int *parts);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s);
 cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s);
 cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s);
-int combine_grad_parts(const CombineGradParams &p);
+// Bytes of the bias gradient's workspace; with `base` also its arrays in p.
+cudaError_t combine_grad_workspace(CombineGradParams *p, size_t *bytes, void *base);
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s);
 
 cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream_t s);
@@ -296,10 +300,10 @@ cudaError_t launch_geometry(const void *func, int threads, size_t smem, int *dev
 // Launch with programmatic dependent launch: the kernel may start while its
 // predecessor drains and calls griddep_wait() before it touches memory.
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, int threads, size_t smem,
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem,
                        cudaStream_t s, A... args) {
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(grid);
+  lc.gridDim = grid;
   lc.blockDim = dim3((unsigned)threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;

@@ -287,13 +287,13 @@ ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out,
   void *ws = nullptr;
   cudaError_t e = cudaSuccess;
   if (p.gbias != nullptr) {
-    p.parts = ep::combine_grad_parts(p);
-    if (p.parts < 1) return EP_ERR_CUDA;
-    p.part = p.gbias;
-    if (p.parts > 1) {
-      e = ep::workspace_alloc(sizeof(float) * (size_t)p.parts * p.E * p.H, s, &ws);
-      if (e != cudaSuccess) return ep::cuda_status(e);
-      p.part = static_cast<float *>(ws);
+    size_t bytes = 0;
+    e = ep::combine_grad_workspace(&p, &bytes, nullptr);
+    if (e == cudaSuccess) e = ep::workspace_alloc(bytes, s, &ws);
+    if (e == cudaSuccess) e = ep::combine_grad_workspace(&p, &bytes, ws);
+    if (e != cudaSuccess) {
+      if (ws != nullptr) ep::workspace_free(ws, s);
+      return ep::cuda_status(e);
     }
   }
   e = ep::launch_combine_grad(p, c.num_sms, s);
