@@ -44,19 +44,23 @@ class _Call:
         """Pointer of an optional tensor of the expected type and shape."""
         if t is None:
             return None
+        if t.get_device() != self.device or t.dtype not in dtypes or (
+                shape is not None and t.shape != shape) or not (strided or t.is_contiguous()):
+            self.refuse(t, what, dtypes, shape)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t.data_ptr() or None
+
+    def refuse(self, t, what, dtypes, shape):
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
         if t.get_device() != self.device:
-            if not t.is_cuda:
-                raise ValueError(f"{what} must be a CUDA tensor")
             raise ValueError(f"{what} is on {t.device}, the call runs on cuda:{self.device}")
         if t.dtype not in dtypes:
             raise ValueError(f"{what} has dtype {t.dtype}, expected {dtypes}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{what} shape {tuple(t.shape)} != {tuple(shape)}")
-        if not strided and not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t.data_ptr() or None
+        raise ValueError(f"{what} must be contiguous")
 
     def empty(self, *shape, dtype):
         """An output tensor of the call's stream."""
@@ -94,9 +98,9 @@ def alloc_rmsnorm(x: torch.Tensor, residual: bool = False, bf16: bool = False, f
     view, column-major with 16-byte aligned columns if ``col_major_sf``: both
     forms are what :func:`ep_dispatch_fp8` takes."""
     T, H = x.shape
-    dev = x.device
-    out = {"residual_out": torch.empty((T, H), dtype=torch.bfloat16, device=dev) if residual else None,
-           "y": torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
+    dev, bf = x.device, torch.bfloat16
+    out = {"residual_out": torch.empty((T, H), dtype=bf, device=dev) if residual else None,
+           "y": torch.empty((T, H), dtype=bf, device=dev) if bf16 else None,
            "y_fp8": None, "y_sf": None,
            "rstd": torch.empty((T,), dtype=torch.float32, device=dev) if rstd else None}
     if fp8:

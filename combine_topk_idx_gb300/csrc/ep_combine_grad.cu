@@ -128,10 +128,11 @@ __device__ __forceinline__ void write_row(const CombineGradParams &p, const Shar
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * N;
-      float f[N];
+      uint64_t f[N / 2];
       bf16_to_f32<U>(g.v[i], f);
+      const uint64_t w2 = f32x2_pack(w, w);
 #pragma unroll
-      for (int k = 0; k < N; ++k) f[k] *= w;
+      for (int k = 0; k < N / 2; ++k) f[k] = f32x2_mul_rn(f[k], w2);
       if (c < p.H) store_bf16<U>(p.gy + at + c, f);
     }
   }
@@ -155,7 +156,7 @@ __device__ __forceinline__ void write_row(const CombineGradParams &p, const Shar
 // U = 2 where H is a multiple of 16: eight neighbouring lanes then hold a
 // scale block.
 template <int U, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) combine_grad_kernel(CombineGradParams p) {
   constexpr int N = 8 * U;
   __shared__ float red_y[2][EP_MAX_TOPK][kMaxWarps + 1];
   __shared__ float red_b[2][EP_MAX_TOPK][kMaxWarps + 1];
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p)
     if (U == 2 && p.q != nullptr) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float f[N];
+        uint64_t f[N / 2];
         bf16_to_f32<U>(g.v[i], f);
         quantise_block<N>(f, q.b[i], &q.s[i]);
       }
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(MAXT) combine_grad_kernel(CombineGradParams p)
 constexpr int kChunkTokens = 128;
 constexpr int kSortWarps = 8;
 constexpr int kBiasCols = 128;     // columns of a warp, four per lane
-constexpr int kBiasExperts = 64;   // experts of a warp: 32 KB of sums
+constexpr int kBiasExperts = 16;   // experts of a warp: 8 KB of sums, so 24 warps share an SM
+constexpr int kBiasWarps = 20;     // warps of an SM that the parts are made for
 constexpr int kBiasAhead = 8;      // slots whose rows are in flight
 
 // Sorts a chunk's slots by expert: entries (token, weight) in (token, slot)
@@ -397,14 +399,14 @@ cudaError_t launch_rows(const CombineGradParams &p, int threads, int sm_cap, cud
 }  // namespace
 
 cudaError_t combine_grad_workspace(CombineGradParams *p, size_t *bytes, void *base) {
-  // enough warps for about five on each SM, at least a chunk each
+  // enough warps for about kBiasWarps on each SM, at least a chunk each
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int64_t experts = bias_experts(p->E), chunks = bias_chunks(*p);
   const int64_t blocks = (int64_t)((p->H + kBiasCols - 1) / kBiasCols) *
                          ((p->E + experts - 1) / experts);
-  const int64_t want = (5 * (int64_t)device_sm_count(dev) + blocks - 1) / blocks;
+  const int64_t want = (kBiasWarps * (int64_t)device_sm_count(dev) + blocks - 1) / blocks;
   p->parts = (int)std::max<int64_t>(1, std::min(want, chunks));
   size_t at = 0;
   auto take = [&](size_t n) {

@@ -62,9 +62,10 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(NormParams p) {
                              : (int64_t)blockIdx.x;
   if (WARP_ROW && t >= p.T) return;
   const float inv_h = 1.0f / (float)p.H;
+  const uint64_t inv2 = f32x2_pack(inv_h, inv_h);
   griddep_wait();
-  float f[NV][N];
-  float ss = 0.f;
+  uint64_t f[NV][N / 2];  // pairs
+  uint64_t ss2 = 0;
   uint4 xv[NV][U], rv[NV][U];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -84,18 +85,18 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(NormParams p) {
     const int c = (i * tpr + tid) * N;
     bf16_to_f32<U>(xv[i], f[i]);
     if (p.residual != nullptr) {
-      float r[N];
+      uint64_t r[N / 2];
       bf16_to_f32<U>(rv[i], r);
 #pragma unroll
-      for (int q = 0; q < N; ++q) f[i][q] += r[q];
+      for (int q = 0; q < N / 2; ++q) f[i][q] = f32x2_add_rn(f[i][q], r[q]);
     }
     if (c < p.H && p.res_out != nullptr) store_bf16<U>(p.res_out + t * (int64_t)p.H + c, f[i]);
     // each term over H before the sum: the mean then fits fp32 as long as it
     // does itself, although the sum of squares may not
 #pragma unroll
-    for (int q = 0; q < N; ++q) ss = fmaf(f[i][q] * inv_h, f[i][q], ss);
+    for (int q = 0; q < N / 2; ++q) ss2 = f32x2_fma_rn(f32x2_mul_rn(f[i][q], inv2), f[i][q], ss2);
   }
-  ss = row_sum<WARP_ROW>(ss, red);
+  const float ss = row_sum<WARP_ROW>(f32x2_lo(ss2) + f32x2_hi(ss2), red);
   const float k = rsqrtf(ss + p.eps);
   if (tid == 0 && p.rstd != nullptr) p.rstd[t] = k;
 #pragma unroll
@@ -108,8 +109,11 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(NormParams p) {
       for (int j = 0; j < U; ++j) {
         float g[8];
         load_gamma(p.gamma, p.gamma_f32, v * U + j, g);
+        const uint64_t k2 = f32x2_pack(k, k);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[i][8 * j + q] = f[i][8 * j + q] * k * g[q];
+        for (int q = 0; q < 4; ++q)
+          f[i][4 * j + q] = f32x2_mul_rn(f32x2_mul_rn(f[i][4 * j + q], k2),
+                                         f32x2_pack(g[2 * q], g[2 * q + 1]));
       }
       if (p.y != nullptr) store_bf16<U>(p.y + t * (int64_t)p.H + c, f[i]);
     }

@@ -54,30 +54,29 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float *f) {
                     cvt_bf16x2(f[6], f[7]));
 }
 
-// The eight e4m3 values of an 8-byte vector as fp32 (exact; through f16,
-// which holds every e4m3 value).
-__device__ __forceinline__ void e4m3x8_to_f32(const uint2 &v, float *f) {
-  const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    asm("{\n\t.reg .b16 l, h, e0, e1, e2, e3;\n\t.reg .b32 p, q;\n\t"
-        "mov.b32 {l, h}, %4;\n\t"
-        "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\t"
-        "mov.b32 {e0, e1}, p;\n\tmov.b32 {e2, e3}, q;\n\t"
-        "cvt.f32.f16 %0, e0;\n\tcvt.f32.f16 %1, e1;\n\t"
-        "cvt.f32.f16 %2, e2;\n\tcvt.f32.f16 %3, e3;\n\t}"
-        : "=f"(f[4 * i]), "=f"(f[4 * i + 1]), "=f"(f[4 * i + 2]), "=f"(f[4 * i + 3])
-        : "r"(w[i]));
-  }
+// Four e4m3 values as two pairs of fp32 (exact; through f16, which holds every
+// e4m3 value).
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t v, uint64_t *f) {
+  float a, b, c, d;
+  asm("{\n\t.reg .b16 l, h, e0, e1, e2, e3;\n\t.reg .b32 p, q;\n\t"
+      "mov.b32 {l, h}, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\t"
+      "mov.b32 {e0, e1}, p;\n\tmov.b32 {e2, e3}, q;\n\t"
+      "cvt.f32.f16 %0, e0;\n\tcvt.f32.f16 %1, e1;\n\t"
+      "cvt.f32.f16 %2, e2;\n\tcvt.f32.f16 %3, e3;\n\t}"
+      : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+      : "r"(v));
+  f[0] = f32x2_pack(a, b);
+  f[1] = f32x2_pack(c, d);
 }
 
-// Largest magnitude of N values; NaN if any is one.
+// Largest magnitude of N values held in pairs; NaN if any is one.
 template <int N>
-__device__ __forceinline__ float amax_of(const float *f) {
+__device__ __forceinline__ float amax_of(const uint64_t *f) {
   float m = 0.f;
 #pragma unroll
-  for (int q = 0; q < N; q += 2)
-    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f[q]), "f"(f[q + 1]));
+  for (int q = 0; q < N / 2; ++q)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f32x2_lo(f[q])), "f"(f32x2_hi(f[q])));
   return m;
 }
 
@@ -91,7 +90,7 @@ __device__ __forceinline__ float amax_of(const float *f) {
 // code in every byte; one holding an infinity scale +inf, zeros for its finite
 // values and the NaN code for the infinite ones.
 template <int N>
-__device__ __forceinline__ void quantise_block(const float *f, uint32_t *bytes, float *scale) {
+__device__ __forceinline__ void quantise_block(const uint64_t *f, uint32_t *bytes, float *scale) {
   float amax = amax_of<N>(f);
 #pragma unroll
   for (int o = 1; o < 128 / N; o *= 2)
@@ -101,7 +100,13 @@ __device__ __forceinline__ void quantise_block(const float *f, uint32_t *bytes, 
   if (amax < 0x1p-100f) {
 #pragma unroll
     for (int i = 0; i < N / 8; ++i) {
-      const uint2 b = sc != 0.f ? e4m3_block8(f + 8 * i, sc) : make_uint2(0, 0);
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = f32x2_lo(f[4 * i + q]);
+        v[2 * q + 1] = f32x2_hi(f[4 * i + q]);
+      }
+      const uint2 b = sc != 0.f ? e4m3_block8(v, sc) : make_uint2(0, 0);
       bytes[2 * i] = b.x;
       bytes[2 * i + 1] = b.y;
     }
@@ -111,23 +116,31 @@ __device__ __forceinline__ void quantise_block(const float *f, uint32_t *bytes, 
   const uint64_t r2 = f32x2_pack(r, r);
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const uint64_t v = f32x2_mul_rn(f32x2_pack(f[4 * i], f[4 * i + 1]), r2);
-    const uint64_t w = f32x2_mul_rn(f32x2_pack(f[4 * i + 2], f[4 * i + 3]), r2);
+    const uint64_t v = f32x2_mul_rn(f[2 * i], r2), w = f32x2_mul_rn(f[2 * i + 1], r2);
     bytes[i] = cvt_e4m3x4(f32x2_lo(v), f32x2_hi(v), f32x2_lo(w), f32x2_hi(w));
   }
 }
 
-// A thread's U vectors of eight BF16 values, and U * 8 e4m3 bytes.
+// A thread's U vectors of eight BF16 values as pairs of fp32, and U * 8 e4m3
+// bytes.
 template <int U>
-__device__ __forceinline__ void bf16_to_f32(const uint4 *v, float *f) {
+__device__ __forceinline__ void bf16_to_f32(const uint4 *v, uint64_t *f) {
 #pragma unroll
-  for (int i = 0; i < U; ++i) bf16x8_to_f32(v[i], f + 8 * i);
+  for (int i = 0; i < U; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[4 * i + q] = f32x2_pack(bf16_lo(w[q]), bf16_hi(w[q]));
+  }
 }
 template <int U>
-__device__ __forceinline__ void store_bf16(void *p, const float *f) {
+__device__ __forceinline__ void store_bf16(void *p, const uint64_t *f) {
 #pragma unroll
-  for (int i = 0; i < U; ++i)
-    st_stream_v4(static_cast<uint8_t *>(p) + 16 * i, f32_to_bf16x8(f + 8 * i));
+  for (int i = 0; i < U; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = cvt_bf16x2(f32x2_lo(f[4 * i + q]), f32x2_hi(f[4 * i + q]));
+    st_stream_v4(static_cast<uint8_t *>(p) + 16 * i, make_uint4(w[0], w[1], w[2], w[3]));
+  }
 }
 template <int U>
 __device__ __forceinline__ void store_bytes(void *p, const uint32_t *b) {

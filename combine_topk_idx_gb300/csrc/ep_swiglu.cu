@@ -24,13 +24,17 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileVecs = 1024;  // vectors of F per tile: rows per tile = kTileVecs / (F / 8)
-constexpr int kMaxTileRows = 64; // F >= 128: at most 1024 / 16 rows
+constexpr int kTileElems = 32768;  // of F per tile, at most
+constexpr int kMaxTileRows = 64;
 
-// 1 / (1 + e^-g): relative error about 2^-21 plus the rounding of g's exponent
-// (|g| 2^-24); 0 where e^-g overflows.
-__device__ __forceinline__ float sigmoid(float g) {
-  return rcp_approx(1.0f + exp2_approx(g * -1.4426950408889634f));
+// 1 / (1 + e^-g) of a pair: relative error about 2^-21 plus the rounding of g's
+// exponent (|g| 2^-24); 0 where e^-g overflows.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  const float c = -1.4426950408889634f;
+  const uint64_t x = f32x2_mul_rn(g, f32x2_pack(c, c));
+  const uint64_t y = f32x2_add_rn(f32x2_pack(exp2_approx(f32x2_lo(x)), exp2_approx(f32x2_hi(x))),
+                                  f32x2_pack(1.f, 1.f));
+  return f32x2_pack(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y)));
 }
 
 struct TileRow {
@@ -74,9 +78,28 @@ struct Walk {
 };
 
 // A unit is U vectors: 16 elements (F a multiple of 128, where 8 neighbouring
-// lanes hold one scale block), or 8 (BF16 output only).
+// lanes hold one scale block), or 8 (BF16 output only).  A thread loads a unit
+// while it works on the one before.
 template <int U>
-__global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p, int tile_rows) {
+struct Unit {
+  TileRow t;
+  uint4 g[U], u[U];
+  __device__ __forceinline__ bool use() const { return t.row >= 0 && !t.pad; }
+  __device__ __forceinline__ void load(const SwigluParams &p, const TileRow *rows, const Walk &k,
+                                       bool any) {
+    t = TileRow{-1, 0.f, 0};
+    if (any) t = rows[k.i];
+    const uint16_t *h = p.h + t.row * 2 * p.F + k.v * (8 * U);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      g[i] = use() ? ld_stream_v4(h + 8 * i) : make_uint4(0, 0, 0, 0);
+      u[i] = use() ? ld_stream_v4(h + p.F + 8 * i) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
+template <int U>
+__global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int tile_rows) {
   constexpr int N = 8 * U;
   __shared__ TileRow rows[2][kMaxTileRows];
   griddep_wait();
@@ -92,48 +115,51 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p, int ti
     __syncthreads();
     next = load_row(p.r, p.row_w, i0 + step, tile_rows, items);  // used a tile later
     Walk k = w0;
-    for (int id = threadIdx.x; id - (int)(threadIdx.x & 31) < total; id += kThreads, k.step()) {
-      TileRow t{-1, 0.f, 0};
-      if (id < total) t = rows[par][k.i];
-      const bool use = t.row >= 0 && !t.pad;
-      const int c = k.v * N;  // first column
-      uint4 gv[U], uv[U];
-      const uint16_t *h = p.h + t.row * 2 * p.F + c;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        gv[i] = use ? ld_stream_v4(h + 8 * i) : make_uint4(0, 0, 0, 0);
-        uv[i] = use ? ld_stream_v4(h + p.F + 8 * i) : make_uint4(0, 0, 0, 0);
-      }
-      float g[N], u[N], a[N];
-      bf16_to_f32<U>(gv, g);
-      bf16_to_f32<U>(uv, u);
-#pragma unroll
-      for (int q = 0; q < N; ++q) a[q] = g[q] * sigmoid(g[q]) * (u[q] * t.w);
-      if (p.act != nullptr && t.row >= 0) store_bf16<U>(p.act + t.row * p.F + c, a);
+    Unit<U> ahead;
+    ahead.load(p, rows[par], k, (int)threadIdx.x < total);
+    for (int id = threadIdx.x; id - (int)(threadIdx.x & 31) < total; id += kThreads) {
+      const Unit<U> x = ahead;
+      const TileRow t = x.t;
+      const bool use = x.use();
+      const int v = k.v, c = v * N;  // first column
+      k.step();
+      ahead.load(p, rows[par], k, id + kThreads < total);
+      const int j = v >> 3;
+      const bool first = (v & 7) == 0;
       if constexpr (U == 2) {
-        float sc;
-        uint32_t b[4];
-        const int j = k.v >> 3;
-        const bool first = (k.v & 7) == 0;
+        if (p.ckpt != nullptr) {  // one at a time: fewer values live
+          uint8_t *o = p.ckpt + t.row * 2 * p.F + c;
+          float *os = p.ckpt_sf + t.row * (p.F / 64) + j;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint64_t f[N / 2];
+            uint32_t b[4];
+            float sc;
+            bf16_to_f32<U>(half ? x.u : x.g, f);
+            quantise_block<N>(f, b, &sc);
+            if (use) {
+              store_bytes<U>(o + half * p.F, b);
+              if (first) os[half * (p.F / 128)] = sc;
+            }
+          }
+        }
+      }
+      uint64_t g[N / 2], u[N / 2];
+      bf16_to_f32<U>(x.g, g);
+      bf16_to_f32<U>(x.u, u);
+      const uint64_t w2 = f32x2_pack(t.w, t.w);
+#pragma unroll
+      for (int q = 0; q < N / 2; ++q)
+        g[q] = f32x2_mul_rn(f32x2_mul_rn(g[q], sigmoid2(g[q])), f32x2_mul_rn(u[q], w2));
+      if (p.act != nullptr && t.row >= 0) store_bf16<U>(p.act + t.row * p.F + c, g);
+      if constexpr (U == 2) {
         if (p.q != nullptr) {
-          quantise_block<N>(a, b, &sc);
+          float sc;
+          uint32_t b[4];
+          quantise_block<N>(g, b, &sc);
           if (t.row >= 0) {
             store_bytes<U>(p.q + t.row * p.F + c, b);
             if (first) p.sf[sf_at(p.sfl, t.row, j)] = sc;
-          }
-        }
-        if (p.ckpt != nullptr) {
-          uint8_t *o = p.ckpt + t.row * 2 * p.F + c;
-          float *os = p.ckpt_sf + t.row * (p.F / 64) + j;
-          quantise_block<N>(g, b, &sc);
-          if (use) {
-            store_bytes<U>(o, b);
-            if (first) os[0] = sc;
-          }
-          quantise_block<N>(u, b, &sc);
-          if (use) {
-            store_bytes<U>(o + p.F, b);
-            if (first) os[p.F / 128] = sc;
           }
         }
       }
@@ -141,6 +167,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p, int ti
   }
 }
 
+// Bound by instruction issue rather than by loads: loading a unit ahead as above
+// costs registers, and so resident warps (measured 114 -> 122 us at 4096 tokens
+// x 8 experts, ffn 2048).
 __global__ void __launch_bounds__(kThreads)
     swiglu_backward_kernel(SwigluBackwardParams p, int tile_rows) {
   constexpr int U = 2, N = 8 * U;
@@ -177,27 +206,30 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int i = 0; i < U; ++i) dv[i] = use ? ld_stream_v4(ga + 8 * i) : zero;
       const float gs = use ? __ldg(cs) : 0.f, us = use ? __ldg(cs + nb) : 0.f;
-      float gg[N], gu[N];  // the checkpoint's gate and up, then their gradients
-      e4m3x8_to_f32(make_uint2(gq.x, gq.y), gg);
-      e4m3x8_to_f32(make_uint2(gq.z, gq.w), gg + 8);
-      e4m3x8_to_f32(make_uint2(uq.x, uq.y), gu);
-      e4m3x8_to_f32(make_uint2(uq.z, uq.w), gu + 8);
-      float dot = 0.f;
+      uint64_t gg[N / 2], gu[N / 2];  // the checkpoint's gate and up, then their gradients
+      const uint32_t gw4[4] = {gq.x, gq.y, gq.z, gq.w}, uw4[4] = {uq.x, uq.y, uq.z, uq.w};
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float d[8];
-        bf16x8_to_f32(dv[i], d);
+      for (int q = 0; q < 4; ++q) {
+        e4m3x4_to_f32(gw4[q], gg + 2 * q);
+        e4m3x4_to_f32(uw4[q], gu + 2 * q);
+      }
+      uint64_t d[N / 2], dot2 = 0;
+      bf16_to_f32<U>(dv, d);
+      const uint64_t gs2 = f32x2_pack(gs, gs), us2 = f32x2_pack(us, us);
+      const uint64_t w2 = f32x2_pack(t.w, t.w), one = f32x2_pack(1.f, 1.f);
+      const uint64_t minus = f32x2_pack(-1.f, -1.f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float g = gg[8 * i + q] * gs, u = gu[8 * i + q] * us;
-          const float sg = sigmoid(g), sl = g * sg;
-          const float du = d[q] * u;
-          dot = fmaf(du, sl, dot);
-          gu[8 * i + q] = d[q] * t.w * sl;
-          gg[8 * i + q] = du * t.w * fmaf(sl, 1.f - sg, sg);
-        }
+      for (int q = 0; q < N / 2; ++q) {
+        const uint64_t g = f32x2_mul_rn(gg[q], gs2), u = f32x2_mul_rn(gu[q], us2);
+        const uint64_t sg = sigmoid2(g), sl = f32x2_mul_rn(g, sg);
+        const uint64_t du = f32x2_mul_rn(d[q], u);
+        dot2 = f32x2_fma_rn(du, sl, dot2);
+        gu[q] = f32x2_mul_rn(f32x2_mul_rn(d[q], w2), sl);
+        gg[q] = f32x2_mul_rn(f32x2_mul_rn(du, w2),
+                             f32x2_fma_rn(sl, f32x2_fma_rn(sg, minus, one), sg));
       }
       if (p.gw != nullptr) {
+        float dot = f32x2_lo(dot2) + f32x2_hi(dot2);
 #pragma unroll
         for (int o = 1; o < 8; o *= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (id < total && first) sum[k.i * nb + j] = dot;
@@ -234,34 +266,41 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-int rows_per_tile(int F) { return std::max(1, std::min(kMaxTileRows, kTileVecs / (F / 8))); }
-
-cudaError_t grid_for(const void *func, size_t smem, int64_t rows, int tile, unsigned *grid) {
+// Rows per tile and CTAs: tiles of up to kTileElems elements (a barrier each),
+// shorter where the rows would not give every CTA four, so that the CTAs' loads
+// differ little.
+cudaError_t shape_for(const void *func, int64_t rows, int F, bool sums, int *tile,
+                      unsigned *grid, size_t *smem) {
+  const int most = std::max(1, std::min(kMaxTileRows, kTileElems / F));
+  *smem = sums ? 2 * sizeof(float) * (size_t)most * (F / kFp8Block) : 0;
   int dev = 0, per_sm = 0;
-  const cudaError_t e = launch_geometry(func, kThreads, smem, &dev, &per_sm);
+  const cudaError_t e = launch_geometry(func, kThreads, *smem, &dev, &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (rows + tile - 1) / tile;
-  *grid = (unsigned)std::min<int64_t>(tiles, (int64_t)device_sm_count(dev) * std::max(per_sm, 1));
+  const int64_t ctas = (int64_t)device_sm_count(dev) * std::max(per_sm, 1);
+  *tile = (int)std::max<int64_t>(1, std::min<int64_t>(most, rows / (4 * ctas)));
+  *grid = (unsigned)std::min<int64_t>((rows + *tile - 1) / *tile, ctas);
   return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s) {
-  const int tile = rows_per_tile(p.F);
   auto kern = p.F % kFp8Block == 0 ? swiglu_kernel<2> : swiglu_kernel<1>;
+  int tile = 0;
   unsigned grid = 0;
-  const cudaError_t e = grid_for(reinterpret_cast<const void *>(kern), 0, p.r.rows, tile, &grid);
+  size_t smem = 0;
+  const cudaError_t e = shape_for(reinterpret_cast<const void *>(kern), p.r.rows, p.F, false,
+                                  &tile, &grid, &smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, grid, kThreads, 0, s, p, tile);
+  return launch_pdl(kern, grid, kThreads, smem, s, p, tile);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s) {
-  const int tile = rows_per_tile(p.F);
-  const size_t smem = 2 * sizeof(float) * (size_t)tile * (p.F / 128);
+  int tile = 0;
   unsigned grid = 0;
-  const cudaError_t e = grid_for(reinterpret_cast<const void *>(swiglu_backward_kernel), smem,
-                                 p.r.rows, tile, &grid);
+  size_t smem = 0;
+  const cudaError_t e = shape_for(reinterpret_cast<const void *>(swiglu_backward_kernel), p.r.rows,
+                                  p.F, true, &tile, &grid, &smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(swiglu_backward_kernel, grid, kThreads, smem, s, p, tile);
 }
