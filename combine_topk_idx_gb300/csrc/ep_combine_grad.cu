@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) combine_grad_kernel
   }
 }
 
-constexpr int kChunkTokens = 128;
+constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
 constexpr int kBiasCols = 128;     // columns of a warp, four per lane
 constexpr int kBiasExperts = 16;   // experts of a warp: 8 KB of sums, so 24 warps share an SM
@@ -333,50 +333,51 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   }
 }
 
-__global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p, int experts) {
+// Warp (x, y, z): columns x * 128 .., experts y, y + gridDim.y, ... (popular
+// experts, often neighbours, fall to different warps), chunks z, z + parts, ...
+__global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p) {
   extern __shared__ float4 sum[];  // [experts, 32]
   const int lane = threadIdx.x;
-  const int e0 = blockIdx.y * experts, ne = min(experts, p.E - e0);
+  const int ne = (p.E - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
   const int col = blockIdx.x * kBiasCols + lane * 4;
   const bool in = col < p.H;
-  for (int e = 0; e < ne; ++e) sum[e * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < ne; ++i) sum[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
   griddep_wait();
   const int chunks = (p.T + kChunkTokens - 1) / kChunkTokens;
   const uint16_t *g = p.g + (in ? col : 0);
   for (int c = blockIdx.z; c < chunks; c += p.parts) {
-    const int32_t *off = p.off + (int64_t)c * (p.E + 1) + e0;
+    const int32_t *off = p.off + (int64_t)c * (p.E + 1) + blockIdx.y;
     const int2 *ent = p.ent + (int64_t)c * kChunkTokens * p.K;
-    int first = __ldg(off);
-    for (int e = 0; e < ne; ++e) {
-      const int end = __ldg(off + e + 1);
+    for (int i = 0; i < ne; ++i, off += gridDim.y) {
+      int first = __ldg(off);
+      const int end = __ldg(off + 1);
       if (first == end) continue;
-      float4 a = sum[e * 32 + lane];
+      float4 a = sum[i * 32 + lane];
       for (; first < end; first += kBiasAhead) {
         uint2 v[kBiasAhead];
         float w[kBiasAhead];
 #pragma unroll
-        for (int i = 0; i < kBiasAhead; ++i) {
-          const int2 x = first + i < end ? __ldg(ent + first + i) : make_int2(-1, 0);
-          w[i] = __int_as_float(x.y);
-          v[i] = x.x >= 0 ? __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)x.x * p.H))
+        for (int q = 0; q < kBiasAhead; ++q) {
+          const int2 x = first + q < end ? __ldg(ent + first + q) : make_int2(-1, 0);
+          w[q] = __int_as_float(x.y);
+          v[q] = x.x >= 0 ? __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)x.x * p.H))
                           : make_uint2(0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < kBiasAhead; ++i) {
-          a.x = fmaf(w[i], bf16_lo(v[i].x), a.x);
-          a.y = fmaf(w[i], bf16_hi(v[i].x), a.y);
-          a.z = fmaf(w[i], bf16_lo(v[i].y), a.z);
-          a.w = fmaf(w[i], bf16_hi(v[i].y), a.w);
+        for (int q = 0; q < kBiasAhead; ++q) {
+          a.x = fmaf(w[q], bf16_lo(v[q].x), a.x);
+          a.y = fmaf(w[q], bf16_hi(v[q].x), a.y);
+          a.z = fmaf(w[q], bf16_lo(v[q].y), a.z);
+          a.w = fmaf(w[q], bf16_hi(v[q].y), a.w);
         }
       }
-      first = end;
-      sum[e * 32 + lane] = a;
+      sum[i * 32 + lane] = a;
     }
   }
   if (!in) return;
-  float *o = p.part + ((int64_t)blockIdx.z * p.E + e0) * p.H + col;
-  for (int e = 0; e < ne; ++e)
-    *reinterpret_cast<float4 *>(o + (int64_t)e * p.H) = sum[e * 32 + lane];
+  float *o = p.part + ((int64_t)blockIdx.z * p.E + blockIdx.y) * p.H + col;
+  for (int i = 0; i < ne; ++i)
+    *reinterpret_cast<float4 *>(o + (int64_t)i * gridDim.y * p.H) = sum[i * 32 + lane];
 }
 
 int bias_experts(int E) { return std::min(E, kBiasExperts); }
@@ -456,7 +457,7 @@ cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStre
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((p.H + kBiasCols - 1) / kBiasCols, (p.E + experts - 1) / experts, p.parts);
-  e = launch_pdl(bias_grad_kernel, grid, 32, smem, s, p, experts);
+  e = launch_pdl(bias_grad_kernel, grid, 32, smem, s, p);
   if (e != cudaSuccess || p.part == p.gbias) return e;
   return launch_column_sum(p.part, p.parts, (int64_t)p.E * p.H, p.gbias, s);
 }
