@@ -254,6 +254,7 @@ class Handle:
         self.status = status
         self.T, self.K, self.E, self.R = cfg.num_tokens, cfg.num_topk, cfg.num_experts, cfg.num_ranks
         self.H = cfg.hidden
+        self.sf_layouts = {}  # of sf_layout, by row length
 
     @property
     def ptr(self) -> int:

@@ -44,8 +44,9 @@ class _Call:
         """Pointer of an optional tensor of the expected type and shape."""
         if t is None:
             return None
-        if t.get_device() != self.device or t.dtype not in dtypes or (
-                shape is not None and t.shape != shape) or not (strided or t.is_contiguous()):
+        if (t.get_device() != self.device or t.dtype not in dtypes
+                or (shape is not None and t.shape != shape)
+                or not (strided or t.is_contiguous())):
             self.refuse(t, what, dtypes, shape)
         if self.other is not None:
             t.record_stream(self.other)
@@ -78,11 +79,15 @@ class _Call:
 def sf_layout(handle: Handle, n: int):
     """(numel, token_stride, hidden_stride, expert_stride) of the fp32 scales of
     rows of ``n`` elements in the handle's layout (``ep_sf_layout``)."""
-    v = [ctypes.c_int64() for _ in range(4)]
-    st = load_library().ep_sf_layout(ctypes.c_void_p(handle.ptr), n, *map(ctypes.byref, v))
-    if st != EP_OK:
-        raise EpError(st, "ep_sf_layout")
-    return tuple(x.value for x in v)
+    ptr = ctypes.c_void_p(handle.ptr)
+    known = handle.sf_layouts.get(n)  # fixed for the handle's life
+    if known is None:
+        v = [ctypes.c_int64() for _ in range(4)]
+        st = load_library().ep_sf_layout(ptr, n, *map(ctypes.byref, v))
+        if st != EP_OK:
+            raise EpError(st, "ep_sf_layout")
+        known = handle.sf_layouts[n] = tuple(x.value for x in v)
+    return known
 
 
 def alloc_fp8(handle: Handle, n: int, zero: bool = False):
@@ -98,28 +103,27 @@ def alloc_rmsnorm(x: torch.Tensor, residual: bool = False, bf16: bool = False, f
     view, column-major with 16-byte aligned columns if ``col_major_sf``: both
     forms are what :func:`ep_dispatch_fp8` takes."""
     T, H = x.shape
-    dev, bf = x.device, torch.bfloat16
-    out = {"residual_out": torch.empty((T, H), dtype=bf, device=dev) if residual else None,
-           "y": torch.empty((T, H), dtype=bf, device=dev) if bf16 else None,
-           "y_fp8": None, "y_sf": None,
-           "rstd": torch.empty((T,), dtype=torch.float32, device=dev) if rstd else None}
+    # of x's shape by empty_like: half the time of torch.empty, and a small call is mostly this
+    like, dense, f32 = torch.empty_like, torch.contiguous_format, torch.float32
+    out = {"residual_out": like(x, memory_format=dense) if residual else None,
+           "y": like(x, memory_format=dense) if bf16 else None, "y_fp8": None, "y_sf": None,
+           "rstd": x.new_empty((T,), dtype=f32) if rstd else None}
     if fp8:
-        out["y_fp8"] = torch.empty((T, H), dtype=torch.uint8, device=dev)
+        out["y_fp8"] = like(x, dtype=torch.uint8, memory_format=dense)
         if col_major_sf:
-            sf = torch.empty((H // 128, -(-T // 4) * 4), dtype=torch.float32, device=dev)
-            out["y_sf"] = sf[:, :T].t()
+            # not a view of a larger tensor: slicing and transposing one takes 6 us more
+            out["y_sf"] = x.new_empty_strided((T, H // 128), (1, max(4, -(-T // 4) * 4)), dtype=f32)
         else:
-            out["y_sf"] = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+            out["y_sf"] = x.new_empty((T, H // 128), dtype=f32)
     return out
 
 
 def _row_stride(t: torch.Tensor, what: str) -> int:
     T, H = t.shape
-    if t.numel() == 0:
-        return -(-H // 8) * 8
-    if H > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and H > 1 and T > 0:
         raise ValueError(f"{what} must be dense within a row")
-    return t.stride(0) if T > 1 else -(-H // 8) * 8
+    return row if T > 1 and H > 0 else -(-H // 8) * 8
 
 
 def _gamma(c: _Call, gamma: torch.Tensor, H: int):
@@ -139,20 +143,22 @@ def ep_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float,
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
     T, H = x.shape
-    xp = c.ptr(x, "x", _BF16, strided=True)
-    rp = c.ptr(residual, "residual", _BF16, x.shape, strided=True)
+    shape = x.shape
+    xp = c.ptr(x, "x", _BF16, None, True)
+    rp = c.ptr(residual, "residual", _BF16, shape, True)
     gp, f32 = _gamma(c, gamma, H)
     ts = hs = 0
     sp = None
     if y_sf is not None:
-        sp = c.ptr(y_sf, "y_sf", _F32, (T, H // 128), strided=True)
-        if any(st == 0 and n > 1 for st, n in zip(y_sf.stride(), y_sf.shape)):
+        sp = c.ptr(y_sf, "y_sf", _F32, (T, H // 128), True)
+        ts, hs = y_sf.stride()
+        if (ts == 0 and T > 1) or (hs == 0 and H >= 256):
             raise ValueError("y_sf must not be an expanded tensor")
-        ts, hs = max(y_sf.stride(0), 1), max(y_sf.stride(1), 1)
+        ts, hs = ts or 1, hs or 1
     c(T, H, xp, _row_stride(x, "x"), rp,
       0 if residual is None else _row_stride(residual, "residual"), gp, f32, eps,
-      c.ptr(residual_out, "residual_out", _BF16, x.shape), c.ptr(y, "y", _BF16, x.shape),
-      c.ptr(y_fp8, "y_fp8", _FP8, x.shape), sp, ts, hs, c.ptr(rstd, "rstd", _F32, (T,)))
+      c.ptr(residual_out, "residual_out", _BF16, shape), c.ptr(y, "y", _BF16, shape),
+      c.ptr(y_fp8, "y_fp8", _FP8, shape), sp, ts, hs, c.ptr(rstd, "rstd", _F32, (T,)))
 
 
 def ep_rmsnorm_backward(grad_y: torch.Tensor, normed: torch.Tensor, gamma: torch.Tensor,

@@ -14,7 +14,10 @@
 // gy written once, g once per token.  As FP8 rows, g is quantised once per
 // token: the bytes are those of g (with the sign of the weight), the scale is
 // the scale of g times |w|, so K rows cost one quantisation.  gy's alignment
-// padding is zeroed by the same CTAs afterwards.
+// padding is zeroed by the same CTAs afterwards.  Memory bounds it: 4096 tokens
+// x 8 experts, H = 7168, FP8 rows, 165 us for 771 MB and 77 MB of zeroed
+// padding, 5.1 TB/s; each row of y waits for its token's slots and is then
+// read in two pieces a thread, so the loads in flight limit it.
 //
 // Bias gradient: a sum over tokens per expert, so the slots of each chunk of
 // kChunkTokens tokens are first sorted by expert (stably, once for all columns);
@@ -136,18 +139,20 @@ __device__ __forceinline__ void write_row(const CombineGradParams &p, const Shar
       if (c < p.H) store_bf16<U>(p.gy + at + c, f);
     }
   }
-  if (U == 2 && p.q != nullptr) {
-    const uint32_t flip = w < 0.f ? 0x80808080u : 0u;
-    const uint32_t keep = w != 0.f ? 0xffffffffu : 0u;
+  if constexpr (U == 2) {
+    if (p.q != nullptr) {
+      const uint32_t flip = w < 0.f ? 0x80808080u : 0u;
+      const uint32_t keep = w != 0.f ? 0xffffffffu : 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = i * blockDim.x + threadIdx.x;
-      if (v * N < p.H) {
-        uint32_t b[2 * U];
+      for (int i = 0; i < NV; ++i) {
+        const int v = i * blockDim.x + threadIdx.x;
+        if (v * N < p.H) {
+          uint32_t b[2 * U];
 #pragma unroll
-        for (int k = 0; k < 2 * U; ++k) b[k] = (q.b[i][k] ^ flip) & keep;
-        store_bytes<U>(p.q + at + v * N, b);
-        if ((v & 7) == 0) p.sf[sf0 + (v >> 3) * p.sfl.hs] = fabsf(w) * q.s[i];
+          for (int k = 0; k < 2 * U; ++k) b[k] = (q.b[i][k] ^ flip) & keep;
+          store_bytes16(p.q + at + v * N, b);
+          if ((v & 7) == 0) p.sf[sf0 + (v >> 3) * p.sfl.hs] = fabsf(w) * q.s[i];
+        }
       }
     }
   }
@@ -156,7 +161,8 @@ __device__ __forceinline__ void write_row(const CombineGradParams &p, const Shar
 // U = 2 where H is a multiple of 16: eight neighbouring lanes then hold a
 // scale block.
 template <int U, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) combine_grad_kernel(CombineGradParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
+    combine_grad_kernel(CombineGradParams p) {
   constexpr int N = 8 * U;
   __shared__ float red_y[2][EP_MAX_TOPK][kMaxWarps + 1];
   __shared__ float red_b[2][EP_MAX_TOPK][kMaxWarps + 1];
@@ -169,12 +175,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) combine_grad_kernel
     g.template load<true>(p.g + t * H, p.H, true);
     const Slots s = load_slots(p, t, lane);
     ShareFp8<U, NV> q;
-    if (U == 2 && p.q != nullptr) {
+    if constexpr (U == 2) {
+      if (p.q != nullptr) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        uint64_t f[N / 2];
-        bf16_to_f32<U>(g.v[i], f);
-        quantise_block<N>(f, q.b[i], &q.s[i]);
+        for (int i = 0; i < NV; ++i) {
+          uint64_t f[N / 2];
+          bf16_to_f32<U>(g.v[i], f);
+          quantise_block16(f, q.b[i], &q.s[i]);
+        }
       }
     }
     // the token's rows, two at a time
@@ -254,6 +262,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) combine_grad_kernel
   }
 }
 
+// 16,384 tokens x 6 of 64 experts, skewed, H = 4096: sorting 9 us, sums 150
+// (402 MB of gradient rows, from L2 once each), join 17.  Whole call 372 us;
+// with chunks of 128 tokens 382, with 8 experts a warp 404 and with 32 480.
+// Parts for 32 warps an SM take 362 there but 369 against 354 with 4096 tokens
+// x 8 of 256 experts, H = 7168.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
 constexpr int kBiasCols = 128;     // columns of a warp, four per lane
@@ -431,14 +444,15 @@ cudaError_t combine_grad_workspace(CombineGradParams *p, size_t *bytes, void *ba
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.T > 0 && (p.gy != nullptr || p.q != nullptr || p.gw != nullptr)) {
-    // 32 elements per thread
+    // 32 elements per thread.  Up to 256 threads, H = 8192, with registers for
+    // three CTAs to an SM: 4096 tokens x 8, H = 7168, 165 us against 180 where
+    // the bound is that of longer rows, and 250 with registers without limit.
     const int threads = std::max(32, ((p.H + 31) / 32 + 31) / 32 * 32);
     if (p.H % 16 == 0)
-      e = threads <= 256   ? launch_rows<2, 2, 256>(p, threads, sm_cap, s)
-          : threads <= 512 ? launch_rows<2, 2, 512>(p, threads, sm_cap, s)
-                           : launch_rows<2, 2, 1024>(p, threads, sm_cap, s);
+      e = threads <= 256 ? launch_rows<2, 2, 256>(p, threads, sm_cap, s)
+                         : launch_rows<2, 2, 1024>(p, threads, sm_cap, s);
     else
-      e = threads <= 512 ? launch_rows<1, 4, 512>(p, threads, sm_cap, s)
+      e = threads <= 256 ? launch_rows<1, 4, 256>(p, threads, sm_cap, s)
                          : launch_rows<1, 4, 1024>(p, threads, sm_cap, s);
   }
   if (e != cudaSuccess || p.gbias == nullptr) return e;

@@ -18,7 +18,18 @@
 // Each block's sum has its own scales, so it cannot stay in TMEM.  With the
 // rows in TMEM lanes a block's scale is one register per thread; with the
 // columns there it would be one per accumulator column, and fetching those from
-// shared memory takes longer than the products.
+// shared memory takes longer than the products (2310 us against 1569 in the
+// third case below).  A row leaves as 32-byte stores straight from registers:
+// through shared memory, which the tensor cores keep busy, they took 3 % more.
+//
+// What bounds it.  Few rows, the weights' bytes: 8 rows, each its expert, N 4096,
+// K 7168, 40.5 us for 235 MB, 5.8 TB/s of 6.7 that a copy reaches.  128 rows per
+// expert, 256 experts: 1374 us for 8.0 GB, 5.8 TB/s.  Many rows, the scaled sums:
+// 96,300 rows over 64 experts, N = K = 4096, 1451 us, 2.2 PFLOP/s.  The products
+// of a block would take 512 cycles; 32,768 sums read from TMEM, scaled and added
+// by eight warps, with two barriers, take about twice that.  Pairs of CTAs
+// sharing the operands (1480 us) did not help, nor does any layout in which an
+// epilogue thread spills (20 to 60 % slower): hence 232 registers for it.
 //
 // Every mbarrier wait is bounded: one that gives up sets EP_ERRBIT_TIMEOUT in
 // the handle's error word, and the CTA waits (bounded) for what it has in
@@ -44,8 +55,18 @@ constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kTmemColumns = 2 * kTileC;  // two accumulators
 constexpr int kWarpC = kTileC / 2;        // columns of an epilogue warp
 constexpr int kChunk = 64;                // accumulator columns per TMEM load
-constexpr int kGroup = 2;                 // blocks whose scales are loaded together
-constexpr int kSlice = 32;                // columns of out staged at a time: 64 bytes a row
+// Row tiles that pass over the weights together.  Row tiles first, so that the
+// CTAs at work share a weight tile, but no more of them than stay in L2 for the
+// next column tile: 98,304 rows over 64 experts with a few large ones, K 7168,
+// take 2320 us this way and 2776 with all of an expert's row tiles first.
+constexpr int kRaster = 32;
+// An epilogue thread loads the scales of one block, or of two together, as long
+// ahead of their use.  Two are better where weights stream in for few rows (128
+// rows per expert, 256 experts, N 4096, K 7168: 1358 us against 1446; 375 rows,
+// K 4096: 1606 against 1626), one where the epilogue is all that counts (1500
+// rows per expert, K 4096: 1362 us against 1413).  This many rows per expert, of
+// those allocated, is where the choice turns.
+constexpr int kGroupRows = 512;
 // registers of a control and of an epilogue thread: 128 * 40 + 256 * 232 are
 // the 168 * 384 of the launch
 constexpr int kControlRegs = 40, kEpilogueRegs = 232;
@@ -117,18 +138,19 @@ __device__ __forceinline__ void count_tiles(const ExpertGemmParams &p, int *cum,
   __syncthreads();
 }
 
-// Tile i of the experts' tiles: row tiles first, so that the CTAs at work
-// share a weight tile through L2.
+// Tile i of the experts' tiles.  Whole warps: a search by one thread would be a
+// chain of shared-memory reads, each slow while the tensor cores read there.
 __device__ __forceinline__ Tile find_tile(const ExpertGemmParams &p, const int *cum, int64_t i,
                                           int tiles_c) {
-  int lo = 0, hi = p.E - 1;  // the last expert with cum[e] * tiles_c <= i
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)cum[mid] * tiles_c <= i) lo = mid; else hi = mid - 1;
-  }
+  const int lane = threadIdx.x & 31;
+  int lo = -1;  // the last expert with cum[e] * tiles_c <= i
+  for (int e = lane; e - lane < p.E; e += 32)
+    lo += __popc(__ballot_sync(0xffffffffu, e < p.E && (int64_t)cum[e] * tiles_c <= i));
   const int tr = cum[lo + 1] - cum[lo];
   const int k = (int)(i - (int64_t)cum[lo] * tiles_c);
-  const int c = k / tr, r = k - c * tr;
+  const int g = k / (kRaster * tiles_c) * kRaster;
+  const int n = min(kRaster, tr - g), u = k - g * tiles_c;
+  const int c = u / n, r = g + u - c * n;
   Tile t;
   int used, write;
   int64_t first;
@@ -174,11 +196,11 @@ struct Ring {
   }
 };
 
+template <int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, ExpertGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
-  __shared__ uint4 slices[kEpilogueWarps][32 * kSlice / 8];
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[kThreads / 32];
   // stages on 1024-byte boundaries (the swizzle's period), then cum[E + 1]
@@ -211,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kControlRegs>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------- copies ----------------
       Ring<kStages> st;
       int issued = 0;  // stages filled, counted up to kStages
@@ -219,29 +241,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
         const Tile t = find_tile(p, cum, i, tiles_c);
         if (t.rows == 0) continue;  // padding only: nothing to multiply
-        const uint32_t bytes = (uint32_t)((t.height + kTileC) * kBlockK);
-        const int w_row = t.e * p.N + t.c0;
-        for (int k = 0; k < nk; ++k) {
-          if (!wait(&bar.empty[st.slot], st.phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t *a = smem + st.slot * kStageBytes;
-          uint64_t *const full = &bar.full[st.slot];
-          mbar_arrive_expect_tx(full, bytes);
-          tma_load_2d(a + kABytes, &maps.w, k * kBlockK, w_row, full);
-          int r = 0;
-#pragma unroll
-          for (int b = kRowMaps - 1; b >= 0; --b)  // height = 16 * (sum of 2^b)
-            if (t.height & (kRowStep << b)) {
-              tma_load_2d(a + r * kBlockK, &maps.a[b], k * kBlockK, (int)t.row0 + r, full);
-              r += kRowStep << b;
+        if (lane == 0) {
+          const uint32_t bytes = (uint32_t)((t.height + kTileC) * kBlockK);
+          const int w_row = t.e * p.N + t.c0;
+          for (int k = 0; k < nk; ++k) {
+            if (!wait(&bar.empty[st.slot], st.phase ^ 1)) {
+              ok = false;
+              break;
             }
-          st.next();
-          if (issued < kStages) ++issued;
+            uint8_t *a = smem + st.slot * kStageBytes;
+            uint64_t *const full = &bar.full[st.slot];
+            mbar_arrive_expect_tx(full, bytes);
+            tma_load_2d(a + kABytes, &maps.w, k * kBlockK, w_row, full);
+            int r = 0;
+#pragma unroll
+            for (int b = kRowMaps - 1; b >= 0; --b)  // height = 16 * (sum of 2^b)
+              if (t.height & (kRowStep << b)) {
+                tma_load_2d(a + r * kBlockK, &maps.a[b], k * kBlockK, (int)t.row0 + r, full);
+                r += kRowStep << b;
+              }
+            st.next();
+            if (issued < kStages) ++issued;
+          }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         atomicOr(p.err, EP_ERRBIT_TIMEOUT);
         // copies in flight: slots below st.slot in this round, the others in
         // the round before
@@ -291,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- scaled sums and output ----------------
     setmaxnreg_inc<kEpilogueRegs>();
     const int quarter = warp & 3;           // TMEM lanes of this warp
-    const int j = (warp - 4) >> 2;          // quarter of the columns
+    const int j = (warp - 4) >> 2;          // half of the columns
     const int m = quarter * 32 + lane;      // row of the tile
     const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u + j * kWarpC;
     const int nc = (p.N + 127) / 128;
@@ -358,30 +383,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok || !work) continue;
-      // out: 64 bytes of each row at a time through shared memory, so that a
-      // store covers eight rows with four lanes each instead of 32 rows
-      uint4 *const slice = slices[warp - 4];
-      const int row_r = lane >> 2, row_c = lane & 3;  // as stored: row, 16 bytes of it
+      if (m < t.out_rows) {
+        const int col = t.c0 + j * kWarpC;
+        uint16_t *o = p.out + (t.row0 + m) * p.N + col;
 #pragma unroll
-      for (int c0 = 0; c0 < kWarpC; c0 += kSlice) {
-        __syncwarp();
+        for (int c = 0; c < kWarpC; c += 16) {
+          uint32_t v[8];
 #pragma unroll
-        for (int h = 0; h < kSlice / 8; ++h) {
-          uint32_t v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint64_t x = sum[c0 / 2 + 4 * h + q];
+          for (int q = 0; q < 8; ++q) {
+            const uint64_t x = sum[c / 2 + q];
             v[q] = mine ? cvt_bf16x2(f32x2_lo(x), f32x2_hi(x)) : 0u;
           }
-          slice[lane * 4 + (h ^ (lane >> 1 & 3))] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        __syncwarp();
-        const int col = t.c0 + j * kWarpC + c0 + row_c * 8;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int l = h * 8 + row_r, r = quarter * 32 + l;
-          if (r < t.out_rows && col < p.N)
-            st_stream_v4(p.out + (t.row0 + r) * p.N + col, slice[l * 4 + (row_c ^ (l >> 1 & 3))]);
+          if (p.out32 && col + c + 16 <= p.N) {
+            st_stream_v8(o + c, v);
+          } else {
+            if (col + c + 8 <= p.N) st_stream_v4(o + c, make_uint4(v[0], v[1], v[2], v[3]));
+            if (col + c + 16 <= p.N) st_stream_v4(o + c + 8, make_uint4(v[4], v[5], v[6], v[7]));
+          }
         }
       }
     }
@@ -432,9 +450,11 @@ cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream
   for (int i = 0; i < kRowMaps; ++i)
     ok = ok && make_map(&maps.a[i], p.a, p.rows_alloc, p.K, kRowStep << i);
   if (!ok) return cudaErrorInvalidValue;
+  const auto kernel = p.rows_alloc <= (int64_t)kGroupRows * p.E ? expert_gemm_kernel<2>
+                                                                 : expert_gemm_kernel<1>;
   const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(int) * (p.E + 1);
   int dev = 0;
-  const cudaError_t e = launch_geometry(reinterpret_cast<const void *>(expert_gemm_kernel),
+  const cudaError_t e = launch_geometry(reinterpret_cast<const void *>(kernel),
                                         kThreads, smem, &dev, nullptr);
   if (e != cudaSuccess) return e;
   const int sms = device_sm_count(dev);
@@ -442,7 +462,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream
   // at most this many row tiles hold rows (every expert's last one may be partial)
   const int64_t tiles_r = std::min<int64_t>(p.max_slots, p.E) + 2 * (p.rows_alloc / kTileR);
   const int64_t tiles = std::max<int64_t>(1, tiles_r * ((p.N + kTileC - 1) / kTileC));
-  return launch_pdl(expert_gemm_kernel, (unsigned)std::min<int64_t>(use, tiles), kThreads, smem, s,
+  return launch_pdl(kernel, (unsigned)std::min<int64_t>(use, tiles), kThreads, smem, s,
                     maps, p);
 }
 

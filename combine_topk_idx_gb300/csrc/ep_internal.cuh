@@ -246,6 +246,7 @@ struct ExpertGemmParams {
   const uint8_t *w;         // [E, N, K] e4m3
   const float *w_sf;        // [E, ceil(N / 128), K / 128]
   uint16_t *out;            // [rows_alloc, N] bf16
+  int out32;                // every row of out starts on a 32-byte boundary
   const int32_t *psum_e, *cnt_e;
   int E, N, K;
   int fixed_cap, zero_padding;
@@ -256,7 +257,7 @@ struct ExpertGemmParams {
 
 // Dynamic shared memory above which a kernel must opt in with
 // cudaFuncAttributeMaxDynamicSharedMemorySize: the 48 KB default window less
-// a margin for the kernels' static shared memory (all below 8 KB).
+// a margin for the static shared memory of the kernels that use both (below 8 KB).
 constexpr size_t kDynSmemOptIn = 40 * 1024;
 
 // Launchers (return the first CUDA error, cudaSuccess otherwise).

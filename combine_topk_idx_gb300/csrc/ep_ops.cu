@@ -325,6 +325,7 @@ ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const void *a
   p.w = static_cast<const uint8_t *>(w_fp8);
   p.w_sf = w_sf;
   p.out = static_cast<uint16_t *>(out);
+  p.out32 = ep::aligned(out, 32) && n % 16 == 0;
   p.psum_e = h->lp.psum_e;
   p.cnt_e = h->lp.cnt_e;
   p.E = c.num_experts;

@@ -34,13 +34,6 @@ __device__ __forceinline__ uint4 ld_plain_v4(const void *p) {
   return r;
 }
 
-// 8-byte read-only streaming load.
-__device__ __forceinline__ uint2 ld_stream_v2(const void *p) {
-  uint2 r;
-  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-
 // 16-byte streaming store (written once, not re-read by this kernel).
 __device__ __forceinline__ void st_stream_v4(void *p, uint4 v) {
   asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y),
@@ -48,9 +41,12 @@ __device__ __forceinline__ void st_stream_v4(void *p, uint4 v) {
                : "memory");
 }
 
-// 8-byte streaming store.
-__device__ __forceinline__ void st_stream_v2(void *p, uint2 v) {
-  asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+// 32-byte store, a whole sector from one thread.
+__device__ __forceinline__ void st_stream_v8(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+               "r"(v[7])
+               : "memory");
 }
 
 // Bulk (TMA engine) copy shared::cta -> global, tracked in the issuing thread's bulk group.

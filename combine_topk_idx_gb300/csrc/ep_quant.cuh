@@ -70,36 +70,34 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t v, uint64_t *f) {
   f[1] = f32x2_pack(c, d);
 }
 
-// Largest magnitude of N values held in pairs; NaN if any is one.
-template <int N>
-__device__ __forceinline__ float amax_of(const uint64_t *f) {
+// Largest magnitude of 16 values held in pairs; NaN if any is one.
+__device__ __forceinline__ float amax_of16(const uint64_t *f) {
   float m = 0.f;
 #pragma unroll
-  for (int q = 0; q < N / 2; ++q)
+  for (int q = 0; q < 8; ++q)
     asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f32x2_lo(f[q])), "f"(f32x2_hi(f[q])));
   return m;
 }
 
-// Quantises a 1x128 block held by 128 / N consecutive lanes, N = 8 or 16 fp32
-// values each: scale = amax / 448, bytes = e4m3(value * (1 / scale)) in fp32,
-// to nearest even, saturating.  The inputs are fp32 results with errors of
-// their own, so unlike the dispatch, whose BF16 inputs meet exact ties, a
-// product by the reciprocal (2 ulp) serves instead of the division.  Every
-// lane of the warp calls it.  An all-zero block, or one whose scale rounds to
+// Quantises a 1x128 block held by 8 consecutive lanes, 16 fp32 values each:
+// scale = amax / 448, bytes = e4m3(value * (1 / scale)) in fp32, to nearest
+// even, saturating.  The inputs are fp32 results with errors of their own, so
+// unlike the dispatch, whose BF16 inputs meet exact ties, a product by the
+// reciprocal (2 ulp) serves instead of the division.  Every lane of the warp
+// calls it.  An all-zero block, or one whose scale rounds to
 // 0, has scale 0 and zero bytes; a block holding a NaN a NaN scale and the NaN
 // code in every byte; one holding an infinity scale +inf, zeros for its finite
 // values and the NaN code for the infinite ones.
-template <int N>
-__device__ __forceinline__ void quantise_block(const uint64_t *f, uint32_t *bytes, float *scale) {
-  float amax = amax_of<N>(f);
+__device__ __forceinline__ void quantise_block16(const uint64_t *f, uint32_t *bytes, float *scale) {
+  float amax = amax_of16(f);
 #pragma unroll
-  for (int o = 1; o < 128 / N; o *= 2)
+  for (int o = 1; o < 8; o *= 2)
     amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float sc = amax * (1.0f / 448.0f);
   *scale = sc;
   if (amax < 0x1p-100f) {
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float v[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -115,14 +113,13 @@ __device__ __forceinline__ void quantise_block(const uint64_t *f, uint32_t *byte
   const float r = rcp_approx(sc);  // sc in [2^-109, 2^120), infinite or NaN
   const uint64_t r2 = f32x2_pack(r, r);
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint64_t v = f32x2_mul_rn(f[2 * i], r2), w = f32x2_mul_rn(f[2 * i + 1], r2);
     bytes[i] = cvt_e4m3x4(f32x2_lo(v), f32x2_hi(v), f32x2_lo(w), f32x2_hi(w));
   }
 }
 
-// A thread's U vectors of eight BF16 values as pairs of fp32, and U * 8 e4m3
-// bytes.
+// A thread's U vectors of eight BF16 values as pairs of fp32, and 16 e4m3 bytes.
 template <int U>
 __device__ __forceinline__ void bf16_to_f32(const uint4 *v, uint64_t *f) {
 #pragma unroll
@@ -142,12 +139,8 @@ __device__ __forceinline__ void store_bf16(void *p, const uint64_t *f) {
     st_stream_v4(static_cast<uint8_t *>(p) + 16 * i, make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
-template <int U>
-__device__ __forceinline__ void store_bytes(void *p, const uint32_t *b) {
-  if constexpr (U == 2)
-    st_stream_v4(p, make_uint4(b[0], b[1], b[2], b[3]));
-  else
-    st_stream_v2(p, make_uint2(b[0], b[1]));
+__device__ __forceinline__ void store_bytes16(void *p, const uint32_t *b) {
+  st_stream_v4(p, make_uint4(b[0], b[1], b[2], b[3]));
 }
 
 }  // namespace ep
