@@ -21,8 +21,8 @@
 //
 // Bias gradient: a sum over tokens per expert, so the slots of each chunk of
 // kChunkTokens tokens are first sorted by expert (stably, once for all columns);
-// then each warp owns 128 columns, a range of experts and a part of the chunks
-// and walks an expert's slots with its sums in registers, which meet the sums in
+// then each warp owns 256 columns, a few experts and a part of the chunks and
+// walks an expert's slots with its sums in registers, which meet the sums in
 // shared memory once per chunk and expert.  The parts are added afterwards in a
 // fixed order.  (No atomics, and no dense product with the mostly empty
 // weight matrix: there 0 * inf of one token's gradient would reach experts that
@@ -262,16 +262,16 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
   }
 }
 
-// 16,384 tokens x 6 of 64 experts, skewed, H = 4096: sorting 9 us, sums 150
-// (402 MB of gradient rows, from L2 once each), join 17.  Whole call 372 us;
-// with chunks of 128 tokens 382, with 8 experts a warp 404 and with 32 480.
-// Parts for 32 warps an SM take 362 there but 369 against 354 with 4096 tokens
-// x 8 of 256 experts, H = 7168.
+// 16,384 tokens x 6 of 64 experts, H = 4096: the whole call takes 324 us with a
+// skewed load, 195 of them the row kernel's, and 379 with an even one.  With 8
+// experts a warp and half the warps 349 and 397, with 16 experts and 128 columns
+// 377 and 450: eight columns a lane halve what is spent per slot on its entry and
+// address.  Loads in flight bound it; the gradient rows come from L2.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
-constexpr int kBiasCols = 128;     // columns of a warp, four per lane
-constexpr int kBiasExperts = 16;   // experts of a warp: 8 KB of sums, so 24 warps share an SM
-constexpr int kBiasWarps = 20;     // warps of an SM that the parts are made for
+constexpr int kBiasCols = 256;     // columns of a warp, eight per lane
+constexpr int kBiasExperts = 4;    // experts of a warp: 4 KB of sums
+constexpr int kBiasWarps = 40;     // warps of an SM that the parts are made for
 constexpr int kBiasAhead = 8;      // slots whose rows are in flight
 
 // Sorts a chunk's slots by expert: entries (token, weight) in (token, slot)
@@ -346,15 +346,15 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   }
 }
 
-// Warp (x, y, z): columns x * 128 .., experts y, y + gridDim.y, ... (popular
+// Warp (x, y, z): columns x * kBiasCols .., experts y, y + gridDim.y, ... (popular
 // experts, often neighbours, fall to different warps), chunks z, z + parts, ...
 __global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p) {
-  extern __shared__ float4 sum[];  // [experts, 32]
+  extern __shared__ float4 sum[];  // [experts, 2, 32]
   const int lane = threadIdx.x;
   const int ne = (p.E - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
-  const int col = blockIdx.x * kBiasCols + lane * 4;
+  const int col = blockIdx.x * kBiasCols + lane * 8;
   const bool in = col < p.H;
-  for (int i = 0; i < ne; ++i) sum[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < ne * 2; ++i) sum[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
   griddep_wait();
   const int chunks = (p.T + kChunkTokens - 1) / kChunkTokens;
   const uint16_t *g = p.g + (in ? col : 0);
@@ -365,32 +365,40 @@ __global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p) {
       int first = __ldg(off);
       const int end = __ldg(off + 1);
       if (first == end) continue;
-      float4 a = sum[i * 32 + lane];
+      const float4 a = sum[i * 64 + lane], b = sum[i * 64 + 32 + lane];
+      uint64_t s[4] = {f32x2_pack(a.x, a.y), f32x2_pack(a.z, a.w), f32x2_pack(b.x, b.y),
+                       f32x2_pack(b.z, b.w)};
       for (; first < end; first += kBiasAhead) {
-        uint2 v[kBiasAhead];
+        uint4 v[kBiasAhead];
         float w[kBiasAhead];
 #pragma unroll
         for (int q = 0; q < kBiasAhead; ++q) {
           const int2 x = first + q < end ? __ldg(ent + first + q) : make_int2(-1, 0);
           w[q] = __int_as_float(x.y);
-          v[q] = x.x >= 0 ? __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)x.x * p.H))
-                          : make_uint2(0, 0);
+          v[q] = x.x >= 0 ? ld_cached_v4(g + (int64_t)x.x * p.H)
+                          : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int q = 0; q < kBiasAhead; ++q) {
-          a.x = fmaf(w[q], bf16_lo(v[q].x), a.x);
-          a.y = fmaf(w[q], bf16_hi(v[q].x), a.y);
-          a.z = fmaf(w[q], bf16_lo(v[q].y), a.z);
-          a.w = fmaf(w[q], bf16_hi(v[q].y), a.w);
+          const uint64_t w2 = f32x2_pack(w[q], w[q]);
+          uint64_t f[4];
+          bf16_to_f32<1>(&v[q], f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[k] = f32x2_fma_rn(w2, f[k], s[k]);
         }
       }
-      sum[i * 32 + lane] = a;
+      sum[i * 64 + lane] = make_float4(f32x2_lo(s[0]), f32x2_hi(s[0]), f32x2_lo(s[1]), f32x2_hi(s[1]));
+      sum[i * 64 + 32 + lane] =
+          make_float4(f32x2_lo(s[2]), f32x2_hi(s[2]), f32x2_lo(s[3]), f32x2_hi(s[3]));
     }
   }
   if (!in) return;
   float *o = p.part + ((int64_t)blockIdx.z * p.E + blockIdx.y) * p.H + col;
-  for (int i = 0; i < ne; ++i)
-    *reinterpret_cast<float4 *>(o + (int64_t)i * gridDim.y * p.H) = sum[i * 32 + lane];
+  for (int i = 0; i < ne; ++i) {
+    float4 *const r = reinterpret_cast<float4 *>(o + (int64_t)i * gridDim.y * p.H);
+    r[0] = sum[i * 64 + lane];
+    r[1] = sum[i * 64 + 32 + lane];
+  }
 }
 
 int bias_experts(int E) { return std::min(E, kBiasExperts); }

@@ -18,7 +18,9 @@
 // 4096 tokens x 8 experts, F = 2048, FP8 out and checkpoint kept: 100 us, 4.7
 // TB/s of the rows in use, between memory (71 us at a copy's rate) and the issue
 // of its instructions (59 % of the cycles).  8192 rows without checkpoint: 17.2
-// us, 4.9 TB/s.  The gradient: see its kernel.
+// us, 4.9 TB/s.  Units dealt to the threads of the whole grid, without tiles and
+// their barriers, take 112 us for the first, and with copies into shared memory
+// three units ahead 133.  The gradient: see its kernel.
 #include <algorithm>
 
 #include "ep_internal.cuh"
@@ -104,6 +106,14 @@ struct Unit {
   }
 };
 
+// U vectors of zeros.
+template <int U>
+__device__ __forceinline__ void store_zeros(void *p) {
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    st_stream_v4(static_cast<uint8_t *>(p) + 16 * i, make_uint4(0, 0, 0, 0));
+}
+
 template <int U>
 __global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int tile_rows) {
   constexpr int N = 8 * U;
@@ -132,6 +142,16 @@ __global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int
       ahead.load(p, rows[par], k, id + kThreads < total);
       const int j = v >> 3;
       const bool first = (v & 7) == 0;
+      if (!__any_sync(0xffffffffu, use)) {  // padding of the whole warp: zeros, if anything
+        if (t.row >= 0) {
+          if (p.act != nullptr) store_zeros<U>(p.act + t.row * p.F + c);
+          if (U == 2 && p.q != nullptr) {
+            store_zeros<1>(p.q + t.row * p.F + c);
+            if (first) p.sf[sf_at(p.sfl, t.row, j)] = 0.f;
+          }
+        }
+        continue;
+      }
       if constexpr (U == 2) {
         if (p.ckpt != nullptr) {  // one at a time: fewer values live
           uint8_t *o = p.ckpt + t.row * 2 * p.F + c;
@@ -173,9 +193,12 @@ __global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int
   }
 }
 
-// 4096 tokens x 8 experts, F = 2048, FP8 in and out: 113 us, 3.6 TB/s.  Bound
-// by instruction issue (68 % of the cycles), not by loads: loading a unit ahead
-// as above costs registers, and so resident warps (114 -> 122 us).
+// 4096 tokens x 8 experts, F = 2048, FP8 in and out: 107 us, 3.8 TB/s of the rows
+// in use.  Between the issue of its instructions (two thirds of the cycles) and
+// its loads: loading a unit ahead as above costs registers, and so resident
+// warps (114 -> 122 us); so do whole rows to a warp, without the tile's barrier,
+// in as many registers (112 us); copies into shared memory three units ahead
+// cost more than the wait they save (129 us).
 __global__ void __launch_bounds__(kThreads)
     swiglu_backward_kernel(SwigluBackwardParams p, int tile_rows) {
   constexpr int U = 2, N = 8 * U;
@@ -203,6 +226,26 @@ __global__ void __launch_bounds__(kThreads)
       const bool use = t.row >= 0 && !t.pad;
       const int c = k.v * N, j = k.v >> 3;
       const bool first = (k.v & 7) == 0;
+      if (!__any_sync(0xffffffffu, use)) {  // without this 113 us, a third of the rows padding
+        if (id < total && first && p.gw != nullptr) sum[k.i * nb + j] = 0.f;
+        if (t.row >= 0) {
+          if (p.gh != nullptr) {
+            uint16_t *o = p.gh + t.row * 2 * p.F + c;
+            store_zeros<U>(o);
+            store_zeros<U>(o + p.F);
+          }
+          if (p.q != nullptr) {
+            uint8_t *o = p.q + t.row * 2 * p.F + c;
+            store_zeros<1>(o);
+            store_zeros<1>(o + p.F);
+            if (first) {
+              p.sf[sf_at(p.sfl, t.row, j)] = 0.f;
+              p.sf[sf_at(p.sfl, t.row, j + nb)] = 0.f;
+            }
+          }
+        }
+        continue;
+      }
       const uint8_t *cp = p.ckpt + t.row * 2 * p.F + c;
       const float *cs = p.ckpt_sf + t.row * (2 * nb) + j;
       const uint16_t *ga = p.ga + t.row * p.F + c;
