@@ -15,8 +15,8 @@
 // token: the bytes are those of g (with the sign of the weight), the scale is
 // the scale of g times |w|, so K rows cost one quantisation.  gy's alignment
 // padding is zeroed by the same CTAs afterwards.  Memory bounds it: 4096 tokens
-// x 8 experts, H = 7168, FP8 rows, 165 us for 771 MB and 77 MB of zeroed
-// padding, 5.1 TB/s; each row of y waits for its token's slots and is then
+// x 8 experts, H = 7168, FP8 rows, 164 us for 771 MB and 117 MB of zeroed
+// padding, 5.4 TB/s; each row of y waits for its token's slots and is then
 // read in two pieces a thread, so the loads in flight limit it.
 //
 // Bias gradient: a sum over tokens per expert, so the slots of each chunk of
@@ -263,10 +263,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
 }
 
 // 16,384 tokens x 6 of 64 experts, H = 4096: the whole call takes 324 us with a
-// skewed load, 195 of them the row kernel's, and 379 with an even one.  With 8
-// experts a warp and half the warps 349 and 397, with 16 experts and 128 columns
-// 377 and 450: eight columns a lane halve what is spent per slot on its entry and
-// address.  Loads in flight bound it; the gradient rows come from L2.
+// skewed load, 200 of them the row kernel's and 104 this one's, and 379 with an
+// even one.  With 8 experts a warp and half the warps 349 and 397, with 16 experts
+// and 128 columns 377 and 450: eight columns a lane halve what is spent per slot
+// on its entry and address.  Loads in flight bound it; the gradient rows come
+// from L2.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
 constexpr int kBiasCols = 256;     // columns of a warp, eight per lane

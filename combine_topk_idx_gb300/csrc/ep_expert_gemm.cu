@@ -19,17 +19,19 @@
 // rows in TMEM lanes a block's scale is one register per thread; with the
 // columns there it would be one per accumulator column, and fetching those from
 // shared memory takes longer than the products (2310 us against 1569 in the
-// third case below).  A row leaves as 32-byte stores straight from registers:
+// last case below).  A row leaves as 32-byte stores straight from registers:
 // through shared memory, which the tensor cores keep busy, they took 3 % more.
 //
 // What bounds it.  Few rows, the weights' bytes: 8 rows, each its expert, N 4096,
-// K 7168, 40.5 us for 235 MB, 5.8 TB/s of 6.7 that a copy reaches.  128 rows per
-// expert, 256 experts: 1374 us for 8.0 GB, 5.8 TB/s.  Many rows, the scaled sums:
-// 96,300 rows over 64 experts, N = K = 4096, 1451 us, 2.2 PFLOP/s.  The products
-// of a block would take 512 cycles; 32,768 sums read from TMEM, scaled and added
-// by eight warps, with two barriers, take about twice that.  Pairs of CTAs
-// sharing the operands (1480 us) did not help, nor does any layout in which an
-// epilogue thread spills (20 to 60 % slower): hence 232 registers for it.
+// K 7168, 41 us for 235 MB, 5.7 TB/s of 6.7 that a copy reaches.  128 rows per
+// expert, 256 experts: 1374 to 1455 us on three GPUs for 8.0 GB, 5.5 to 5.8 TB/s.
+// Many rows, the scaled sums: 96,300 rows over 64 experts, N = K = 4096, 1451 to
+// 1494 us, 2.2 PFLOP/s, tensor cores busy 53 % of the time.  The products of a
+// block take 512 cycles; 32,768 sums read from TMEM, scaled and added by eight
+// warps, with two barriers, take 730 by themselves and about 970 beside them.
+// Pairs of CTAs sharing the operands (1480 us where one CTA a tile took 1486) did
+// not help, nor does any layout in which an epilogue thread spills (20 to 60 %
+// slower): hence 232 registers for it.
 //
 // Every mbarrier wait is bounded: one that gives up sets EP_ERRBIT_TIMEOUT in
 // the handle's error word, and the CTA waits (bounded) for what it has in

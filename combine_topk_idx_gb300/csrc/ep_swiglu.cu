@@ -17,10 +17,10 @@
 //
 // 4096 tokens x 8 experts, F = 2048, FP8 out and checkpoint kept: 100 us, 4.7
 // TB/s of the rows in use, between memory (71 us at a copy's rate) and the issue
-// of its instructions (59 % of the cycles).  8192 rows without checkpoint: 17.2
+// of its instructions (66 % of the cycles).  8192 rows without checkpoint: 17.3
 // us, 4.9 TB/s.  Units dealt to the threads of the whole grid, without tiles and
 // their barriers, take 112 us for the first, and with copies into shared memory
-// three units ahead 133.  The gradient: see its kernel.
+// three units ahead 133.  The gradient's figures are at its kernel.
 #include <algorithm>
 
 #include "ep_internal.cuh"
@@ -194,11 +194,11 @@ __global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int
 }
 
 // 4096 tokens x 8 experts, F = 2048, FP8 in and out: 107 us, 3.8 TB/s of the rows
-// in use.  Between the issue of its instructions (two thirds of the cycles) and
-// its loads: loading a unit ahead as above costs registers, and so resident
-// warps (114 -> 122 us); so do whole rows to a warp, without the tile's barrier,
-// in as many registers (112 us); copies into shared memory three units ahead
-// cost more than the wait they save (129 us).
+// in use.  Between the issue of its instructions (59 % of the cycles) and its
+// loads: loading a unit ahead as above costs registers, and so resident warps
+// (114 -> 122 us); whole rows to a warp, without the tile's barrier, gain nothing
+// (108 us); copies into shared memory three units ahead cost more than the wait
+// that they save (129 us).
 __global__ void __launch_bounds__(kThreads)
     swiglu_backward_kernel(SwigluBackwardParams p, int tile_rows) {
   constexpr int U = 2, N = 8 * U;
