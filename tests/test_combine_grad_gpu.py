@@ -38,6 +38,9 @@ CASES = {
     "no_tokens": (0, 4, 8, 2, 128, 4, 4, True, True, True, False, False, 0.0, False),
     "many_experts": (33, 4, 600, 4, 128, 9, 1, True, True, True, False, False, 0.0, False),
     "widest": (6, 2, 8, 2, 32768, 3, 4, True, True, True, True, False, 0.0, False),
+    "wide": (9, 4, 8, 2, 12288, 5, 8, True, True, True, True, False, 0.0, False),
+    "odd_wide": (7, 4, 10, 2, 8200, 4, 1, False, False, True, False, False, 0.1, False),
+    "many_chunks": (1100, 4, 13, 13, 264, 90, 1, True, True, True, False, False, 0.1, False),
     "odd_width": (70, 4, 16, 4, 1000, 20, 1, False, False, True, False, False, 0.1, False),
     "narrow": (513, 2, 4, 1, 8, 513, 8, True, True, True, False, False, 0.1, False),
 }

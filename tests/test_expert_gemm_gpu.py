@@ -99,6 +99,39 @@ def test_against_definition(ep, name):
     h.free()
 
 
+@pytest.mark.parametrize("T,E,n,k", [(4500, 2, 520, 128), (9000, 3, 264, 256), (8300, 1, 768, 128)])
+def test_many_row_tiles(ep, T, E, n, k):
+    """More row tiles per expert than pass over the weights together, several column tiles."""
+    K = min(2, E)
+    cfg = ep.make_config(T, K, E, 1, 128, T, 1, do_expand=True, do_zero_padding=True)
+    h = ep.ep_layout(cfg, routing(T, K, E, 21).cuda())
+    check(ep, h, n, k)
+    h.free()
+
+
+@pytest.mark.parametrize("n", [256, 264])
+def test_out_alignment(ep, n):
+    """Rows of out that start on 32 and on 16 bytes hold the same."""
+    cfg = ep.make_config(90, 2, 4, 2, 128, 45, 16, do_expand=True, do_zero_padding=True)
+    h = ep.ep_layout(cfg, routing(90, 2, 4, 2, 0.1).cuda())
+    q, sf = activations(ep, h, 256, 7)
+    w, wsf = weights(4, n, 256, 8)
+    rows = h.rows_alloc
+    flat = torch.full((rows * n + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert flat.data_ptr() % 32 == 0
+    outs = [flat[o:o + rows * n].view(rows, n) for o in (0, 8, 16)]
+    got = []
+    for o in outs:
+        flat.fill_(7.0)
+        ep.ep_expert_gemm(h, q, sf, w, wsf, out=o)
+        torch.cuda.synchronize()
+        got.append(o.clone())
+        assert (flat[:o.storage_offset()] == 7).all()
+        assert (flat[o.storage_offset() + rows * n:] == 7).all()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    h.free()
+
+
 def test_repeated_experts_overflow(ep):
     """Rows dropped by an overflowing upper bound are not touched."""
     cfg = ep.make_config(2, 4, 2, 2, 128, 1, 1, do_expand=True, do_zero_padding=True,

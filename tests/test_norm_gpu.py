@@ -62,6 +62,31 @@ def test_forward_bf16_any_width(ep, H):
     check_forward(ep, xs[:, :H], rs[:, 8:H + 8], gamma, out)
 
 
+@pytest.mark.parametrize("H", [16, 496, 504, 512, 520, 528, 784, 8176])
+@pytest.mark.parametrize("T", [1, 5, 129])
+def test_forward_bf16_rows_of_a_warp_or_more(ep, T, H):
+    """Widths about the one up to which a row is a warp's, and partial last warps."""
+    g = torch.Generator().manual_seed(T + 3 * H)
+    x, r = normal(g, T, H), normal(g, T, H)
+    out = ep.alloc_rmsnorm(x, residual=True, bf16=True, fp8=False, rstd=True)
+    check_forward(ep, x, r, normal(g, H), out)
+
+
+@pytest.mark.parametrize("T", [0, 1, 3, 4, 7])
+@pytest.mark.parametrize("H", [128, 256])
+def test_allocated_scales(ep, T, H):
+    """The scales' shapes and strides of few rows, taken by the norm as they are."""
+    x = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    gamma = torch.ones(H, device="cuda")
+    for col in (False, True):
+        o = ep.alloc_rmsnorm(x, fp8=True, col_major_sf=col)
+        assert o["y_sf"].shape == (T, H // 128)
+        assert not col or H == 128 or o["y_sf"].stride(1) % 4 == 0
+        ep.ep_rmsnorm(x, gamma, EPS, **o)
+        torch.cuda.synchronize()
+        assert torch.allclose(o["y_sf"], torch.full_like(o["y_sf"], 1 / 448), rtol=1e-5)
+
+
 def test_forward_in_place_residual(ep):
     g = torch.Generator().manual_seed(2)
     x, r = normal(g, 40, 2048), normal(g, 40, 2048)
