@@ -27,8 +27,9 @@
 // expert, 256 experts: 1374 to 1455 us on three GPUs for 8.0 GB, 5.5 to 5.8 TB/s.
 // Many rows, the scaled sums: 96,300 rows over 64 experts, N = K = 4096, 1451 to
 // 1494 us, 2.2 PFLOP/s, tensor cores busy 53 % of the time.  The products of a
-// block take 512 cycles; 32,768 sums read from TMEM, scaled and added by eight
-// warps, with two barriers, take 730 by themselves and about 970 beside them.
+// block take 512 cycles, its operands' way into shared memory and out 768, the
+// scaled sums 730 by themselves; with the barriers over two accumulators, all that
+// TMEM holds, a block takes about 970.
 // Pairs of CTAs sharing the operands (1480 us where one CTA a tile took 1486) did
 // not help, nor does any layout in which an epilogue thread spills (20 to 60 %
 // slower): hence 232 registers for it.
