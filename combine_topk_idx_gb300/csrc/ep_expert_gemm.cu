@@ -29,10 +29,9 @@
 // 1494 us, 2.2 PFLOP/s, tensor cores busy 53 % of the time.  The products of a
 // block take 512 cycles, its operands' way into shared memory and out 768, the
 // scaled sums 730 by themselves; with the barriers over two accumulators, all that
-// TMEM holds, a block takes about 970.
-// Pairs of CTAs sharing the operands (1480 us where one CTA a tile took 1486) did
-// not help, nor does any layout in which an epilogue thread spills (20 to 60 %
-// slower): hence 232 registers for it.
+// TMEM holds, a block takes about 970.  Pairs of CTAs sharing the operands (1480
+// us where one CTA a tile took 1486) did not help, nor does any layout in which an
+// epilogue thread spills (20 to 60 % slower): hence 232 registers for it.
 //
 // Every mbarrier wait is bounded: one that gives up sets EP_ERRBIT_TIMEOUT in
 // the handle's error word, and the CTA waits (bounded) for what it has in
