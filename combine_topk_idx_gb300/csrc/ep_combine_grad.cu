@@ -262,14 +262,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
   }
 }
 
-// 16,384 tokens x 6 of 64 experts, H = 4096: the whole call takes 324 us with a
-// skewed load, 200 of them the row kernel's and 104 this one's, and 379 with an
-// even one.  With 8 experts a warp and half the warps 349 and 397, with 16 experts
-// and 128 columns 377 and 450: eight columns a lane halve what is spent per slot
+// 16,384 tokens x 6 of 64 experts, H = 4096, skewed: the whole call takes 310 us,
+// 197 of them the row kernel's, 10 the sort's, 103 the sums' and 8 the joining of
+// their parts.  With 8 experts a warp and half the warps 25 us more, with 16
+// experts and 128 columns 53: eight columns a lane halve what is spent per slot
 // on its entry and address.  Loads in flight bound it; the gradient rows come
 // from L2.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
+constexpr int kSortAhead = 8;      // steps of 32 slots whose loads are in flight
 constexpr int kBiasCols = 256;     // columns of a warp, eight per lane
 constexpr int kBiasExperts = 4;    // experts of a warp: 4 KB of sums
 constexpr int kBiasWarps = 40;     // warps of an SM that the parts are made for
@@ -292,11 +293,18 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   auto expert = [&](int64_t s) {
     return s < s1 && __ldg(p.dst + s) >= 0 ? __ldg(p.topk32 + s) : -1;
   };
-  for (int64_t s = s0 + lane; s - lane < s1; s += 32) {
-    const int e = expert(s);
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-    __syncwarp();
+  // kSortAhead steps' loads at once: 16,384 tokens x 6 take 10 us, and 16 with the
+  // loads one after the other
+  for (int64_t s = s0 + lane; s - lane < s1; s += 32 * kSortAhead) {
+    int ex[kSortAhead];
+#pragma unroll
+    for (int q = 0; q < kSortAhead; ++q) ex[q] = expert(s + 32 * q);
+#pragma unroll
+    for (int q = 0; q < kSortAhead; ++q) {
+      const unsigned peers = __match_any_sync(0xffffffffu, ex[q]);
+      if (ex[q] >= 0 && lane == __ffs(peers) - 1) mine[ex[q]] += __popc(peers);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // counts -> first entry of each (expert, warp)
@@ -333,17 +341,26 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   }
   if (threadIdx.x == 0) off[p.E] = base;
   int2 *ent = p.ent + (int64_t)blockIdx.x * kChunkTokens * p.K;
-  for (int64_t s = s0 + lane; s - lane < s1; s += 32) {
-    const int e = expert(s);
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
-    const int at = e >= 0 ? mine[e] : 0;
-    __syncwarp();
-    if (e >= 0) {
-      ent[at + __popc(peers & lanemask_lt())] =
-          make_int2((int)(s / p.K), __float_as_int(__ldg(p.topk_w + s)));
-      if (lane == __ffs(peers) - 1) mine[e] = at + __popc(peers);
+  for (int64_t s = s0 + lane; s - lane < s1; s += 32 * kSortAhead) {
+    int ex[kSortAhead];
+    float w[kSortAhead];
+#pragma unroll
+    for (int q = 0; q < kSortAhead; ++q) {
+      ex[q] = expert(s + 32 * q);
+      w[q] = s + 32 * q < s1 ? __ldg(p.topk_w + s + 32 * q) : 0.f;
     }
-    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kSortAhead; ++q) {
+      const unsigned peers = __match_any_sync(0xffffffffu, ex[q]);
+      const int at = ex[q] >= 0 ? mine[ex[q]] : 0;
+      __syncwarp();
+      if (ex[q] >= 0) {
+        ent[at + __popc(peers & lanemask_lt())] =
+            make_int2((int)((s + 32 * q) / p.K), __float_as_int(w[q]));
+        if (lane == __ffs(peers) - 1) mine[ex[q]] = at + __popc(peers);
+      }
+      __syncwarp();
+    }
   }
 }
 

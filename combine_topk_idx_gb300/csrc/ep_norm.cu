@@ -12,7 +12,7 @@
 // registers between the sum and the result, as 16-byte vectors of eight
 // elements.  What bounds them is memory.  4096 rows of 7168, residual in and
 // out, FP8 out: 33.7 us for 206 MB, 6.1 TB/s, where a copy reaches 6.7.
-// Gradient of 16,384 rows of 4096 with a residual's: 94 us for 537 MB, 5.7 TB/s.
+// Gradient of 16,384 rows of 4096 with a residual's: 92 us for 537 MB, 5.8 TB/s.
 // One row of 7168: 6.5 us in a CUDA graph, most of it the launch.
 #include <algorithm>
 
@@ -24,6 +24,7 @@ namespace ep {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kWideSum = 65536;  // columns
 constexpr int kWarpRow = 512;  // elements of a row that a warp takes, at most
 
 // Sum over the threads of a row: a warp, or the whole CTA (`red` then holds
@@ -216,23 +217,37 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(NormBackwardParams 
   }
 }
 
-// out[c] = sum over i < parts of part[i, c], in a fixed order: 8 threads of a
-// column sum every eighth row, then one adds the eight.
-constexpr int kSumCols = 32, kSumSplit = 8;
-__global__ void __launch_bounds__(kSumCols *kSumSplit)
+// out[c] = sum over i < parts of part[i, c], in a fixed order: SPLIT threads of a
+// column sum every SPLIT-th row, then one adds their sums.  A thread has V
+// columns, V * 4 bytes of each row.
+template <int V, int SPLIT>
+__global__ void __launch_bounds__(32 * SPLIT)
     column_sum_kernel(const float *part, int parts, int64_t n, float *out) {
-  __shared__ float s[kSumSplit][kSumCols];
-  const int c = threadIdx.x & (kSumCols - 1), k = threadIdx.x / kSumCols;
-  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+  __shared__ float s[SPLIT][32 * V];
+  const int c = (threadIdx.x & 31) * V, k = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * (32 * V) + c;
   griddep_wait();
-  float v = 0.f;
-  if (col < n)
-    for (int i = k; i < parts; i += kSumSplit) v += part[(int64_t)i * n + col];
-  s[k][c] = v;
+  float v[V] = {};
+  if (col < n) {
+#pragma unroll 4
+    for (int i = k; i < parts; i += SPLIT) {
+      const float *a = part + (int64_t)i * n + col;
+      if constexpr (V == 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(a));
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      } else {
+        v[0] += __ldg(a);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) s[k][c + j] = v[j];
   __syncthreads();
-  if (k == 0 && col < n) {
-    for (int i = 1; i < kSumSplit; ++i) v += s[i][c];
-    out[col] = v;
+  const int o = threadIdx.x;
+  if (o < 32 * V && (int64_t)blockIdx.x * (32 * V) + o < n) {
+    float t = s[0][o];
+    for (int i = 1; i < SPLIT; ++i) t += s[i][o];
+    out[(int64_t)blockIdx.x * (32 * V) + o] = t;
   }
 }
 
@@ -256,8 +271,13 @@ auto backward_kernel(int threads) {
 
 cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
                               cudaStream_t s) {
-  return launch_pdl(column_sum_kernel, (unsigned)((n + kSumCols - 1) / kSumCols),
-                    kSumCols * kSumSplit, 0, s, part, parts, n, out);
+  // Few columns: 32 threads of each; many: 16 bytes a thread, 8 of a column.  608
+  // rows of 4096 take 6.7 us one way and 10 the other, 24 of 262,144 33 and 7.8.
+  if (n >= kWideSum)
+    return launch_pdl(column_sum_kernel<4, 8>, (unsigned)((n + 127) / 128), 32 * 8, 0, s, part,
+                      parts, n, out);
+  return launch_pdl(column_sum_kernel<1, 32>, (unsigned)((n + 31) / 32), 32 * 32, 0, s, part, parts,
+                    n, out);
 }
 
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
