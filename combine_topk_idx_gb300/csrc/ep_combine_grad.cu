@@ -262,18 +262,19 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
   }
 }
 
-// 16,384 tokens x 6 of 64 experts, H = 4096, skewed: the whole call takes 310 us,
-// 197 of them the row kernel's, 10 the sort's, 103 the sums' and 8 the joining of
-// their parts.  With 8 experts a warp and half the warps 25 us more, with 16
-// experts and 128 columns 53: eight columns a lane halve what is spent per slot
-// on its entry and address.  Loads in flight bound it; the gradient rows come
-// from L2.
+// 16,384 tokens x 6 of 64 experts, H = 4096, skewed: the whole call takes 294 us,
+// 197 of them the row kernel's and 10 the sort's.  With 8 experts a warp and half
+// as many parts 25 us more, with 16 experts and 128 columns 53: eight columns a
+// lane halve what is spent per slot on its entry and address.  Many small parts
+// even out a skewed load (40 warps' parts 14 us more, 27 warps' 35) and cost an
+// even one 1 %; their sums take 50 MB at most.  Loads in flight bound it; the
+// gradient rows come from L2.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
 constexpr int kSortAhead = 8;      // steps of 32 slots whose loads are in flight
 constexpr int kBiasCols = 256;     // columns of a warp, eight per lane
 constexpr int kBiasExperts = 4;    // experts of a warp: 4 KB of sums
-constexpr int kBiasWarps = 40;     // warps of an SM that the parts are made for
+constexpr int kBiasWarps = 80;     // warps of an SM that the parts are made for
 constexpr int kBiasAhead = 8;      // slots whose rows are in flight
 
 // Sorts a chunk's slots by expert: entries (token, weight) in (token, slot)
