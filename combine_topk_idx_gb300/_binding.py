@@ -254,6 +254,7 @@ class Handle:
         self.status = status
         self.T, self.K, self.E, self.R = cfg.num_tokens, cfg.num_topk, cfg.num_experts, cfg.num_ranks
         self.H = cfg.hidden
+        self.rows_alloc = int(info.rows_alloc)
         self.sf_layouts = {}  # of sf_layout, by row length
 
     @property
@@ -261,10 +262,6 @@ class Handle:
         if not self._ptr:
             raise RuntimeError("handle already freed")
         return self._ptr
-
-    @property
-    def rows_alloc(self) -> int:
-        return int(self.info.rows_alloc)
 
     def tensor(self, name: str) -> torch.Tensor:
         """Zero-copy torch view of one of the handle's device arrays."""

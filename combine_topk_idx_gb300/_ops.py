@@ -79,7 +79,7 @@ class _Call:
 def sf_layout(handle: Handle, n: int):
     """(numel, token_stride, hidden_stride, expert_stride) of the fp32 scales of
     rows of ``n`` elements in the handle's layout (``ep_sf_layout``)."""
-    ptr = ctypes.c_void_p(handle.ptr)
+    ptr = handle.ptr
     known = handle.sf_layouts.get(n)  # fixed for the handle's life
     if known is None:
         v = [ctypes.c_int64() for _ in range(4)]
@@ -191,7 +191,7 @@ def _rows(handle: Optional[Handle], t: torch.Tensor, what: str):
         raise ValueError(f"{what} must have two dimensions")
     if handle is None:
         return None, t.shape[0]
-    return ctypes.c_void_p(handle.ptr), handle.rows_alloc
+    return handle.ptr, handle.rows_alloc
 
 
 def _sf_numel(handle: Optional[Handle], rows: int, n: int):
@@ -253,7 +253,7 @@ def ep_combine_weighted_backward(handle: Handle, grad_out: torch.Tensor,
     (``ep_combine_weighted_backward``)."""
     c = _Call("ep_combine_weighted_backward", stream)
     T, K, E, H, rows = handle.T, handle.K, handle.E, handle.H, handle.rows_alloc
-    c(ctypes.c_void_p(handle.ptr), c.ptr(grad_out, "grad_out", _BF16, (T, H)),
+    c(handle.ptr, c.ptr(grad_out, "grad_out", _BF16, (T, H)),
       c.ptr(y, "y", _BF16, (rows, H)), c.ptr(topk_weights, "topk_weights", _F32, (T, K)),
       c.ptr(expert_bias, "expert_bias", _BF16, (E, H)), c.ptr(grad_y, "grad_y", _BF16, (rows, H)),
       c.ptr(grad_y_fp8, "grad_y_fp8", _FP8, (rows, H)),
@@ -281,7 +281,7 @@ def ep_expert_gemm(handle: Handle, a: torch.Tensor, a_sf: torch.Tensor, w: torch
     rows = handle.rows_alloc
     if out is None:
         out = c.empty(rows, n, dtype=torch.bfloat16)
-    c(ctypes.c_void_p(handle.ptr), n, k, c.ptr(a, "a", _FP8, (rows, k)),
+    c(handle.ptr, n, k, c.ptr(a, "a", _FP8, (rows, k)),
       c.ptr(a_sf, "a_sf", _F32, (sf_layout(handle, k)[0],)), c.ptr(w, "w", _FP8),
       c.ptr(w_sf, "w_sf", _F32, (E, -(-n // 128), k // 128)),
       c.ptr(out, "out", _BF16, (rows, n)))
