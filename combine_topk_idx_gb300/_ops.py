@@ -38,7 +38,9 @@ class _Call:
         else:
             self.raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
             if self.raw != current:
-                self.other = torch.cuda.ExternalStream(self.raw)
+                # the default stream's handle is 0, of which ExternalStream makes a new stream
+                self.other = (torch.cuda.ExternalStream(self.raw) if self.raw
+                              else torch.cuda.default_stream(self.device))
 
     def ptr(self, t: Optional[torch.Tensor], what: str, dtypes: tuple, shape=None, strided=False):
         """Pointer of an optional tensor of the expected type and shape."""
