@@ -151,7 +151,8 @@ __device__ __forceinline__ void write_row(const CombineGradParams &p, const Shar
 #pragma unroll
           for (int k = 0; k < 2 * U; ++k) b[k] = (q.b[i][k] ^ flip) & keep;
           store_bytes16(p.q + at + v * N, b);
-          if ((v & 7) == 0) p.sf[sf0 + (v >> 3) * p.sfl.hs] = fabsf(w) * q.s[i];
+          if ((v & 7) == 0)  // weight 0: a scale of 0, whatever the gradient holds
+            p.sf[sf0 + (v >> 3) * p.sfl.hs] = w != 0.f ? fabsf(w) * q.s[i] : 0.f;
         }
       }
     }

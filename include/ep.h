@@ -454,7 +454,8 @@ EP_API ep_status ep_swiglu_backward(const ep_handle *h, int64_t rows, int32_t ff
  *   grad_y_fp8 e4m3 [rows_alloc, H] with grad_y_sf (ep_sf_layout of hidden, a
  *     multiple of 128): the same rows in 8 bits -- the bytes are grad_out
  *     quantised once per token, negated for a negative weight, the scale is the
- *     token's scale times |weight| (weight 0: zero bytes and scales);
+ *     token's scale times |weight| (weight 0: zero bytes and scales, also where
+ *     grad_out is infinite or NaN, which grad_y has as 0 * grad_out);
  *   grad_topk_weights fp32 [T, K]: <grad_out[t], y[row] + expert_bias[e]>, 0 for
  *     a slot without a row;
  *   grad_expert_bias fp32 [E, H]: sum over the slots routed to e of weight *
