@@ -281,16 +281,14 @@ constexpr int kBiasAhead = 8;      // slots whose rows are in flight
 // Sorts a chunk's slots by expert: entries (token, weight) in (token, slot)
 // order within an expert, off[e] the first entry of expert e.  Each warp takes
 // consecutive tokens, 32 slots at a step.
-__global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradParams p) {
-  extern __shared__ int cnt[];  // [kSortWarps, E]
-  __shared__ int warp_sum[kSortWarps];
+__device__ __forceinline__ void sort_chunk(const CombineGradParams &p, int chunk, int *cnt,
+                                           int *warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nt = kSortWarps * 32;
   int *const mine = cnt + warp * p.E;
   for (int i = threadIdx.x; i < kSortWarps * p.E; i += nt) cnt[i] = 0;
-  griddep_wait();
   __syncthreads();
   constexpr int per = kChunkTokens / kSortWarps;
-  const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens + warp * per;
+  const int64_t t0 = (int64_t)chunk * kChunkTokens + warp * per;
   const int64_t s0 = min(t0, (int64_t)p.T) * p.K, s1 = min(t0 + per, (int64_t)p.T) * p.K;
   auto expert = [&](int64_t s) {
     return s < s1 && __ldg(p.dst + s) >= 0 ? __ldg(p.topk32 + s) : -1;
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   }
   __syncthreads();
   // counts -> first entry of each (expert, warp)
-  int32_t *off = p.off + (int64_t)blockIdx.x * (p.E + 1);
+  int32_t *off = p.off + (int64_t)chunk * (p.E + 1);
   int base = 0;
   for (int e0 = 0; e0 < p.E; e0 += nt) {
     const int e = e0 + threadIdx.x;
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
     __syncthreads();
   }
   if (threadIdx.x == 0) off[p.E] = base;
-  int2 *ent = p.ent + (int64_t)blockIdx.x * kChunkTokens * p.K;
+  int2 *ent = p.ent + (int64_t)chunk * kChunkTokens * p.K;
   for (int64_t s = s0 + lane; s - lane < s1; s += 32 * kSortAhead) {
     int ex[kSortAhead];
     float w[kSortAhead];
@@ -366,22 +364,38 @@ __global__ void __launch_bounds__(kSortWarps * 32) bias_sort_kernel(CombineGradP
   }
 }
 
-// Warp (x, y, z): columns x * kBiasCols .., experts y, y + gridDim.y, ... (popular
+// A CTA sorts one chunk, or with CAPPED the chunks in turn.
+template <bool CAPPED>
+__global__ void __launch_bounds__(kSortWarps * 32)
+    bias_sort_kernel(CombineGradParams p, int chunks) {
+  extern __shared__ int cnt[];  // [kSortWarps, E]
+  __shared__ int warp_sum[kSortWarps];
+  griddep_wait();
+  if constexpr (!CAPPED) {
+    sort_chunk(p, blockIdx.x, cnt, warp_sum);
+  } else {
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+      sort_chunk(p, c, cnt, warp_sum);
+      __syncthreads();  // the next chunk clears the counts
+    }
+  }
+}
+
+// A warp's share (x, y, z): columns x * kBiasCols .., experts y, y + ny, ... (popular
 // experts, often neighbours, fall to different warps), chunks z, z + parts, ...
-__global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p) {
-  extern __shared__ float4 sum[];  // [experts, 2, 32]
+__device__ __forceinline__ void bias_share(const CombineGradParams &p, int x, int y, int z, int ny,
+                                           float4 *sum) {
   const int lane = threadIdx.x;
-  const int ne = (p.E - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
-  const int col = blockIdx.x * kBiasCols + lane * 8;
+  const int ne = (p.E - y + ny - 1) / ny;
+  const int col = x * kBiasCols + lane * 8;
   const bool in = col < p.H;
   for (int i = 0; i < ne * 2; ++i) sum[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-  griddep_wait();
   const int chunks = (p.T + kChunkTokens - 1) / kChunkTokens;
   const uint16_t *g = p.g + (in ? col : 0);
-  for (int c = blockIdx.z; c < chunks; c += p.parts) {
-    const int32_t *off = p.off + (int64_t)c * (p.E + 1) + blockIdx.y;
+  for (int c = z; c < chunks; c += p.parts) {
+    const int32_t *off = p.off + (int64_t)c * (p.E + 1) + y;
     const int2 *ent = p.ent + (int64_t)c * kChunkTokens * p.K;
-    for (int i = 0; i < ne; ++i, off += gridDim.y) {
+    for (int i = 0; i < ne; ++i, off += ny) {
       int first = __ldg(off);
       const int end = __ldg(off + 1);
       if (first == end) continue;
@@ -413,11 +427,25 @@ __global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p) {
     }
   }
   if (!in) return;
-  float *o = p.part + ((int64_t)blockIdx.z * p.E + blockIdx.y) * p.H + col;
+  float *o = p.part + ((int64_t)z * p.E + y) * p.H + col;
   for (int i = 0; i < ne; ++i) {
-    float4 *const r = reinterpret_cast<float4 *>(o + (int64_t)i * gridDim.y * p.H);
+    float4 *const r = reinterpret_cast<float4 *>(o + (int64_t)i * ny * p.H);
     r[0] = sum[i * 64 + lane];
     r[1] = sum[i * 64 + 32 + lane];
+  }
+}
+
+// A warp's share is its place in the grid, or with CAPPED warps take the nx * ny *
+// parts shares in turn (the skewed case above takes 300 us that way).
+template <bool CAPPED>
+__global__ void __launch_bounds__(32) bias_grad_kernel(CombineGradParams p, int nx, int ny) {
+  extern __shared__ float4 sum[];  // [experts, 2, 32]; a lane touches its own columns only
+  griddep_wait();
+  if constexpr (!CAPPED) {
+    bias_share(p, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y, sum);
+  } else {
+    for (int b = blockIdx.x; b < nx * ny * p.parts; b += gridDim.x)
+      bias_share(p, b % nx, b / nx % ny, b / (nx * ny), ny, sum);
   }
 }
 
@@ -431,8 +459,7 @@ cudaError_t launch_rows(const CombineGradParams &p, int threads, int sm_cap, cud
   const cudaError_t e =
       launch_geometry(reinterpret_cast<const void *>(kern), threads, 0, &dev, &per_sm);
   if (e != cudaSuccess) return e;
-  const int sms = device_sm_count(dev);
-  const int use = (sm_cap > 0 && sm_cap < sms) ? sm_cap : sms;
+  const int use = sms_to_use(dev, sm_cap);
   const int64_t items = (int64_t)p.T + (p.zero_padding ? p.rows_alloc : 0);  // tokens, then padding
   const int64_t grid = std::min<int64_t>((int64_t)use * std::max(per_sm, 1), items);
   return launch_pdl(kern, (unsigned)grid, threads, 0, s, p);
@@ -487,21 +514,30 @@ cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStre
   const int experts = bias_experts(p.E);
   const size_t sort_smem = sizeof(int) * kSortWarps * (size_t)p.E;
   const size_t smem = (size_t)experts * kBiasCols * sizeof(float);
-  int dev = 0;
-  e = launch_geometry(reinterpret_cast<const void *>(bias_sort_kernel), kSortWarps * 32, sort_smem,
-                      &dev, nullptr);
+  int dev = 0, sort_per_sm = 0, per_sm = 0;
+  const auto sort = sm_cap > 0 ? bias_sort_kernel<true> : bias_sort_kernel<false>;
+  e = launch_geometry(reinterpret_cast<const void *>(sort), kSortWarps * 32, sort_smem, &dev,
+                      &sort_per_sm);
   if (e != cudaSuccess) return e;
-  e = launch_geometry(reinterpret_cast<const void *>(bias_grad_kernel), 32, smem, &dev, nullptr);
+  const auto bias = sm_cap > 0 ? bias_grad_kernel<true> : bias_grad_kernel<false>;
+  e = launch_geometry(reinterpret_cast<const void *>(bias), 32, smem, &dev, &per_sm);
   if (e != cudaSuccess) return e;
+  // as many CTAs as the SMs of a cap hold
+  auto most = [&](int64_t items, int per) {
+    return (unsigned)std::min(items, (int64_t)sms_to_use(dev, sm_cap) * std::max(per, 1));
+  };
+  const int chunks = bias_chunks(p);
   if (p.T > 0) {
-    e = launch_pdl(bias_sort_kernel, dim3((unsigned)bias_chunks(p)), kSortWarps * 32, sort_smem, s,
-                   p);
+    e = launch_pdl(sort, sm_cap > 0 ? most(chunks, sort_per_sm) : (unsigned)chunks,
+                   kSortWarps * 32, sort_smem, s, p, chunks);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid((p.H + kBiasCols - 1) / kBiasCols, (p.E + experts - 1) / experts, p.parts);
-  e = launch_pdl(bias_grad_kernel, grid, 32, smem, s, p);
+  const int nx = (p.H + kBiasCols - 1) / kBiasCols, ny = (p.E + experts - 1) / experts;
+  const dim3 grid = sm_cap > 0 ? dim3(most((int64_t)nx * ny * p.parts, per_sm))
+                               : dim3(nx, ny, p.parts);
+  e = launch_pdl(bias, grid, 32, smem, s, p, nx, ny);
   if (e != cudaSuccess || p.part == p.gbias) return e;
-  return launch_column_sum(p.part, p.parts, (int64_t)p.E * p.H, p.gbias, s);
+  return launch_column_sum(p.part, p.parts, (int64_t)p.E * p.H, p.gbias, sm_cap, s);
 }
 
 }  // namespace ep

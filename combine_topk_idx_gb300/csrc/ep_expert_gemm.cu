@@ -459,8 +459,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream
   const cudaError_t e = launch_geometry(reinterpret_cast<const void *>(kernel),
                                         kThreads, smem, &dev, nullptr);
   if (e != cudaSuccess) return e;
-  const int sms = device_sm_count(dev);
-  const int use = (sm_cap > 0 && sm_cap < sms) ? sm_cap : sms;
+  const int use = sms_to_use(dev, sm_cap);
   // at most this many row tiles hold rows (every expert's last one may be partial)
   const int64_t tiles_r = std::min<int64_t>(p.max_slots, p.E) + 2 * (p.rows_alloc / kTileR);
   const int64_t tiles = std::max<int64_t>(1, tiles_r * ((p.N + kTileC - 1) / kTileC));

@@ -272,14 +272,14 @@ cudaError_t launch_combine(const CombineParams &p, int sm_cap, cudaStream_t s);
 cudaError_t launch_combine_weights(const CombineWeightsParams &p, cudaStream_t s);
 
 // out[c] = sum over i < parts of part[i * n + c], in a fixed order.
-cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
+cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out, int sm_cap,
                               cudaStream_t s);
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s);
 // Rows of partial sums (CTAs) a backward call will write.
 cudaError_t norm_backward_parts(const NormBackwardParams &p, int *parts);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s);
-cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s);
-cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s);
+cudaError_t launch_swiglu(const SwigluParams &p, int sm_cap, cudaStream_t s);
+cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, int sm_cap, cudaStream_t s);
 // Bytes of the bias gradient's workspace; with `base` also its arrays in p.
 cudaError_t combine_grad_workspace(CombineGradParams *p, size_t *bytes, void *base);
 cudaError_t launch_combine_grad(const CombineGradParams &p, int sm_cap, cudaStream_t s);
@@ -288,6 +288,12 @@ cudaError_t launch_expert_gemm(const ExpertGemmParams &p, int sm_cap, cudaStream
 
 // Device facts, cached per device.
 int device_sm_count(int device);
+
+// SMs that a call may use: all of the device's, or the cap of its layout.
+inline int sms_to_use(int device, int sm_cap) {
+  const int sms = device_sm_count(device);
+  return (sm_cap > 0 && sm_cap < sms) ? sm_cap : sms;
+}
 
 // Resident CTAs per SM of `func` at (threads, dynamic shared memory) on the
 // current device, with the dynamic shared-memory opt-in (above

@@ -217,16 +217,14 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(NormBackwardParams 
   }
 }
 
-// out[c] = sum over i < parts of part[i, c], in a fixed order: SPLIT threads of a
-// column sum every SPLIT-th row, then one adds their sums.  A thread has V
-// columns, V * 4 bytes of each row.
+// out[c] = sum over i < parts of part[i, c], in a fixed order, for the 32 * V
+// columns from c0: SPLIT threads of a column sum every SPLIT-th row, then one adds
+// their sums.  A thread has V columns, V * 4 bytes of each row.
 template <int V, int SPLIT>
-__global__ void __launch_bounds__(32 * SPLIT)
-    column_sum_kernel(const float *part, int parts, int64_t n, float *out) {
-  __shared__ float s[SPLIT][32 * V];
+__device__ __forceinline__ void column_block(const float *part, int parts, int64_t n, float *out,
+                                             int64_t c0, float (*s)[32 * V]) {
   const int c = (threadIdx.x & 31) * V, k = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * (32 * V) + c;
-  griddep_wait();
+  const int64_t col = c0 + c;
   float v[V] = {};
   if (col < n) {
 #pragma unroll 4
@@ -244,11 +242,45 @@ __global__ void __launch_bounds__(32 * SPLIT)
   for (int j = 0; j < V; ++j) s[k][c + j] = v[j];
   __syncthreads();
   const int o = threadIdx.x;
-  if (o < 32 * V && (int64_t)blockIdx.x * (32 * V) + o < n) {
+  if (o < 32 * V && c0 + o < n) {
     float t = s[0][o];
     for (int i = 1; i < SPLIT; ++i) t += s[i][o];
-    out[(int64_t)blockIdx.x * (32 * V) + o] = t;
+    out[c0 + o] = t;
   }
+}
+
+// A CTA takes one block of columns, or with CAPPED blocks in turn (the loop's
+// registers cost 0.7 us of 10 where every block has its CTA).
+template <int V, int SPLIT, bool CAPPED>
+__global__ void __launch_bounds__(32 * SPLIT)
+    column_sum_kernel(const float *part, int parts, int64_t n, float *out) {
+  __shared__ float s[SPLIT][32 * V];
+  griddep_wait();
+  int64_t c0 = (int64_t)blockIdx.x * (32 * V);
+  if constexpr (!CAPPED) {
+    column_block<V, SPLIT>(part, parts, n, out, c0, s);
+  } else {
+    for (; c0 < n; c0 += (int64_t)gridDim.x * (32 * V)) {
+      column_block<V, SPLIT>(part, parts, n, out, c0, s);
+      __syncthreads();
+    }
+  }
+}
+
+template <int V, int SPLIT>
+cudaError_t launch_columns(const float *part, int parts, int64_t n, float *out, int sm_cap,
+                           cudaStream_t s) {
+  const int64_t blocks = (n + 32 * V - 1) / (32 * V);
+  if (sm_cap <= 0)
+    return launch_pdl(column_sum_kernel<V, SPLIT, false>, (unsigned)blocks, 32 * SPLIT, 0, s, part,
+                      parts, n, out);
+  auto kern = column_sum_kernel<V, SPLIT, true>;
+  int dev = 0, per_sm = 0;
+  const cudaError_t e =
+      launch_geometry(reinterpret_cast<const void *>(kern), 32 * SPLIT, 0, &dev, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = (int64_t)sms_to_use(dev, sm_cap) * std::max(per_sm, 1);
+  return launch_pdl(kern, (unsigned)std::min(blocks, ctas), 32 * SPLIT, 0, s, part, parts, n, out);
 }
 
 // Four vectors per thread (two: 74 us against 60 for 4096 rows of 7168, for the
@@ -269,15 +301,12 @@ auto backward_kernel(int threads) {
 
 }  // namespace
 
-cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out,
+cudaError_t launch_column_sum(const float *part, int parts, int64_t n, float *out, int sm_cap,
                               cudaStream_t s) {
   // Few columns: 32 threads of each; many: 16 bytes a thread, 8 of a column.  608
   // rows of 4096 take 6.7 us one way and 10 the other, 24 of 262,144 33 and 7.8.
-  if (n >= kWideSum)
-    return launch_pdl(column_sum_kernel<4, 8>, (unsigned)((n + 127) / 128), 32 * 8, 0, s, part,
-                      parts, n, out);
-  return launch_pdl(column_sum_kernel<1, 32>, (unsigned)((n + 31) / 32), 32 * 32, 0, s, part, parts,
-                    n, out);
+  return n >= kWideSum ? launch_columns<4, 8>(part, parts, n, out, sm_cap, s)
+                       : launch_columns<1, 32>(part, parts, n, out, sm_cap, s);
 }
 
 cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
@@ -307,7 +336,7 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t s) {
   const int threads = backward_threads(p.H);
   const cudaError_t e = launch_pdl(backward_kernel(threads), (unsigned)p.parts, threads, 0, s, p);
   if (e != cudaSuccess || p.ggamma == nullptr) return e;
-  return launch_column_sum(p.part, p.parts, p.H, p.ggamma, s);
+  return launch_column_sum(p.part, p.parts, p.H, p.ggamma, 0, s);
 }
 
 }  // namespace ep

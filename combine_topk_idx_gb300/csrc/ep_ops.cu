@@ -203,7 +203,8 @@ ep_status ep_swiglu(const ep_handle *h, int64_t rows, int32_t ffn, const void *g
   p.sfl = ep::rows_sf(h, ffn);
   p.ckpt = static_cast<uint8_t *>(ckpt_fp8);
   p.ckpt_sf = ckpt_sf;
-  return ep::cuda_status(ep::launch_swiglu(p, reinterpret_cast<cudaStream_t>(stream)));
+  return ep::cuda_status(ep::launch_swiglu(p, h != nullptr ? h->cfg.num_sms : 0,
+                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ep_status ep_swiglu_backward(const ep_handle *h, int64_t rows, int32_t ffn, const void *grad_act,
@@ -233,7 +234,8 @@ ep_status ep_swiglu_backward(const ep_handle *h, int64_t rows, int32_t ffn, cons
   p.sf = grad_sf;
   p.sfl = ep::rows_sf(h, 2 * (int64_t)ffn);
   p.gw = grad_row_weights;
-  return ep::cuda_status(ep::launch_swiglu_backward(p, reinterpret_cast<cudaStream_t>(stream)));
+  return ep::cuda_status(ep::launch_swiglu_backward(p, h != nullptr ? h->cfg.num_sms : 0,
+                                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out, const void *y,

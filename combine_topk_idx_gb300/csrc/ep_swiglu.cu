@@ -319,14 +319,14 @@ __global__ void __launch_bounds__(kThreads)
 // 8192, 32,768 rows of F = 2048 take 122 us against 108 with the checkpoint),
 // shorter where the rows would not give every CTA four, so that the CTAs' loads
 // differ little (8192 rows: 24.7 us against 27.8 with the longest).
-cudaError_t shape_for(const void *func, int64_t rows, int F, bool sums, int *tile,
+cudaError_t shape_for(const void *func, int64_t rows, int F, bool sums, int sm_cap, int *tile,
                       unsigned *grid, size_t *smem) {
   const int most = std::max(1, std::min(kMaxTileRows, kTileElems / F));
   *smem = sums ? 2 * sizeof(float) * (size_t)most * (F / kFp8Block) : 0;
   int dev = 0, per_sm = 0;
   const cudaError_t e = launch_geometry(func, kThreads, *smem, &dev, &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (int64_t)device_sm_count(dev) * std::max(per_sm, 1);
+  const int64_t ctas = (int64_t)sms_to_use(dev, sm_cap) * std::max(per_sm, 1);
   *tile = (int)std::max<int64_t>(1, std::min<int64_t>(most, rows / (4 * ctas)));
   *grid = (unsigned)std::min<int64_t>((rows + *tile - 1) / *tile, ctas);
   return cudaSuccess;
@@ -334,23 +334,23 @@ cudaError_t shape_for(const void *func, int64_t rows, int F, bool sums, int *til
 
 }  // namespace
 
-cudaError_t launch_swiglu(const SwigluParams &p, cudaStream_t s) {
+cudaError_t launch_swiglu(const SwigluParams &p, int sm_cap, cudaStream_t s) {
   auto kern = p.F % kFp8Block == 0 ? swiglu_kernel<2> : swiglu_kernel<1>;
   int tile = 0;
   unsigned grid = 0;
   size_t smem = 0;
   const cudaError_t e = shape_for(reinterpret_cast<const void *>(kern), p.r.rows, p.F, false,
-                                  &tile, &grid, &smem);
+                                  sm_cap, &tile, &grid, &smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, kThreads, smem, s, p, tile);
 }
 
-cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, cudaStream_t s) {
+cudaError_t launch_swiglu_backward(const SwigluBackwardParams &p, int sm_cap, cudaStream_t s) {
   int tile = 0;
   unsigned grid = 0;
   size_t smem = 0;
   const cudaError_t e = shape_for(reinterpret_cast<const void *>(swiglu_backward_kernel), p.r.rows,
-                                  p.F, true, &tile, &grid, &smem);
+                                  p.F, true, sm_cap, &tile, &grid, &smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(swiglu_backward_kernel, grid, kThreads, smem, s, p, tile);
 }

@@ -345,10 +345,12 @@ EP_API void ep_handle_free(ep_handle *h);
  * cfg->use_fp8 says.  FP8 rows are e4m3 bytes with one fp32 scale per 1x128
  * block: scale = amax / 448, bytes = e4m3(value * (1 / scale)) in fp32, to
  * nearest even, saturating; zero, infinite and NaN blocks as in ep_dispatch.  A
- * row of n elements has its scales where ep_sf_layout says.  Rows past the real total (or past an expert's count, in
- * the fixed-capacity layout) are neither read nor written.  Alignment padding
+ * row of n elements has its scales where ep_sf_layout says.  Rows past the real
+ * total (or past an expert's count, in the fixed-capacity layout) are neither
+ * read nor written.  Alignment padding
  * rows are not read; outputs there are zeroed when cfg->do_zero_padding, else
- * left as they are.
+ * left as they are.  Every launch of such a call keeps to cfg->num_sms: at most
+ * the CTAs that so many SMs hold, with the same results.
  */
 
 /*
