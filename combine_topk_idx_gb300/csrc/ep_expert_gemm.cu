@@ -34,8 +34,8 @@
 // epilogue thread spills (20 to 60 % slower): hence 232 registers for it.
 //
 // Every mbarrier wait is bounded: one that gives up sets EP_ERRBIT_TIMEOUT in
-// the handle's error word, and the CTA waits (bounded) for what it has in
-// flight, frees its TMEM and returns.
+// the handle's error word.  However it ends, the CTA waits (bounded) for what it
+// has in flight, frees its TMEM and returns.
 #include <algorithm>
 
 #include "ep_internal.cuh"
@@ -268,13 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (!ok && lane == 0) {
-        atomicOr(p.err, EP_ERRBIT_TIMEOUT);
-        // copies in flight: slots below st.slot in this round, the others in
-        // the round before
-        for (int s = 0; s < kStages; ++s)
-          if (s < st.slot || issued == kStages)
-            wait(&bar.full[s], s < st.slot ? st.phase : st.phase ^ 1);
+      if (lane == 0) {
+        // The products' last arrivals on the stages' barriers: nothing else waits
+        // for them, and they must not come after the CTA's shared memory is gone.
+        Ring<kStages> left = st;
+        for (int s = 0; s < kStages && ok; ++s, left.next())
+          ok = wait(&bar.empty[left.slot], left.phase ^ 1);
+        if (!ok) {
+          atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+          // copies in flight: slots below st.slot in this round, the others in
+          // the round before
+          for (int s = 0; s < kStages; ++s)
+            if (s < st.slot || issued == kStages)
+              wait(&bar.full[s], s < st.slot ? st.phase : st.phase ^ 1);
+        }
       }
     } else if (warp == 1) {
       // ---------------- products ----------------
