@@ -3,7 +3,7 @@
 // Forward, per row of H elements:
 //   s = x + residual (fp32), r = bf16(s), k = 1 / sqrt(mean(s^2) + eps),
 //   v = s * k * gamma; written as bf16(v) and/or as e4m3 bytes with one fp32
-//   scale per 1x128 block (amax / 448), the input of a pre-quantised dispatch.
+//   scale per 1x128 block (amax * (1 / 448)), the input of a pre-quantised dispatch.
 // Backward, with xh = r * k:
 //   m = mean(gy * gamma * xh), gx = k * (gy * gamma - xh * m) + gres,
 //   ggamma = sum over rows of gy * xh.

@@ -343,9 +343,12 @@ EP_API void ep_handle_free(ep_handle *h);
  * Rows, scales and padding of the calls below that take a handle: they work on
  * the rows of its layout (expanded, rank or fixed capacity), whatever
  * cfg->use_fp8 says.  FP8 rows are e4m3 bytes with one fp32 scale per 1x128
- * block: scale = amax / 448, bytes = e4m3(value * (1 / scale)) in fp32, to
- * nearest even, saturating; zero, infinite and NaN blocks as in ep_dispatch.  A
- * row of n elements has its scales where ep_sf_layout says.  Rows past the real
+ * block: scale = amax * (1 / 448), bytes = e4m3(value * r) with r the scale's
+ * reciprocal to within one unit in the last place, all in fp32, to nearest even,
+ * saturating; zero, infinite and NaN blocks as in ep_dispatch.  (ep_dispatch
+ * divides, by 448 and by the scale.  Of the same BF16 row its scales may differ
+ * in the last place, and its bytes where a quotient lies next to the middle of
+ * two e4m3 values; both are then equally near.)  A row of n elements has its scales where ep_sf_layout says.  Rows past the real
  * total (or past an expert's count, in the fixed-capacity layout) are neither
  * read nor written.  Alignment padding
  * rows are not read; outputs there are zeroed when cfg->do_zero_padding, else
