@@ -17,7 +17,9 @@
 // padding is zeroed by the same CTAs afterwards.  Memory bounds it: 4096 tokens
 // x 8 experts, H = 7168, FP8 rows, 164 us for 771 MB and 117 MB of zeroed
 // padding, 5.4 TB/s; each row of y waits for its token's slots and is then
-// read in two pieces a thread, so the loads in flight limit it.
+// read in two pieces a thread, so the loads in flight limit it.  The registers of
+// three CTAs to an SM leave 72 bytes a thread spilt (432 for H above 8192); with
+// registers without limit, and nothing spilt, it takes 250.
 //
 // Bias gradient: a sum over tokens per expert, so the slots of each chunk of
 // kChunkTokens tokens are first sorted by expert (stably, once for all columns);
@@ -263,13 +265,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1)
   }
 }
 
-// 16,384 tokens x 6 of 64 experts, H = 4096, skewed: the whole call takes 294 us,
+// 16,384 tokens x 6 of 64 experts, H = 4096, skewed: the whole call takes 295 us,
 // 197 of them the row kernel's and 10 the sort's.  With 8 experts a warp and half
 // as many parts 25 us more, with 16 experts and 128 columns 53: eight columns a
 // lane halve what is spent per slot on its entry and address.  Many small parts
 // even out a skewed load (40 warps' parts 14 us more, 27 warps' 35) and cost an
-// even one 1 %; their sums take 50 MB at most.  Loads in flight bound it; the
-// gradient rows come from L2.
+// even one 1 %.  Their sums take about 50 MB; the parts are rounded up, so that it
+// can be just under twice that (E 772, H 16128, two parts: 99.6 MB).  Loads in
+// flight bound it; the gradient rows come from L2.
 constexpr int kChunkTokens = 256;
 constexpr int kSortWarps = 8;
 constexpr int kSortAhead = 8;      // steps of 32 slots whose loads are in flight

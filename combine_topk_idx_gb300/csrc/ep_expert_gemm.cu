@@ -24,9 +24,9 @@
 //
 // What bounds it.  Few rows, the weights' bytes: 8 rows, each its expert, N 4096,
 // K 7168, 41 us for 235 MB, 5.7 TB/s of 6.7 that a copy reaches.  128 rows per
-// expert, 256 experts: 1374 to 1455 us on three GPUs for 8.0 GB, 5.5 to 5.8 TB/s.
+// expert, 256 experts: 1374 to 1475 us, by GPU, for 8.0 GB, 5.4 to 5.8 TB/s.
 // Many rows, the scaled sums: 96,300 rows over 64 experts, N = K = 4096, 1451 to
-// 1494 us, 2.2 PFLOP/s, tensor cores busy 53 % of the time.  The products of a
+// 1513 us, 2.1 to 2.2 PFLOP/s, tensor cores busy 53 % of the time.  The products of a
 // block take 512 cycles, its operands' way into shared memory and out 768, the
 // scaled sums 730 by themselves; with the barriers over two accumulators, all that
 // TMEM holds, a block takes about 970.  Pairs of CTAs sharing the operands (1480

@@ -15,10 +15,11 @@
 // costs no reads: its rows are recognised by their source token and, where the
 // layout zeroes padding, written as 0.
 //
-// 4096 tokens x 8 experts, F = 2048, FP8 out and checkpoint kept: 100 us, 4.7
+// 4096 tokens x 8 experts, F = 2048, FP8 out and checkpoint kept: 100 to 104 us, 4.6
 // TB/s of the rows in use, between memory (71 us at a copy's rate) and the issue
 // of its instructions (66 % of the cycles).  8192 rows without checkpoint: 17.3
-// us, 4.9 TB/s.  Units dealt to the threads of the whole grid, without tiles and
+// us, 4.9 TB/s; a call of a few rows takes 5.  36 bytes a thread are spilt at three
+// CTAs to an SM.  Units dealt to the threads of the whole grid, without tiles and
 // their barriers, take 112 us for the first, and with copies into shared memory
 // three units ahead 133.  The gradient's figures are at its kernel.
 #include <algorithm>
@@ -36,7 +37,8 @@ constexpr int kTileElems = 32768;  // of F per tile, at most
 constexpr int kMaxTileRows = 64;
 
 // 1 / (1 + e^-g) of a pair: relative error about 2^-21 plus the rounding of g's
-// exponent (|g| 2^-24); 0 where e^-g overflows.
+// exponent (|g| 2^-24); 0 where 1 + e^-g passes 2^126 (g below -87.3), for a
+// subnormal reciprocal counts as 0.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
   const float c = -1.4426950408889634f;
   const uint64_t x = f32x2_mul_rn(g, f32x2_pack(c, c));
@@ -193,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 3) swiglu_kernel(SwigluParams p, int
   }
 }
 
-// 4096 tokens x 8 experts, F = 2048, FP8 in and out: 107 us, 3.8 TB/s of the rows
-// in use.  Between the issue of its instructions (59 % of the cycles) and its
+// 4096 tokens x 8 experts, F = 2048, FP8 in and out: 107 to 111 us, 3.8 TB/s of the
+// rows in use; BF16 out 117 us, 4.6 TB/s.  52 bytes a thread are spilt at four CTAs
+// to an SM.  Between the issue of its instructions (59 % of the cycles) and its
 // loads: loading a unit ahead as above costs registers, and so resident warps
 // (114 -> 122 us); whole rows to a warp, without the tile's barrier, gain nothing
 // (108 us); copies into shared memory three units ahead cost more than the wait

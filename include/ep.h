@@ -352,7 +352,8 @@ EP_API void ep_handle_free(ep_handle *h);
  * total (or past an expert's count, in the fixed-capacity layout) are neither
  * read nor written.  Alignment padding
  * rows are not read; outputs there are zeroed when cfg->do_zero_padding, else
- * left as they are.  Every launch of such a call keeps to cfg->num_sms: at most
+ * left as they are.  Outputs overlap neither each other nor an input, unless the
+ * call says that they may.  Every launch of such a call keeps to cfg->num_sms: at most
  * the CTAs that so many SMs hold, with the same results.
  */
 
@@ -466,7 +467,8 @@ EP_API ep_status ep_swiglu_backward(const ep_handle *h, int64_t rows, int32_t ff
  *   grad_expert_bias fp32 [E, H]: sum over the slots routed to e of weight *
  *     grad_out, in a fixed order; 0 for an expert without slots.
  * The gradient of bias_0 and bias_1 is grad_out.  Uses a stream-ordered
- * workspace if grad_expert_bias is given.
+ * workspace if grad_expert_bias is given: 8 bytes per slot and up to 100 MB of
+ * partial sums, which the device's pool keeps for later calls.
  */
 EP_API ep_status ep_combine_weighted_backward(const ep_handle *h, const void *grad_out,
                                               const void *y, const float *topk_weights,
