@@ -19,3 +19,7 @@ from ._ops import (  # noqa: F401
     alloc_fp8, alloc_rmsnorm, ep_combine_weighted_backward, ep_expert_gemm, ep_rmsnorm,
     ep_rmsnorm_backward, ep_swiglu, ep_swiglu_backward, sf_layout,
 )
+from ._ffn import (  # noqa: F401
+    GradPlan, ep_clip_grads, ep_ffn_gated, ep_ffn_gated_backward, ep_ffn_product,
+    ep_ffn_weight_grad, ep_grad_norm, plan_grads,
+)

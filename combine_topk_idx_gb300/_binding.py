@@ -150,6 +150,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ep_combine_weighted_backward.restype = ctypes.c_int
     lib.ep_expert_gemm.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp]
     lib.ep_expert_gemm.restype = ctypes.c_int
+    lib.ep_ffn_gated.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp]
+    lib.ep_ffn_gated_backward.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp]
+    lib.ep_ffn_product.argtypes = [vp, i64, i32, i32, vp, i64, vp, i32, vp, vp]
+    lib.ep_ffn_weight_grad.argtypes = [vp, i64, i32, i32, vp, i64, vp, i64, vp, i32, i32, vp]
+    lib.ep_clip_grads.argtypes = [i32, vp, vp, vp, vp, ctypes.c_float, vp, vp]
+    for fn in (lib.ep_ffn_gated, lib.ep_ffn_gated_backward, lib.ep_ffn_product,
+               lib.ep_ffn_weight_grad, lib.ep_clip_grads):
+        fn.restype = ctypes.c_int
     if lib.ep_abi_version() != EP_ABI_VERSION:
         raise RuntimeError("libep.so ABI version does not match this binding")
     _lib = lib

@@ -42,6 +42,7 @@
 #include "ep_ptx.cuh"
 #include "ep_rows.cuh"
 #include "ep_tcgen05.cuh"
+#include "ep_tma_host.cuh"
 
 namespace ep {
 namespace {
@@ -418,24 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, kTmemColumns);
-}
-
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
 }
 
 // Rows of K bytes, copied as boxes of 128 bytes x box_rows, zeros outside.

@@ -1,0 +1,799 @@
+// The BF16 products of a trained feed-forward block, with what stands around
+// them fused into their last step.  W [E, ...] one matrix per expert, rows r of
+// a layout sorted by expert (or E = 1 and all rows):
+//   gated        h = x W^T, W [2F, K] gate rows then up rows;
+//                act = silu(h_gate) * h_up, and h itself for the backward pass
+//   gated grad   d = g W, W [K, F] the down projection; with the forward's h:
+//                dh = (d h_up silu'(h_gate), d silu(h_gate)), act once more
+//   product      out = a W^T, W [N, K], or a W, W [K, N] (transposed)
+//   weight grad  W'[e] = sum over e's rows of g[r]^T a[r]
+// Sums in fp32 (TMEM), each output rounded once.
+//
+// A tile is 128 rows x 256 columns of a CTA's TMEM (gated: 128 gate columns and
+// the 128 up columns beside them).  Warps of a CTA:
+//   0       copies the operands, 64 reduction elements per stage, into a ring of
+//           stages (tiled TMA, 128-byte swizzle)
+//   1       issues the products into one of two accumulators
+//   4..11   four for each half of the columns: read a finished accumulator, apply
+//           the rest of the formula and store, while the next tile is multiplied
+// An operand whose contiguous dimension is the reduction is taken row by row, one
+// whose contiguous dimension is the output's as it lies in memory too (the tensor
+// cores transpose): no operand is laid out again.
+//
+// Three forms of one kernel:
+//   kPair 1   persistent, a CTA per SM
+//   kPair 2   persistent, two CTAs on a 256 x 256 tile: each holds its 128 rows and
+//             half of the columns' operand
+//   kSplit    few tiles: a cluster per tile, its CTAs share the reduction and add
+//             up through each other's shared memory, in a fixed order
+//
+// Rows that are not an expert's own never reach its results: in the row products
+// they are other rows of the accumulator; in the weight gradient, where they
+// would be summed, an expert's tensor map ends with its last row, and what a copy
+// reads behind it is zero.
+//
+// Every mbarrier wait is bounded.  One that gives up sets EP_ERRBIT_TIMEOUT in
+// the handle's error word (where there is one) and the tiles that are not done
+// hold NaN.  However it ends, the CTA waits (bounded) for what it has in flight,
+// frees its TMEM and returns.
+#include <algorithm>
+
+#include "ep_ffn.cuh"
+#include "ep_ptx.cuh"
+#include "ep_tcgen05.cuh"
+#include "ep_tma_host.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
+constexpr int kRowStep = 16;   // a tile's rows are copied up to a multiple of this
+constexpr int kRowMaps = 4;    // boxes of 16, 32, 64 and 128 rows
+constexpr int kBoxBytes = 64 * kBlockK * 2;  // 64 columns of a 64-element block
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
+constexpr int kRaster = 16;    // row tiles that pass over the columns together
+constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
+constexpr uint32_t kWaitHintNs = 500000;
+
+template <int kPair>
+struct Ring_ {
+  static constexpr int kABytes = kTileM * kBlockK * 2;
+  static constexpr int kBBytes = kTileN / kPair * kBlockK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = kPair == 2 ? 6 : 4;
+};
+
+struct Maps {
+  CUtensorMap a[kRowMaps], b;
+};
+
+struct __align__(8) Barriers {
+  uint64_t full[6];       // a stage's copies landed (the pair's first CTA)
+  uint64_t empty[6];      // the products that read a stage are done
+  uint64_t acc_full[2];   // an accumulator is complete
+  uint64_t acc_empty[2];  // an accumulator is read (the pair's first CTA)
+  uint64_t drain;
+};
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t phase) {
+  return mbar_wait_bounded(bar, phase, kWaitIters, kWaitHintNs);
+}
+
+// Position in a ring of N slots; see the waits: a consumer waits for `phase`, a
+// producer for the round before (`phase ^ 1`, which a fresh barrier passes).
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+struct Tile {
+  int e;         // expert
+  int64_t row0;  // first row of the output (weight gradient: within the expert's matrix)
+  int used;      // rows of the tile with a result
+  int write;     // rows to write: the used ones, then zeros
+  int n0;        // first column
+  int64_t k0;    // weight gradient: first row of the sum
+  int blocks;    // blocks of the reduction
+};
+
+// Row tiles of the experts before e (row products; e <= E) in cum[e].  All threads.
+__device__ __forceinline__ void count_tiles(const FfnParams &p, int rows_per_tile, int *cum,
+                                            int *warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int e0 = 0; e0 < p.s.E; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    int m = 0;
+    if (e < p.s.E) {
+      const SegmentRows r = segment_rows(p.s, e);
+      m = (int)((r.write + rows_per_tile - 1) / rows_per_tile);
+    }
+    int v = m;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    int before = base, all = base;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (e < p.s.E) cum[e] = before + v - m;
+    base = all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[p.s.E] = base;
+  __syncthreads();
+}
+
+// (row, column) of tile k of tr x tc: kRaster row tiles pass over the columns together.
+__device__ __forceinline__ void raster(int64_t k, int tr, int tc, int *r, int *c) {
+  const int64_t per = (int64_t)kRaster * tc;
+  const int g = (int)(k / per) * kRaster;
+  const int n = min(kRaster, tr - g);
+  const int u = (int)(k - (int64_t)g * tc);
+  *c = u / n;
+  *r = g + u - *c * n;
+}
+
+// Tile i.  Whole warps.
+template <int kMode>
+__device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, int64_t i,
+                                          int rows_per_tile, int tiles_n) {
+  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
+  Tile t;
+  int r, c;
+  if constexpr (kMode == kFfnWeightGrad) {
+    const int tr = (p.M + rows_per_tile - 1) / rows_per_tile;
+    const int64_t per = (int64_t)tr * tiles_n;
+    t.e = (int)(i / per);
+    raster(i - t.e * per, tr, tiles_n, &r, &c);
+    const SegmentRows s = segment_rows(p.s, t.e);
+    t.row0 = (int64_t)r * rows_per_tile;
+    t.used = t.write = min(rows_per_tile, p.M - (int)t.row0);
+    t.k0 = s.first;
+    t.blocks = (int)((s.used + kBlockK - 1) / kBlockK);
+  } else {
+    const int lane = threadIdx.x & 31;
+    int lo = -1;  // the last expert with cum[e] * tiles_n <= i
+    for (int e = lane; e - lane < p.s.E; e += 32)
+      lo += __popc(__ballot_sync(0xffffffffu, e < p.s.E && (int64_t)cum[e] * tiles_n <= i));
+    raster(i - (int64_t)cum[lo] * tiles_n, cum[lo + 1] - cum[lo], tiles_n, &r, &c);
+    const SegmentRows s = segment_rows(p.s, lo);
+    const int64_t off = (int64_t)r * rows_per_tile;
+    t.e = lo;
+    t.row0 = s.first + off;
+    t.used = (int)max((int64_t)0, min((int64_t)rows_per_tile, s.used - off));
+    t.write = (int)min((int64_t)rows_per_tile, s.write - off);
+    t.k0 = 0;
+    t.blocks = t.used > 0 ? (p.K + kBlockK - 1) / kBlockK : 0;
+  }
+  t.n0 = c * kCols;
+  return t;
+}
+
+// Rows of a tile that CTA `rank` of a pair takes: from which, and how many of n.
+// Halves are multiples of kRowStep, so that few rows are shared out too.
+template <int kMode, int kPair>
+__device__ __forceinline__ int half_of(const Tile &t) {
+  if (kPair == 1) return kTileM;
+  if (kMode == kFfnWeightGrad) return kTileM;
+  return ((t.write + 1) / 2 + kRowStep - 1) / kRowStep * kRowStep;
+}
+
+// ---- what is computed of 16 accumulated columns -----------------------------------------
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return rcp_approx(1.f + exp2_approx(-1.4426950408889634f * g));
+}
+
+__device__ __forceinline__ void store16_bf16(uint16_t *o, int col, int N, bool whole, bool zero,
+                                             const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) w[q] = zero ? 0u : cvt_bf16x2(v[2 * q], v[2 * q + 1]);
+  if (whole && col + 16 <= N) {
+    st_stream_v8(o, w);
+  } else {
+    if (col + 8 <= N) st_stream_v4(o, make_uint4(w[0], w[1], w[2], w[3]));
+    if (col + 16 <= N) st_stream_v4(o + 8, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+
+// 16 BF16 values from column `col` of a row; zeros behind column N.
+__device__ __forceinline__ void load16_bf16(const uint16_t *a, int col, int N, uint4 (&v)[2]) {
+  v[0] = col + 8 <= N ? ld_stream_v4(a) : make_uint4(0, 0, 0, 0);
+  v[1] = col + 16 <= N ? ld_stream_v4(a + 8) : make_uint4(0, 0, 0, 0);
+}
+
+// Gate and up of the forward at 16 columns of a row.
+struct Kept {
+  uint4 g[2], u[2];
+};
+__device__ __forceinline__ void load_kept(const FfnParams &p, int64_t row, int col, Kept *k) {
+  const uint16_t *h = p.kept + row * 2 * p.N + col;
+  load16_bf16(h, col, p.N, k->g);
+  load16_bf16(h + p.N, col, p.N, k->u);
+}
+
+// Writes 16 columns of a row from the accumulated v (gated: gate v, up u).
+template <int kMode>
+__device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e, int col,
+                                         bool zero, const float (&v)[16], const float (&u)[16],
+                                         const Kept &k) {
+  const int N = p.N;
+  if constexpr (kMode == kFfnGated) {
+    if (p.out != nullptr) {
+      float a[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] = v[i] * sigmoid(v[i]) * u[i];
+      store16_bf16(p.out + row * N + col, col, N, p.out32, zero, a);
+    }
+    if (p.out2 != nullptr) {
+      uint16_t *h = p.out2 + row * 2 * N + col;
+      store16_bf16(h, col, N, p.out2_32, zero, v);
+      store16_bf16(h + N, col, N, p.out2_32, zero, u);
+    }
+  } else if constexpr (kMode == kFfnGatedGrad) {
+    float dg[16], du[16], a[16];
+    const uint32_t *gw = reinterpret_cast<const uint32_t *>(k.g);
+    const uint32_t *uw = reinterpret_cast<const uint32_t *>(k.u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float g = i & 1 ? bf16_hi(gw[i / 2]) : bf16_lo(gw[i / 2]);
+      const float up = i & 1 ? bf16_hi(uw[i / 2]) : bf16_lo(uw[i / 2]);
+      const float s = sigmoid(g), silu = g * s;
+      dg[i] = v[i] * up * (s + silu * (1.f - s));
+      du[i] = v[i] * silu;
+      a[i] = silu * up;
+    }
+    uint16_t *h = p.out + row * 2 * N + col;
+    store16_bf16(h, col, N, p.out32, zero, dg);
+    store16_bf16(h + N, col, N, p.out32, zero, du);
+    if (p.out2 != nullptr) store16_bf16(p.out2 + row * N + col, col, N, p.out2_32, zero, a);
+  } else if constexpr (kMode == kFfnWeightGrad) {
+    const int64_t at = ((int64_t)e * p.M + row) * N + col;
+    if (p.f32) {
+      float *o = reinterpret_cast<float *>(p.out) + at;
+#pragma unroll
+      for (int q = 0; q < 16; q += 4) {
+        if (col + q + 4 > N) break;
+        float4 r = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+        if (zero) r = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.accumulate) {
+          const float4 b = *reinterpret_cast<const float4 *>(o + q);
+          r = make_float4(r.x + b.x, r.y + b.y, r.z + b.z, r.w + b.w);
+        }
+        __stcs(reinterpret_cast<float4 *>(o + q), r);
+      }
+    } else {
+      uint16_t *o = p.out + at;
+      if (p.accumulate) {
+        uint4 b[2];
+        b[0] = col + 8 <= N ? ld_plain_v4(o) : make_uint4(0, 0, 0, 0);
+        b[1] = col + 16 <= N ? ld_plain_v4(o + 8) : make_uint4(0, 0, 0, 0);
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(b);
+        float s[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[i] = v[i] + (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]));
+        store16_bf16(o, col, N, p.out32, false, s);
+      } else {
+        store16_bf16(o, col, N, p.out32, zero, v);
+      }
+    }
+  } else {
+    store16_bf16(p.out + row * N + col, col, N, p.out32, zero, v);
+  }
+}
+
+// ---- the kernel ---------------------------------------------------------------------------
+
+template <int kMode, int kPair, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
+  using R = Ring_<kPair>;
+  constexpr int kStages = R::kStages;
+  constexpr bool kAMn = kMode == kFfnWeightGrad;
+  constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kMode == kFfnWeightGrad;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int warp_sum[kThreads / 32];
+  // stages on 1024-byte boundaries (the swizzle's period), then cum[E + 1]
+  uint8_t *smem = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;
+  int *cum = reinterpret_cast<int *>(smem + kStages * R::kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair == 2 || kSplit ? (int)cluster_rank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar.full[s], 1);
+      mbar_init(&bar.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar.acc_full[b], 1);
+      mbar_init(&bar.acc_empty[b], kEpilogueWarps * kPair);
+    }
+    mbar_init(&bar.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_group<kPair>(&tmem_slot, kTmemColumns);
+  griddep_wait();
+  if constexpr (kMode != kFfnWeightGrad) count_tiles(p, kTileM * kPair, cum, warp_sum);
+  __syncthreads();
+  if constexpr (kPair == 2) {  // the other CTA's barriers are ready
+    cluster_arrive_release();
+    cluster_wait();
+  }
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
+  const int tiles_n = (p.N + kCols - 1) / kCols;
+  int64_t tiles;
+  if constexpr (kMode == kFfnWeightGrad)
+    tiles = (int64_t)p.s.E * ((p.M + kTileM * kPair - 1) / (kTileM * kPair)) * tiles_n;
+  else
+    tiles = (int64_t)cum[p.s.E] * tiles_n;
+  // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
+  const int share = kSplit ? p.split : kPair;
+  const int64_t first = blockIdx.x / share, step = gridDim.x / share;
+  const auto tile_at = [&](int64_t i) {
+    return find_tile<kMode>(p, cum, i, kTileM * kPair, tiles_n);
+  };
+  // this CTA's part of a tile's reduction
+  const auto part = [&](int blocks, int r) {
+    return kSplit ? (int)((int64_t)blocks * r / p.split) : (r == 0 ? 0 : blocks);
+  };
+  const int part_rank = kSplit ? rank : 0;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    Ring<kStages> st;
+    int issued = 0;  // stages filled, counted up to kStages
+    for (int64_t i = first; i < tiles && ok; i += step) {
+      const Tile t = tile_at(i);
+      const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
+      if (lane == 0 && kb < ke) {
+        const int half = half_of<kMode, kPair>(t);
+        const int mine0 = kPair == 2 ? rank * half : 0;
+        // rows copied: up to a multiple of kRowStep; of both CTAs of a pair
+        const int left = kPair == 2 ? min(half, t.used) : t.used;
+        const auto up = [](int n) { return max(0, (n + kRowStep - 1) / kRowStep * kRowStep); };
+        const int rows0 = kAMn ? kTileM : up(left);
+        const int rows1 = kPair == 1 ? 0 : kAMn ? kTileM : up(t.used - half);
+        const int rows = rank != 0 && kPair == 2 ? rows1 : rows0;
+        const uint32_t bytes = (uint32_t)((rows0 + rows1 + kTileN) * kBlockK * 2);
+        const CUtensorMap *ma = &maps.a[0], *mb = &maps.b;
+        if (kAMn && p.seg_maps != nullptr) {
+          ma = reinterpret_cast<const CUtensorMap *>(p.seg_maps) + 2 * t.e;
+          mb = ma + 1;
+          tma_acquire_map(ma);
+          tma_acquire_map(mb);
+        }
+        for (int k = kb; k < ke; ++k) {
+          if (!wait(&bar.empty[st.slot], st.phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t *a = smem + st.slot * R::kStageBytes, *b = a + R::kABytes;
+          const uint32_t full = kPair == 2 ? cluster_map(&bar.full[st.slot], 0)
+                                           : smem_u32(&bar.full[st.slot]);
+          if (kPair == 1 || rank == 0) mbar_arrive_expect_tx(&bar.full[st.slot], bytes);
+          if constexpr (kAMn) {
+            const int y = (int)(t.k0 + (int64_t)k * kBlockK);
+#pragma unroll
+            for (int j = 0; j < kTileM / 64; ++j)
+              tma_load_3d<kPair>(a + j * kBoxBytes, ma, (int)t.row0 + mine0 + 64 * j, y, 0, full);
+          } else {
+            int r = 0;
+#pragma unroll
+            for (int q = kRowMaps - 1; q >= 0; --q)  // rows = 16 * (sum of 2^q)
+              if (rows & (kRowStep << q)) {
+                tma_load_3d<kPair>(a + r * kBlockK * 2, &maps.a[q], k * kBlockK,
+                                   (int)t.row0 + mine0 + r, 0, full);
+                r += kRowStep << q;
+              }
+          }
+          if constexpr (kBMn) {
+            const int y = kMode == kFfnWeightGrad ? (int)(t.k0 + (int64_t)k * kBlockK)
+                                                  : k * kBlockK;
+            const int z = kMode == kFfnWeightGrad ? 0 : t.e;
+            const int x = t.n0 + (kPair == 2 ? rank * (kTileN / 2) : 0);
+#pragma unroll
+            for (int j = 0; j < kTileN / kPair / 64; ++j)
+              tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, z, full);
+          } else {
+            // 128 rows of the matrix per box: gate and up, or two neighbours
+            const int far = kMode == kFfnGated ? p.N : kTileN / 2;
+#pragma unroll
+            for (int j = 0; j < 2 / kPair; ++j)
+              tma_load_3d<kPair>(b + 2 * j * kBoxBytes, mb, k * kBlockK,
+                                 t.n0 + (kPair == 2 ? rank : j) * far, t.e, full);
+          }
+          st.next();
+          if (issued < kStages) ++issued;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
+      // The products' last arrivals on the stages' barriers: nothing else waits for
+      // them, and they must not come after the CTA's shared memory is gone.
+      Ring<kStages> left = st;
+      for (int s = 0; s < kStages && ok; ++s, left.next())
+        ok = wait(&bar.empty[left.slot], left.phase ^ 1);
+      if (!ok) {
+        if (p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+        // copies in flight: slots below st.slot in this round, the others in the
+        // round before
+        if (kPair == 1 || rank == 0)
+          for (int s = 0; s < kStages; ++s)
+            if (s < st.slot || issued == kStages)
+              wait(&bar.full[s], s < st.slot ? st.phase : st.phase ^ 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && (kPair == 1 || rank == 0)) {
+    // ---------------- products ----------------
+    constexpr uint32_t idesc = idesc_bf16(kTileM * kPair, kTileN, kAMn, kBMn);
+    constexpr int kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
+    Ring<kStages> st;
+    Ring<2> acc;
+    const uint32_t smem0 = smem_u32(smem);
+    for (int64_t i = first; i < tiles && ok; i += step) {
+      const Tile t = tile_at(i);
+      const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
+      if (kb == ke) continue;
+      ok = __all_sync(0xffffffffu, wait(&bar.acc_empty[acc.slot], acc.phase ^ 1));
+      for (int k = kb; k < ke && ok; ++k) {
+        ok = __all_sync(0xffffffffu, wait(&bar.full[st.slot], st.phase));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = smem0 + st.slot * R::kStageBytes, b = a + R::kABytes;
+        const uint64_t da = kAMn ? smem_desc_mn128(a) : smem_desc_k128(a);
+        const uint64_t db = kBMn ? smem_desc_mn128(b) : smem_desc_k128(b);
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < kBlockK / 16; ++q)
+            mma_bf16<kPair>(tmem + acc.slot * kTileN, da + q * kAStep, db + q * kBStep, idesc,
+                            q > 0 || k > kb);
+          mma_commit_group<kPair>(&bar.empty[st.slot]);
+          if (k + 1 == ke) mma_commit_group<kPair>(&bar.acc_full[acc.slot]);
+        }
+        __syncwarp();
+        st.next();
+      }
+      acc.next();
+    }
+    if (!ok) {
+      if (elect_one()) {
+        if (p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+        mma_commit_group<kPair>(&bar.drain);
+      }
+      __syncwarp();
+      wait(&bar.drain, 0);
+    }
+  } else if (warp >= 4 && !kSplit) {
+    // ---------------- the rest of the formula, and output ----------------
+    const int quarter = warp & 3;       // TMEM lanes of this warp
+    const int j = (warp - 4) >> 2;      // half of the columns
+    const int m = quarter * 32 + lane;  // row of the CTA's part of the tile
+    const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u;
+    constexpr int kWarpCols = kCols / 2;
+    Ring<2> acc;
+    for (int64_t i = first; i < tiles; i += step) {
+      const Tile t = tile_at(i);
+      const int half = half_of<kMode, kPair>(t);
+      const int mine0 = kPair == 2 ? rank * half : 0;
+      const int used = kPair == 2 ? max(0, min(half, t.used - mine0)) : t.used;
+      const int write = kPair == 2 ? max(0, min(half, t.write - mine0)) : t.write;
+      const int64_t row = t.row0 + mine0 + m;
+      const bool mine = m < used;
+      const bool work = quarter * 32 < write;  // any row of the warp
+      const bool mma = t.blocks > 0;
+      if (mma) {
+        // after a wait that gave up, the rest is walked without waiting
+        if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
+        tc_fence_after();
+      } else if (kMode == kFfnWeightGrad && p.accumulate) {
+        continue;
+      }
+      const bool zero = !mma || !mine;
+      const uint32_t ta = taddr + acc.slot * kTileN;
+      if (work) {
+        Kept next;
+        if constexpr (kMode == kFfnGatedGrad)
+          if (mine) load_kept(p, row, t.n0 + j * kWarpCols, &next);
+#pragma unroll 1
+        for (int c = 0; c < kWarpCols; c += 32) {
+          uint32_t d[32], d2[32];
+          const int c0 = j * kWarpCols + c;
+          if (mma) {
+            tmem_load32(ta + c0, d);
+            if constexpr (kMode == kFfnGated) tmem_load32(ta + kTileN / 2 + c0, d2);
+            tmem_load_wait(d);
+            if constexpr (kMode == kFfnGated) tmem_load_wait(d2);
+          }
+          if (mma && c + 32 == kWarpCols) {  // read: a later tile may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (kPair == 2)
+                mbar_arrive_cluster(cluster_map(&bar.acc_empty[acc.slot], 0));
+              else
+                mbar_arrive(&bar.acc_empty[acc.slot]);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            float v[16], u[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              v[x] = ok ? __uint_as_float(d[q + x]) : __uint_as_float(0x7fffffffu);
+              u[x] = kMode != kFfnGated ? 0.f
+                     : ok               ? __uint_as_float(d2[q + x])
+                                        : __uint_as_float(0x7fffffffu);
+            }
+            const int col = t.n0 + c0 + q;
+            Kept now = next;
+            if constexpr (kMode == kFfnGatedGrad)
+              if (mine && (c + q + 16 < kWarpCols)) load_kept(p, row, col + 16, &next);
+            if (m < write && col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, u, now);
+          }
+        }
+      } else if (mma && lane == 0) {
+        if constexpr (kPair == 2)
+          mbar_arrive_cluster(cluster_map(&bar.acc_empty[acc.slot], 0));
+        else
+          mbar_arrive(&bar.acc_empty[acc.slot]);
+      }
+      if (mma) acc.next();
+    }
+    if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+    tc_fence_before();
+  }
+
+  if constexpr (kSplit) {
+    // ---------------- a tile shared by the cluster ----------------
+    // Each CTA gets the sums of kCols / split columns from all of them: 16-byte
+    // pieces of fp32, rows[source][row][piece ^ row % 8] over the stages.
+    const Tile t = tile_at(first);
+    const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
+    const int kb = part(t.blocks, rank), ke = part(t.blocks, rank + 1);
+    const int quarter = warp & 3, j = (warp - 4) >> 2, m = quarter * 32 + lane;
+    if (warp >= 4 && kb < ke) {
+      ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
+      tc_fence_after();
+    }
+    __syncwarp();
+    cluster_arrive_release();  // this CTA's products are done with its stages
+    cluster_wait();
+    if (warp >= 4 && quarter * 32 < t.used) {
+      const uint32_t ta = tmem + (uint32_t)(quarter * 32) * 65536u + j * (kTileN / 2);
+#pragma unroll 1
+      for (int c = 0; c < kTileN / 2; c += 32) {
+        uint32_t d[32];
+        if (kb < ke) {
+          tmem_load32(ta + c, d);
+          tmem_load_wait(d);
+        }
+#pragma unroll
+        for (int q = 0; q < 32; q += 16) {
+          // gated: a CTA's gate columns, then as many up columns
+          const int cc = kMode == kFfnGated ? c + q : j * (kTileN / 2) + c + q;
+          const int per = kMode == kFfnGated ? wide / 2 : wide;
+          const int to = cc / per;
+          const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
+          const uint32_t base = cluster_map(smem, to) + (uint32_t)((rank * kTileM + m) * wide * 4);
+          if (m < t.used)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float v[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                v[y] = kb == ke ? 0.f
+                       : ok     ? __uint_as_float(d[q + 4 * x + y])
+                                : __uint_as_float(0x7fffffffu);
+              st_cluster_v4(base + (uint32_t)(((piece + x) ^ (m & 7)) * 16), v[0], v[1], v[2],
+                            v[3]);
+            }
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait();
+    if (warp >= 4 && !(kMode == kFfnWeightGrad && p.accumulate && t.blocks == 0)) {
+      const int per = kMode == kFfnGated ? wide / 2 : wide, groups = per / 16;
+      const float *in = reinterpret_cast<const float *>(smem);
+      for (int i = threadIdx.x - 128; i < t.write * groups; i += 32 * kEpilogueWarps) {
+        const int r = i / groups, g = i - r * groups;
+        const int col = t.n0 + rank * per + g * 16;
+        if (col >= p.N) continue;
+        const bool zero = r >= t.used || t.blocks == 0;
+        float v[16], u[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = u[x] = 0.f;
+        if (!zero)
+          for (int s = 0; s < S; ++s) {
+            const float *from = in + (int64_t)(s * kTileM + r) * wide;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float4 a =
+                  *reinterpret_cast<const float4 *>(from + (((g * 4 + x) ^ (r & 7)) * 4));
+              v[4 * x] += a.x, v[4 * x + 1] += a.y, v[4 * x + 2] += a.z, v[4 * x + 3] += a.w;
+              if constexpr (kMode == kFfnGated) {
+                const float4 b = *reinterpret_cast<const float4 *>(
+                    from + (((per / 4 + g * 4 + x) ^ (r & 7)) * 4));
+                u[4 * x] += b.x, u[4 * x + 1] += b.y, u[4 * x + 2] += b.z, u[4 * x + 3] += b.w;
+              }
+            }
+          }
+        Kept k{};
+        if constexpr (kMode == kFfnGatedGrad)
+          if (!zero) load_kept(p, t.row0 + r, col, &k);
+        finish16<kMode>(p, t.row0 + r, t.e, col, zero, v, u, k);
+      }
+    }
+    if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
+  }
+  __syncwarp();
+  __syncthreads();
+  if constexpr (kPair == 2) {
+    // neither CTA leaves while the other may still arrive on its barriers, read
+    // its operands or write into its TMEM
+    cluster_arrive_release();
+    cluster_wait();
+  }
+  if (warp == 1) tmem_dealloc_group<kPair>(tmem, kTmemColumns);
+}
+
+// Tensor maps of an expert's rows for the weight gradient: the given ones with
+// their rows ending at the expert's last.  A block per map: 2 * e + (0: a, 1: b).
+__global__ void ffn_segment_maps_kernel(const __grid_constant__ Maps maps, Segments s,
+                                        CUtensorMap *out) {
+  const int e = blockIdx.x >> 1;
+  griddep_wait();
+  const uint4 *from = reinterpret_cast<const uint4 *>(blockIdx.x & 1 ? &maps.b : &maps.a[0]);
+  uint4 *to = reinterpret_cast<uint4 *>(out + blockIdx.x);
+  if (threadIdx.x < sizeof(CUtensorMap) / 16) to[threadIdx.x] = from[threadIdx.x];
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const SegmentRows r = segment_rows(s, e);
+    tma_replace_rows(out + blockIdx.x, (uint32_t)max((int64_t)1, r.first + r.used));
+  }
+}
+
+// A BF16 array [z, y, x] (x contiguous, rows y_stride apart) copied in boxes of
+// 64 x box_y x 1, zeros outside.
+bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t z,
+              int64_t y_stride, int box_y) {
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+  const cuuint64_t strides[2] = {(cuuint64_t)(2 * y_stride),
+                                 (cuuint64_t)(2 * y_stride * (z > 1 ? y : 1))};
+  const cuuint32_t box[3] = {(cuuint32_t)kBlockK, (cuuint32_t)box_y, 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kMode, int kPair, bool kSplit>
+cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
+                        cudaStream_t s) {
+  using R = Ring_<kPair>;
+  const auto kernel = ffn_kernel<kMode, kPair, kSplit>;
+  const size_t cum = kMode == kFfnWeightGrad ? 0 : sizeof(int) * (p.s.E + 1);
+  const size_t smem = 1024 + (size_t)R::kStages * R::kStageBytes + cum;
+  int dev = 0;
+  cudaError_t e = launch_geometry(reinterpret_cast<const void *>(kernel), kThreads, smem, &dev,
+                                  nullptr);
+  if (e != cudaSuccess) return e;
+  const int64_t groups = kSplit ? tiles : std::max<int64_t>(1, std::min<int64_t>(use / share, tiles));
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)(groups * share));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)share;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = share > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&lc, kernel, maps, p);
+}
+
+template <int kMode>
+cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
+  constexpr bool kAMn = kMode == kFfnWeightGrad;
+  FfnParams p = p0;
+  Maps maps;
+  bool ok = true;
+  if constexpr (kAMn) {
+    ok = make_map(&maps.a[0], p.a, p.M, p.s.rows, 1, p.a_stride, 64);
+    for (int i = 1; i < kRowMaps; ++i) maps.a[i] = maps.a[0];
+    ok = ok && make_map(&maps.b, p.b, p.N, p.s.rows, 1, p.b_stride, 64);
+  } else {
+    for (int i = 0; i < kRowMaps; ++i)
+      ok = ok && make_map(&maps.a[i], p.a, p.K, p.s.rows, 1, p.a_stride, kRowStep << i);
+    if constexpr (kMode == kFfnGated)
+      ok = ok && make_map(&maps.b, p.b, p.K, 2 * (int64_t)p.N, p.s.E, p.K, 128);
+    else if constexpr (kMode == kFfnProduct)
+      ok = ok && make_map(&maps.b, p.b, p.K, p.N, p.s.E, p.K, 128);
+    else
+      ok = ok && make_map(&maps.b, p.b, p.N, p.K, p.s.E, p.N, 64);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int use = sms_to_use(dev, sm_cap);
+  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
+  const int64_t tiles_n = (p.N + kCols - 1) / kCols;
+  // at most this many row tiles of `m` rows hold rows (every expert's last one may be partial)
+  const auto tiles_of = [&](int m) {
+    const int64_t r = kAMn ? (int64_t)p.s.E * ((p.M + m - 1) / m)
+                           : std::min<int64_t>(p.max_segments, p.s.E) + (p.s.rows - 1) / m;
+    return r * tiles_n;
+  };
+  if (p.s.cnt_e == nullptr) {
+    // Few tiles: clusters of 2, 4 or 8 share each one's reduction, as many as there
+    // are SMs for.
+    const int64_t tiles = tiles_of(kTileM);
+    const int64_t blocks = ((kAMn ? p.s.rows : p.K) + kBlockK - 1) / kBlockK;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= use && blocks >= split * 4) split *= 2;
+    if (split > 1) {
+      p.split = split;
+      return launch_form<kMode, 1, true>(maps, p, tiles, use, split, s);
+    }
+  } else if constexpr (kAMn) {
+    e = launch_pdl(ffn_segment_maps_kernel, (unsigned)(2 * p.s.E), 32, 0, s, maps, p.s,
+                   static_cast<CUtensorMap *>(p.seg_maps));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM), use, 1, s);
+}
+
+}  // namespace
+
+size_t ffn_workspace(int mode, const FfnParams &p) {
+  return mode == kFfnWeightGrad && p.s.cnt_e != nullptr ? 2 * sizeof(CUtensorMap) * p.s.E : 0;
+}
+
+cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s) {
+  switch (mode) {
+    case kFfnGated:
+      return launch_mode<kFfnGated>(p, sm_cap, s);
+    case kFfnGatedGrad:
+      return launch_mode<kFfnGatedGrad>(p, sm_cap, s);
+    case kFfnProduct:
+      return launch_mode<kFfnProduct>(p, sm_cap, s);
+    case kFfnProductT:
+      return launch_mode<kFfnProductT>(p, sm_cap, s);
+    default:
+      return launch_mode<kFfnWeightGrad>(p, sm_cap, s);
+  }
+}
+
+}  // namespace ep

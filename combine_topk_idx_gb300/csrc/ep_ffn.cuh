@@ -1,0 +1,56 @@
+// The products of the trained feed-forward block: parameters and launchers.
+#pragma once
+
+#include "ep_internal.cuh"
+
+namespace ep {
+
+enum FfnMode { kFfnGated, kFfnGatedGrad, kFfnProduct, kFfnProductT, kFfnWeightGrad };
+
+// The rows of each expert: of an expanded layout, or (cnt_e NULL, E = 1) all rows.
+struct Segments {
+  const int32_t *psum_e, *cnt_e;
+  int E, fixed_cap, zero_padding;
+  int64_t rows;             // rows allocated
+};
+
+struct SegmentRows {
+  int64_t first, used, write;  // first row, rows in use, rows to write (then zeros)
+};
+
+__device__ __forceinline__ SegmentRows segment_rows(const Segments &s, int e) {
+  if (s.cnt_e == nullptr) return {0, s.rows, s.rows};
+  const int64_t cnt = __ldg(s.cnt_e + e);
+  if (s.fixed_cap > 0) {
+    const int64_t n = cnt < s.fixed_cap ? cnt : s.fixed_cap;
+    return {(int64_t)e * s.fixed_cap, n, n};
+  }
+  const int64_t r0 = __ldg(s.psum_e + e);
+  const int64_t left = max((int64_t)0, s.rows - r0);
+  const int64_t used = min(cnt, left);
+  return {r0, used, s.zero_padding ? min((int64_t)__ldg(s.psum_e + e + 1) - r0, left) : used};
+}
+
+struct FfnParams {
+  Segments s;
+  int64_t max_segments;     // experts that can have rows
+  // a: the rows [rows, K] (weight gradient: the gradient [rows, M]); b: the matrix of
+  // each expert (weight gradient: the rows [rows, N]); strides of rows, in elements
+  const uint16_t *a, *b;
+  int64_t a_stride, b_stride;
+  int M, N, K;              // N: columns of the output (gated: F); M: weight gradient only
+  const uint16_t *kept;     // gated gradient: [rows, 2N] gate | up of the forward
+  uint16_t *out;            // gated: act; gated gradient: of gate_up; else the output
+  uint16_t *out2;           // gated: gate_up; gated gradient: act; may be nullptr
+  int out32, out2_32;       // every row (and its up half) starts on a 32-byte boundary
+  int f32, accumulate;      // weight gradient: out is fp32; is added to
+  int split;                // CTAs that share a tile's reduction
+  void *seg_maps;           // workspace: two tensor maps per expert
+  unsigned *err;            // the handle's error word (EP_ERRBIT_TIMEOUT), or nullptr
+};
+
+// Bytes of workspace (FfnParams::seg_maps, 128-byte aligned); 0: none.
+size_t ffn_workspace(int mode, const FfnParams &p);
+cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s);
+
+}  // namespace ep

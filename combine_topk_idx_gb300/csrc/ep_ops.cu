@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include "ep_clip.cuh"
+#include "ep_ffn.cuh"
 #include "ep_host.cuh"
 
 namespace ep {
@@ -69,6 +71,58 @@ SfLayout rows_sf(const ep_handle *h, int64_t n) {
 ep_status check_norm(int32_t num_tokens, int32_t hidden) {
   if (num_tokens < 0 || hidden < 8 || hidden % 8 != 0) return EP_ERR_INVALID_ARG;
   return hidden > EP_MAX_HIDDEN ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+// A dimension of a matrix that the tensor cores take.
+bool gemm_size(int64_t n) { return n >= 8 && n % 8 == 0; }
+
+// Checks what the calls of the feed-forward block share: the rows (h may be NULL:
+// `rows` rows, one matrix), the sizes of the matrix.
+ep_status check_ffn(const ep_handle *h, int64_t rows, int64_t n, int64_t k, int64_t most_n) {
+  if (rows < 0 || !gemm_size(n) || !gemm_size(k)) return EP_ERR_INVALID_ARG;
+  if (n > most_n || k > EP_MAX_GEMM || rows > 0x7fffffffLL) return EP_ERR_UNSUPPORTED;
+  if (h == nullptr) return EP_OK;
+  if (!h->cfg.do_expand) return EP_ERR_UNSUPPORTED;
+  if (rows != h->rows_alloc) return EP_ERR_INVALID_ARG;
+  return check_device(h);
+}
+
+bool row_stride(int64_t stride, int64_t n) { return stride >= n && stride % 8 == 0; }
+
+FfnParams ffn_params(const ep_handle *h, int64_t rows) {
+  FfnParams p{};
+  p.s.E = 1;
+  p.s.rows = rows;
+  p.max_segments = 1;
+  if (h == nullptr) return p;
+  const ep_config &c = h->cfg;
+  p.s.psum_e = h->lp.psum_e;
+  p.s.cnt_e = h->lp.cnt_e;
+  p.s.E = c.num_experts;
+  p.s.fixed_cap = h->lp.fixed_cap;
+  p.s.zero_padding = c.do_zero_padding;
+  p.max_segments = (int64_t)c.num_tokens * c.num_topk;
+  p.err = reinterpret_cast<unsigned *>(h->lp.ctrl + kCtrlError);
+  return p;
+}
+
+bool rows_on_32(const void *p, int64_t n) { return aligned(p, 32) && n % 16 == 0; }
+
+ep_status run_ffn(int mode, FfnParams &p, const ep_handle *h, ep_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t bytes = ffn_workspace(mode, p);
+  void *ws = nullptr;
+  if (bytes > 0) {
+    const cudaError_t e = workspace_alloc(bytes, s, &ws);
+    if (e != cudaSuccess) return cuda_status(e);
+    p.seg_maps = ws;
+  }
+  cudaError_t e = launch_ffn(mode, p, h != nullptr ? h->cfg.num_sms : 0, s);
+  if (ws != nullptr) {
+    const cudaError_t f = workspace_free(ws, s);
+    if (e == cudaSuccess) e = f;
+  }
+  return cuda_status(e);
 }
 
 }  // namespace
@@ -340,6 +394,128 @@ ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const void *a
   p.err = reinterpret_cast<unsigned *>(h->lp.ctrl + ep::kCtrlError);
   return ep::cuda_status(
       ep::launch_expert_gemm(p, c.num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ep_status ep_ffn_gated(const ep_handle *h, int64_t rows, int32_t ffn, int32_t k, const void *x,
+                       int64_t x_stride, const void *w, void *act, void *gate_up,
+                       ep_stream_t stream) {
+  if (const ep_status st = ep::check_ffn(h, rows, ffn, k, EP_MAX_GEMM / 2); st != EP_OK) return st;
+  if (act == nullptr && gate_up == nullptr && rows > 0) return EP_ERR_INVALID_ARG;
+  if (!ep::row_stride(x_stride, k)) return EP_ERR_INVALID_ARG;
+  if (rows == 0) return EP_OK;
+  if (!have(x, 16) || !have(w, 16) || !maybe(act, 16) || !maybe(gate_up, 16))
+    return EP_ERR_INVALID_ARG;
+  ep::FfnParams p = ep::ffn_params(h, rows);
+  p.a = static_cast<const uint16_t *>(x);
+  p.a_stride = x_stride;
+  p.b = static_cast<const uint16_t *>(w);
+  p.N = ffn;
+  p.K = k;
+  p.out = static_cast<uint16_t *>(act);
+  p.out2 = static_cast<uint16_t *>(gate_up);
+  p.out32 = ep::rows_on_32(act, ffn);
+  p.out2_32 = ep::rows_on_32(gate_up, ffn);
+  return ep::run_ffn(ep::kFfnGated, p, h, stream);
+}
+
+ep_status ep_ffn_gated_backward(const ep_handle *h, int64_t rows, int32_t ffn, int32_t n,
+                                const void *grad_out, int64_t grad_out_stride, const void *w,
+                                const void *gate_up, void *grad_gate_up, void *act,
+                                ep_stream_t stream) {
+  if (const ep_status st = ep::check_ffn(h, rows, ffn, n, EP_MAX_GEMM / 2); st != EP_OK) return st;
+  if (!ep::row_stride(grad_out_stride, n)) return EP_ERR_INVALID_ARG;
+  if (rows == 0) return EP_OK;
+  if (!have(grad_out, 16) || !have(w, 16) || !have(gate_up, 16) || !have(grad_gate_up, 16) ||
+      !maybe(act, 16))
+    return EP_ERR_INVALID_ARG;
+  ep::FfnParams p = ep::ffn_params(h, rows);
+  p.a = static_cast<const uint16_t *>(grad_out);
+  p.a_stride = grad_out_stride;
+  p.b = static_cast<const uint16_t *>(w);
+  p.N = ffn;
+  p.K = n;
+  p.kept = static_cast<const uint16_t *>(gate_up);
+  p.out = static_cast<uint16_t *>(grad_gate_up);
+  p.out2 = static_cast<uint16_t *>(act);
+  p.out32 = ep::rows_on_32(grad_gate_up, ffn);
+  p.out2_32 = ep::rows_on_32(act, ffn);
+  return ep::run_ffn(ep::kFfnGatedGrad, p, h, stream);
+}
+
+ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int32_t k, const void *a,
+                         int64_t a_stride, const void *w, int32_t transposed, void *out,
+                         ep_stream_t stream) {
+  if (const ep_status st = ep::check_ffn(h, rows, n, k, EP_MAX_GEMM); st != EP_OK) return st;
+  if (!ep::row_stride(a_stride, k) || transposed < 0 || transposed > 1) return EP_ERR_INVALID_ARG;
+  if (rows == 0) return EP_OK;
+  if (!have(a, 16) || !have(w, 16) || !have(out, 16)) return EP_ERR_INVALID_ARG;
+  ep::FfnParams p = ep::ffn_params(h, rows);
+  p.a = static_cast<const uint16_t *>(a);
+  p.a_stride = a_stride;
+  p.b = static_cast<const uint16_t *>(w);
+  p.N = n;
+  p.K = k;
+  p.out = static_cast<uint16_t *>(out);
+  p.out32 = ep::rows_on_32(out, n);
+  return ep::run_ffn(transposed ? ep::kFfnProductT : ep::kFfnProduct, p, h, stream);
+}
+
+ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
+                             const void *grad, int64_t grad_stride, const void *a,
+                             int64_t a_stride, void *grad_w, int32_t grad_w_is_fp32,
+                             int32_t accumulate, ep_stream_t stream) {
+  if (const ep_status st = ep::check_ffn(h, rows, n, k, EP_MAX_GEMM); st != EP_OK) return st;
+  if (!ep::row_stride(grad_stride, n) || !ep::row_stride(a_stride, k) || grad_w_is_fp32 < 0 ||
+      grad_w_is_fp32 > 1 || accumulate < 0 || accumulate > 1)
+    return EP_ERR_INVALID_ARG;
+  if (!have(grad_w, 16)) return EP_ERR_INVALID_ARG;
+  ep::FfnParams p = ep::ffn_params(h, rows);
+  if (rows == 0) {
+    if (accumulate) return EP_OK;
+    const size_t bytes = (size_t)p.s.E * n * k * (grad_w_is_fp32 ? 4 : 2);
+    return ep::cuda_status(
+        cudaMemsetAsync(grad_w, 0, bytes, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  if (!have(grad, 16) || !have(a, 16)) return EP_ERR_INVALID_ARG;
+  p.a = static_cast<const uint16_t *>(grad);
+  p.a_stride = grad_stride;
+  p.b = static_cast<const uint16_t *>(a);
+  p.b_stride = a_stride;
+  p.M = n;
+  p.N = k;
+  p.out = static_cast<uint16_t *>(grad_w);
+  p.out32 = ep::rows_on_32(grad_w, k);
+  p.f32 = grad_w_is_fp32;
+  p.accumulate = accumulate;
+  return ep::run_ffn(ep::kFfnWeightGrad, p, h, stream);
+}
+
+ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *outs,
+                        const int64_t *numels, const uint8_t *is_fp32, float max_norm, float *norm,
+                        ep_stream_t stream) {
+  if (count < 0 || !(max_norm >= 0.f) || !maybe(norm, 4)) return EP_ERR_INVALID_ARG;
+  if (outs == nullptr && norm == nullptr) return EP_ERR_INVALID_ARG;
+  if (count > 0 && (grads == nullptr || numels == nullptr || is_fp32 == nullptr))
+    return EP_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    if (numels[i] < 0 || is_fp32[i] > 1) return EP_ERR_INVALID_ARG;
+    if (numels[i] > (1LL << 40)) return EP_ERR_UNSUPPORTED;
+    if (numels[i] == 0) continue;
+    const uintptr_t size = is_fp32[i] ? 4 : 2;
+    if (!have(grads[i], size) || (outs != nullptr && !have(outs[i], size)))
+      return EP_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return ep::cuda_status(e);
+  const ep::GradList l{count, grads, outs, numels, is_fp32};
+  const int sms = ep::device_sm_count(dev);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void *ws = nullptr;
+  cudaError_t e = ep::workspace_alloc(ep::clip_workspace(l, sms), s, &ws);
+  if (e != cudaSuccess) return ep::cuda_status(e);
+  e = ep::launch_clip(l, max_norm, norm, ws, sms, s);
+  const cudaError_t f = ep::workspace_free(ws, s);
+  return ep::cuda_status(e != cudaSuccess ? e : f);
 }
 
 }  // extern "C"

@@ -22,6 +22,51 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t columns) {
                : "memory");
 }
 
+// The same over a pair of CTAs: one warp of each executes it, the columns are
+// taken in both.
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc_group(uint32_t *smem_dst, uint32_t columns) {
+  if constexpr (kCtas == 1) {
+    tmem_alloc(smem_dst, columns);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(smem_dst)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_dealloc_group(uint32_t addr, uint32_t columns) {
+  if constexpr (kCtas == 1)
+    tmem_dealloc(addr, columns);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns)
+                 : "memory");
+}
+
+// 32 columns of this warp's 32 lanes: lane l gets (l, column 0..31) from addr.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// Waits for this thread's TMEM loads and orders the uses of r after them.
+template <int N>
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // 64 columns of this warp's 32 lanes: lane l gets (l, column 0..63) from addr.
 __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t *r) {
   asm volatile(
@@ -96,6 +141,110 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+// ---- bf16 products ----
+// Descriptor of a tile whose rows run along the reduction (its other dimension
+// contiguous): blocks of 64 columns x 64 reduction rows of 128 bytes in 128-byte
+// swizzle (what a tiled TMA load of such a box writes), 8192 bytes apart along the
+// columns, eight reduction rows 1024 bytes apart; + 2048 bytes per 16 reduction rows.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(8192 >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Instruction descriptor: bf16 x bf16 -> fp32, M x N; a_mn, b_mn: the operand's
+// rows run along the reduction.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 |
+         (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+
+// D (TMEM) = A B^T (+ D if accumulate); K = 16; one thread issues it, for a pair
+// of CTAs one of the first CTA.
+template <int kCtas>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool accumulate) {
+  if constexpr (kCtas == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// Arrives on `bar`, for a pair on the barrier at that offset in both CTAs, when
+// the products issued so far by this thread are done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit_group(uint64_t *bar) {
+  if constexpr (kCtas == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Tiled TMA load of the map's box at (x, y, z) into this CTA, counted on the
+// barrier at the shared::cluster address `bar`, which a pair's first CTA holds.
+template <int kCtas>
+__device__ __forceinline__ void tma_load_3d(void *sdst, const CUtensorMap *map, int x, int y,
+                                            int z, uint32_t bar) {
+  if constexpr (kCtas == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(sdst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(sdst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Ends the rows (dimension 1) of a tensor map in global memory at `rows`, and makes
+// the change visible to later readers of the map.
+__device__ __forceinline__ void tma_replace_rows(CUtensorMap *map, uint32_t rows) {
+  asm volatile(
+      "tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;\n\t"
+      "fence.proxy.tensormap::generic.release.gpu;" ::"l"(map),
+      "r"(rows)
+      : "memory");
+}
+// Before the first use of a map that another kernel wrote.
+__device__ __forceinline__ void tma_acquire_map(const CUtensorMap *map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
+// ---- clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// shared::cluster address of what `p` is in CTA `cta` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(const void *p, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+               "f"(c), "f"(d)
+               : "memory");
 }
 
 // Tiled TMA load of the map's box at (x, y), counted on `bar`.

@@ -498,6 +498,97 @@ EP_API ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const 
                                 const float *a_sf, const void *w_fp8, const float *w_sf,
                                 void *out, ep_stream_t stream);
 
+/* ---- the trained feed-forward block ------------------------------------- */
+
+/*
+ * The BF16 products of a gated feed-forward block whose weights train, forward and
+ * backward.  h: the handle of an expanded layout (do_expand, fixed capacity too;
+ * else EP_ERR_UNSUPPORTED): one matrix per expert, `rows` its rows_alloc, each row
+ * meets its expert's matrix.  Or NULL: one matrix and `rows` rows, all in use (a
+ * shared expert).  Below E is the number of experts, 1 without a handle.
+ *
+ * Rows and padding as for the operators above.  What rows that are not in use hold
+ * (infinities and NaN too) reaches no other row and no weight's gradient.
+ * Matrices are BF16, dense; arrays of rows that the products read (x, grad_out, a,
+ * grad) may be row-strided (elements, a multiple of 8, at least the row's length).
+ * Sizes n, k, ffn: multiples of 8, at most EP_MAX_GEMM (ffn: half of that).
+ * 16-byte aligned.  Sums are fp32, each output is rounded once.  The same call gives
+ * the same bits each time.  A device-side wait that gives up leaves NaN in the tiles
+ * it was for and, with a handle, sets EP_ERRBIT_TIMEOUT.
+ */
+
+/*
+ * ep_ffn_gated -- both projections, the activation and the product in one kernel.
+ *
+ * x: BF16 [rows, k].  w: BF16 [E, 2 * ffn, k], ffn rows of the gate, then ffn of up.
+ *   g = x Wg^T, u = x Wu^T;  act = g * sigmoid(g) * u   (from the fp32 sums)
+ * Outputs, at least one given: act BF16 [rows, ffn]; gate_up BF16 [rows, 2 * ffn],
+ *   g then u, for ep_ffn_gated_backward.
+ */
+EP_API ep_status ep_ffn_gated(const ep_handle *h, int64_t rows, int32_t ffn, int32_t k,
+                              const void *x, int64_t x_stride, const void *w, void *act,
+                              void *gate_up, ep_stream_t stream);
+
+/*
+ * ep_ffn_gated_backward -- gradient of gate and up through the down projection.
+ *
+ * grad_out: BF16 [rows, n], gradient of the block's output act W^T, w: BF16
+ *   [E, n, ffn], the down projection.  gate_up: as ep_ffn_gated wrote it.
+ * With d = grad_out W (fp32), g, u of gate_up, s = sigmoid(g):
+ *   grad_gate_up BF16 [rows, 2 * ffn]: d * u * s * (1 + g * (1 - s)), then d * g * s;
+ *   act BF16 [rows, ffn], or NULL: g * s * u, which the down projection's
+ *     ep_ffn_weight_grad takes (so that the forward need not keep it).
+ */
+EP_API ep_status ep_ffn_gated_backward(const ep_handle *h, int64_t rows, int32_t ffn, int32_t n,
+                                       const void *grad_out, int64_t grad_out_stride,
+                                       const void *w, const void *gate_up, void *grad_gate_up,
+                                       void *act, ep_stream_t stream);
+
+/*
+ * ep_ffn_product -- the rows' product with a matrix: the down projection, and with
+ * `transposed` the gradient of the rows that went into a projection.
+ *
+ * a: BF16 [rows, k].  w: BF16 [E, n, k], out = a W^T; transposed: [E, k, n], out = a W.
+ * out: BF16 [rows, n].
+ */
+EP_API ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
+                                const void *a, int64_t a_stride, const void *w,
+                                int32_t transposed, void *out, ep_stream_t stream);
+
+/*
+ * ep_ffn_weight_grad -- gradient of a projection's matrix.
+ *
+ * grad: BF16 [rows, n], gradient of the projection's output; a: BF16 [rows, k], its input.
+ * grad_w: fp32 or BF16 [E, n, k]: sum over the rows r of expert e of
+ *   grad[r, i] * a[r, j]; with `accumulate` added to what grad_w holds (in fp32, then
+ *   rounded).  An expert without rows has zeros, or is left as it is.
+ * With a handle it uses a stream-ordered workspace of 256 bytes per expert.
+ */
+EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
+                                    const void *grad, int64_t grad_stride, const void *a,
+                                    int64_t a_stride, void *grad_w, int32_t grad_w_is_fp32,
+                                    int32_t accumulate, ep_stream_t stream);
+
+/*
+ * ep_clip_grads -- the global norm of many gradients, and their clipping to it.
+ *
+ * count: tensors; grads, numels, is_fp32 and outs are HOST arrays of that length,
+ *   read before the call returns.  Tensor i: numels[i] elements, fp32 or BF16,
+ *   contiguous, aligned to its element's size; empty ones are skipped.
+ *   norm = sqrt(sum of all squares), fp32 sums of at most 32 squares joined in fp64;
+ *     finite whenever fp32 holds it, though the squares may not be.
+ *   c = 1 if norm + 1e-6 <= max_norm, else max_norm / (norm + 1e-6): a norm that is
+ *     infinite makes c zero, one that is NaN makes it NaN.
+ * outs[i]: c * grads[i] in fp32, rounded to the tensor's type; may be grads[i] itself
+ *   (and is then not written if c = 1), else overlaps no gradient and no other
+ *   output.  outs NULL: the norm only.
+ * norm: device fp32, or NULL if outs is given.  max_norm: >= 0, or infinite.
+ * Uses a stream-ordered workspace of 8 bytes per CTA.  The same bits each time.
+ */
+EP_API ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *outs,
+                               const int64_t *numels, const uint8_t *is_fp32, float max_norm,
+                               float *norm, ep_stream_t stream);
+
 /* ---- layout without any allocation ------------------------------------- */
 
 /*

@@ -102,3 +102,35 @@ def expert_gemm(a, a_sf, w, w_sf, starts, counts):
         wv = w[e] * np.repeat(np.repeat(w_sf[e], 128, axis=0)[:n], 128, axis=1)
         out[r0:r1] = av @ wv.T
     return out
+
+
+# ---- the trained feed-forward block: rows [starts[e], + counts[e]) meet matrix e ----
+
+def segment_product(a, w, starts, counts, transposed=False):
+    """a w[e]^T, or with `transposed` a w[e]; other rows 0."""
+    out = np.zeros((a.shape[0], w.shape[2] if transposed else w.shape[1]))
+    for e in range(w.shape[0]):
+        rows = slice(starts[e], starts[e] + counts[e])
+        out[rows] = a[rows] @ (w[e] if transposed else w[e].T)
+    return out
+
+
+def segment_outer(grad, a, starts, counts):
+    """[E, n, k]: sum over the rows of e of grad[r]^T a[r]."""
+    return np.stack([grad[s:s + c].T @ a[s:s + c] for s, c in zip(starts, counts)])
+
+
+def gated_slopes(gate_up):
+    """What the gradient of the activation is multiplied by for gate | up, and the activation."""
+    F = gate_up.shape[1] // 2
+    g, u = gate_up[:, :F], gate_up[:, F:]
+    sg = _sigmoid(g)
+    return np.concatenate([u * sg * (1 + g * (1 - sg)), g * sg], axis=1), g * sg * u
+
+
+def global_norm(grads):
+    """2-norm of all arrays together, safe from overflow."""
+    top = max((float(np.abs(g).max()) for g in grads if g.size), default=0.0)
+    if top == 0.0 or not np.isfinite(top):
+        return top
+    return top * float(np.sqrt(sum(float(((g / top) ** 2).sum()) for g in grads)))
