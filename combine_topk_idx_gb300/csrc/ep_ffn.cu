@@ -37,6 +37,9 @@
 // hold NaN.  However it ends, the CTA waits (bounded) for what it has in flight,
 // frees its TMEM and returns.
 #include <algorithm>
+#include <cstdlib>
+#include <mutex>
+#include <vector>
 
 #include "ep_ffn.cuh"
 #include "ep_ptx.cuh"
@@ -53,7 +56,23 @@ constexpr int kBoxBytes = 64 * kBlockK * 2;  // 64 columns of a 64-element block
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
-constexpr int kRaster = 16;    // row tiles that pass over the columns together
+// Blocks that a weight gradient in 32 bits adds up in TMEM before its sums go on in
+// registers, rounded to nearest: the tensor cores cut off what does not fit, which
+// over 4096 rows is 4.4e-6 of the result, over 512 about an eighth of that.
+constexpr int kJoin = 8;
+// registers of a control and of an epilogue thread where those sums are held:
+// 128 * 72 + 256 * 216 are the 168 * 384 of the launch
+constexpr int kControlRegs = 72, kEpilogueRegs = 216;
+#ifndef RASTER
+#define RASTER 16
+#endif
+#ifndef PROMO
+#define PROMO CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+#endif
+#ifndef BOXM
+#define BOXM 4
+#endif
+constexpr int kRaster = RASTER;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
 
@@ -64,6 +83,10 @@ struct Ring_ {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = kPair == 2 ? 6 : 4;
 };
+
+__host__ __device__ constexpr bool weight_grad(int mode) {
+  return mode == kFfnWeightGrad || mode == kFfnWeightGrad32;
+}
 
 struct Maps {
   CUtensorMap a[kRowMaps], b;
@@ -155,7 +178,7 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
   constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
   Tile t;
   int r, c;
-  if constexpr (kMode == kFfnWeightGrad) {
+  if constexpr (weight_grad(kMode)) {
     const int tr = (p.M + rows_per_tile - 1) / rows_per_tile;
     const int64_t per = (int64_t)tr * tiles_n;
     t.e = (int)(i / per);
@@ -189,7 +212,7 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
 template <int kMode, int kPair>
 __device__ __forceinline__ int half_of(const Tile &t) {
   if (kPair == 1) return kTileM;
-  if (kMode == kFfnWeightGrad) return kTileM;
+  if (weight_grad(kMode)) return kTileM;
   return ((t.write + 1) / 2 + kRowStep - 1) / kRowStep * kRowStep;
 }
 
@@ -263,9 +286,9 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
     store16_bf16(h, col, N, p.out32, zero, dg);
     store16_bf16(h + N, col, N, p.out32, zero, du);
     if (p.out2 != nullptr) store16_bf16(p.out2 + row * N + col, col, N, p.out2_32, zero, a);
-  } else if constexpr (kMode == kFfnWeightGrad) {
+  } else if constexpr (weight_grad(kMode)) {
     const int64_t at = ((int64_t)e * p.M + row) * N + col;
-    if (p.f32) {
+    if constexpr (kMode == kFfnWeightGrad32) {
       float *o = reinterpret_cast<float *>(p.out) + at;
 #pragma unroll
       for (int q = 0; q < 16; q += 4) {
@@ -299,6 +322,46 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
   }
 }
 
+// An epilogue warp has read an accumulator.
+template <int kPair>
+__device__ __forceinline__ void release(uint64_t *acc_empty) {
+  if ((threadIdx.x & 31) != 0) return;
+  if constexpr (kPair == 2)
+    mbar_arrive_cluster(cluster_map(acc_empty, 0));
+  else
+    mbar_arrive(acc_empty);
+}
+
+// Adds `parts` accumulators, as they become complete, up in sum: kTileN / 2 columns
+// from `taddr` of this warp's lanes.  Rows nobody needs (!work) are not read.
+template <int kPair>
+__device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int parts, bool work,
+                                          Ring<2> &acc, bool &ok, float (&sum)[kTileN / 2]) {
+#pragma unroll
+  for (int c = 0; c < kTileN / 2; ++c) sum[c] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
+    tc_fence_after();
+    if (work) {
+#pragma unroll
+      for (int c = 0; c < kTileN / 2; c += 32) {
+        uint32_t d[32];
+        tmem_load32(taddr + acc.slot * kTileN + c, d);
+        tmem_load_wait(d);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) sum[c + x] += __uint_as_float(d[x]);
+      }
+      tc_fence_before();
+      __syncwarp();
+    }
+    release<kPair>(&bar.acc_empty[acc.slot]);
+    acc.next();
+  }
+  if (!ok)
+#pragma unroll
+    for (int c = 0; c < kTileN / 2; ++c) sum[c] = __uint_as_float(0x7fffffffu);
+}
+
 // ---- the kernel ---------------------------------------------------------------------------
 
 template <int kMode, int kPair, bool kSplit>
@@ -306,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
   using R = Ring_<kPair>;
   constexpr int kStages = R::kStages;
-  constexpr bool kAMn = kMode == kFfnWeightGrad;
-  constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kMode == kFfnWeightGrad;
+  constexpr bool kAMn = weight_grad(kMode);
+  constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kAMn;
+  constexpr bool kF32 = kMode == kFfnWeightGrad32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
   __shared__ uint32_t tmem_slot;
@@ -332,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc_group<kPair>(&tmem_slot, kTmemColumns);
   griddep_wait();
-  if constexpr (kMode != kFfnWeightGrad) count_tiles(p, kTileM * kPair, cum, warp_sum);
+  if constexpr (!kAMn) count_tiles(p, kTileM * kPair, cum, warp_sum);
   __syncthreads();
   if constexpr (kPair == 2) {  // the other CTA's barriers are ready
     cluster_arrive_release();
@@ -343,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
   const int tiles_n = (p.N + kCols - 1) / kCols;
   int64_t tiles;
-  if constexpr (kMode == kFfnWeightGrad)
+  if constexpr (kAMn)
     tiles = (int64_t)p.s.E * ((p.M + kTileM * kPair - 1) / (kTileM * kPair)) * tiles_n;
   else
     tiles = (int64_t)cum[p.s.E] * tiles_n;
@@ -360,75 +424,80 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part_rank = kSplit ? rank : 0;
   bool ok = true;
 
-  if (warp == 0) {
+  if (warp < 4) {
+   if constexpr (kF32) setmaxnreg_dec<kControlRegs>();
+   if (warp == 0) {
     // ---------------- copies ----------------
+    // The warp stays whole and one lane of it issues, so that the copies' addresses
+    // and coordinates are in uniform registers: from a branch of lane 0 alone a
+    // stage's two copies took 540 cycles to issue, longer than its products run.
     Ring<kStages> st;
     int issued = 0;  // stages filled, counted up to kStages
+    const uint32_t full0 = kPair == 2 ? cluster_map(&bar.full[0], 0) : smem_u32(&bar.full[0]);
+    const int half_rank = kPair == 2 ? rank : 0;
     for (int64_t i = first; i < tiles && ok; i += step) {
       const Tile t = tile_at(i);
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
-      if (lane == 0 && kb < ke) {
-        const int half = half_of<kMode, kPair>(t);
-        const int mine0 = kPair == 2 ? rank * half : 0;
-        // rows copied: up to a multiple of kRowStep; of both CTAs of a pair
-        const int left = kPair == 2 ? min(half, t.used) : t.used;
-        const auto up = [](int n) { return max(0, (n + kRowStep - 1) / kRowStep * kRowStep); };
-        const int rows0 = kAMn ? kTileM : up(left);
-        const int rows1 = kPair == 1 ? 0 : kAMn ? kTileM : up(t.used - half);
-        const int rows = rank != 0 && kPair == 2 ? rows1 : rows0;
-        const uint32_t bytes = (uint32_t)((rows0 + rows1 + kTileN) * kBlockK * 2);
-        const CUtensorMap *ma = &maps.a[0], *mb = &maps.b;
-        if (kAMn && p.seg_maps != nullptr) {
-          ma = reinterpret_cast<const CUtensorMap *>(p.seg_maps) + 2 * t.e;
-          mb = ma + 1;
-          tma_acquire_map(ma);
-          tma_acquire_map(mb);
-        }
-        for (int k = kb; k < ke; ++k) {
-          if (!wait(&bar.empty[st.slot], st.phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t *a = smem + st.slot * R::kStageBytes, *b = a + R::kABytes;
-          const uint32_t full = kPair == 2 ? cluster_map(&bar.full[st.slot], 0)
-                                           : smem_u32(&bar.full[st.slot]);
+      if (kb == ke) continue;
+      const int half = half_of<kMode, kPair>(t);
+      // rows copied: up to a multiple of kRowStep; of both CTAs of a pair
+      const int left = kPair == 2 ? min(half, t.used) : t.used;
+      const auto up = [](int n) { return max(0, (n + kRowStep - 1) / kRowStep * kRowStep); };
+      const int rows0 = kAMn ? kTileM : up(left);
+      const int rows1 = kPair == 1 ? 0 : kAMn ? kTileM : up(t.used - half);
+      const int rows = half_rank ? rows1 : rows0;
+      const uint32_t bytes = (uint32_t)((rows0 + rows1 + kTileN) * kBlockK * 2);
+      const CUtensorMap *ma = &maps.a[0], *mb = &maps.b;
+      if (kAMn && p.seg_maps != nullptr) {
+        ma = reinterpret_cast<const CUtensorMap *>(p.seg_maps) + 2 * t.e;
+        mb = ma + 1;
+        tma_acquire_map(ma);
+        tma_acquire_map(mb);
+      }
+      const int a_row = (int)t.row0 + half_rank * half;
+      for (int k = kb; k < ke; ++k) {
+        ok = __all_sync(0xffffffffu, wait(&bar.empty[st.slot], st.phase ^ 1));
+        if (!ok) break;
+        uint8_t *a = smem + st.slot * R::kStageBytes, *b = a + R::kABytes;
+        const uint32_t full = full0 + st.slot * 8;
+        if (elect_one()) {
           if (kPair == 1 || rank == 0) mbar_arrive_expect_tx(&bar.full[st.slot], bytes);
           if constexpr (kAMn) {
             const int y = (int)(t.k0 + (int64_t)k * kBlockK);
 #pragma unroll
             for (int j = 0; j < kTileM / 64; ++j)
-              tma_load_3d<kPair>(a + j * kBoxBytes, ma, (int)t.row0 + mine0 + 64 * j, y, 0, full);
+              tma_load_3d<kPair>(a + j * kBoxBytes, ma, a_row + 64 * j, y, 0, full);
+          } else if (rows == kTileM) {
+            tma_load_3d<kPair>(a, &maps.a[kRowMaps - 1], k * kBlockK, a_row, 0, full);
           } else {
             int r = 0;
 #pragma unroll
-            for (int q = kRowMaps - 1; q >= 0; --q)  // rows = 16 * (sum of 2^q)
+            for (int q = kRowMaps - 2; q >= 0; --q)  // rows = 16 * (sum of 2^q)
               if (rows & (kRowStep << q)) {
-                tma_load_3d<kPair>(a + r * kBlockK * 2, &maps.a[q], k * kBlockK,
-                                   (int)t.row0 + mine0 + r, 0, full);
+                tma_load_3d<kPair>(a + r * kBlockK * 2, &maps.a[q], k * kBlockK, a_row + r, 0,
+                                   full);
                 r += kRowStep << q;
               }
           }
           if constexpr (kBMn) {
-            const int y = kMode == kFfnWeightGrad ? (int)(t.k0 + (int64_t)k * kBlockK)
-                                                  : k * kBlockK;
-            const int z = kMode == kFfnWeightGrad ? 0 : t.e;
-            const int x = t.n0 + (kPair == 2 ? rank * (kTileN / 2) : 0);
+            const int y = kAMn ? (int)(t.k0 + (int64_t)k * kBlockK) : k * kBlockK;
+            const int x = t.n0 + half_rank * (kTileN / 2);
 #pragma unroll
             for (int j = 0; j < kTileN / kPair / 64; ++j)
-              tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, z, full);
+              tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, kAMn ? 0 : t.e, full);
           } else {
             // 128 rows of the matrix per box: gate and up, or two neighbours
             const int far = kMode == kFfnGated ? p.N : kTileN / 2;
 #pragma unroll
             for (int j = 0; j < 2 / kPair; ++j)
               tma_load_3d<kPair>(b + 2 * j * kBoxBytes, mb, k * kBlockK,
-                                 t.n0 + (kPair == 2 ? rank : j) * far, t.e, full);
+                                 t.n0 + (half_rank + j) * far, t.e, full);
           }
-          st.next();
-          if (issued < kStages) ++issued;
         }
+        __syncwarp();
+        st.next();
+        if (issued < kStages) ++issued;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     if (lane == 0) {
       // The products' last arrivals on the stages' barriers: nothing else waits for
@@ -447,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 && (kPair == 1 || rank == 0)) {
+   } else if (warp == 1 && (kPair == 1 || rank == 0)) {
     // ---------------- products ----------------
     constexpr uint32_t idesc = idesc_bf16(kTileM * kPair, kTileN, kAMn, kBMn);
     constexpr int kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
@@ -458,9 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(i);
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
       if (kb == ke) continue;
-      ok = __all_sync(0xffffffffu, wait(&bar.acc_empty[acc.slot], acc.phase ^ 1));
       for (int k = kb; k < ke && ok; ++k) {
-        ok = __all_sync(0xffffffffu, wait(&bar.full[st.slot], st.phase));
+        // an accumulator takes the whole sum, or kJoin blocks of it
+        const bool begins = kF32 ? (k - kb) % kJoin == 0 : k == kb;
+        const bool ends = k + 1 == ke || (kF32 && (k + 1 - kb) % kJoin == 0);
+        if (begins) ok = __all_sync(0xffffffffu, wait(&bar.acc_empty[acc.slot], acc.phase ^ 1));
+        if (ok) ok = __all_sync(0xffffffffu, wait(&bar.full[st.slot], st.phase));
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = smem0 + st.slot * R::kStageBytes, b = a + R::kABytes;
@@ -470,25 +542,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kBlockK / 16; ++q)
             mma_bf16<kPair>(tmem + acc.slot * kTileN, da + q * kAStep, db + q * kBStep, idesc,
-                            q > 0 || k > kb);
+                            q > 0 || !begins);
           mma_commit_group<kPair>(&bar.empty[st.slot]);
-          if (k + 1 == ke) mma_commit_group<kPair>(&bar.acc_full[acc.slot]);
+          if (ends) mma_commit_group<kPair>(&bar.acc_full[acc.slot]);
         }
         __syncwarp();
         st.next();
+        if (ends) acc.next();
       }
-      acc.next();
     }
     if (!ok) {
       if (elect_one()) {
         if (p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
-        mma_commit_group<kPair>(&bar.drain);
+        mma_commit_here<kPair>(&bar.drain);
       }
       __syncwarp();
       wait(&bar.drain, 0);
     }
-  } else if (warp >= 4 && !kSplit) {
+   }
+   __syncwarp();
+   if constexpr (kSplit) {  // see below
+     cluster_arrive_release();
+     cluster_wait();
+     cluster_arrive_release();
+     cluster_wait();
+   }
+  } else if (!kSplit) {
     // ---------------- the rest of the formula, and output ----------------
+    if constexpr (kF32) setmaxnreg_inc<kEpilogueRegs>();
     const int quarter = warp & 3;       // TMEM lanes of this warp
     const int j = (warp - 4) >> 2;      // half of the columns
     const int m = quarter * 32 + lane;  // row of the CTA's part of the tile
@@ -505,14 +586,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = m < used;
       const bool work = quarter * 32 < write;  // any row of the warp
       const bool mma = t.blocks > 0;
+      const bool zero = !mma || !mine;
+      if constexpr (kF32) {
+        if (!mma && p.accumulate) continue;
+        float sum[kWarpCols];
+        join_sums<kPair>(bar, taddr + j * kWarpCols, (t.blocks + kJoin - 1) / kJoin, work, acc, ok,
+                         sum);
+        if (m < write)
+#pragma unroll
+          for (int c = 0; c < kWarpCols; c += 16) {
+            const int col = t.n0 + j * kWarpCols + c;
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = sum[c + x];
+            if (col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, v, Kept{});
+          }
+        continue;
+      }
       if (mma) {
         // after a wait that gave up, the rest is walked without waiting
         if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
         tc_fence_after();
-      } else if (kMode == kFfnWeightGrad && p.accumulate) {
+      } else if (kAMn && p.accumulate) {
         continue;
       }
-      const bool zero = !mma || !mine;
       const uint32_t ta = taddr + acc.slot * kTileN;
       if (work) {
         Kept next;
@@ -531,12 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mma && c + 32 == kWarpCols) {  // read: a later tile may overwrite it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if constexpr (kPair == 2)
-                mbar_arrive_cluster(cluster_map(&bar.acc_empty[acc.slot], 0));
-              else
-                mbar_arrive(&bar.acc_empty[acc.slot]);
-            }
+            release<kPair>(&bar.acc_empty[acc.slot]);
           }
 #pragma unroll
           for (int q = 0; q < 32; q += 16) {
@@ -555,62 +647,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (m < write && col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, u, now);
           }
         }
-      } else if (mma && lane == 0) {
-        if constexpr (kPair == 2)
-          mbar_arrive_cluster(cluster_map(&bar.acc_empty[acc.slot], 0));
-        else
-          mbar_arrive(&bar.acc_empty[acc.slot]);
+      } else if (mma) {
+        release<kPair>(&bar.acc_empty[acc.slot]);
       }
       if (mma) acc.next();
     }
     if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
     tc_fence_before();
-  }
-
-  if constexpr (kSplit) {
+  } else {
     // ---------------- a tile shared by the cluster ----------------
+    if constexpr (kF32) setmaxnreg_inc<kEpilogueRegs>();
     // Each CTA gets the sums of kCols / split columns from all of them: 16-byte
     // pieces of fp32, rows[source][row][piece ^ row % 8] over the stages.
     const Tile t = tile_at(first);
     const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
     const int kb = part(t.blocks, rank), ke = part(t.blocks, rank + 1);
     const int quarter = warp & 3, j = (warp - 4) >> 2, m = quarter * 32 + lane;
-    if (warp >= 4 && kb < ke) {
+    const bool work = quarter * 32 < t.used;  // any row of the warp
+    const uint32_t ta = tmem + (uint32_t)(quarter * 32) * 65536u + j * (kTileN / 2);
+    float sum[kF32 ? kTileN / 2 : 1];
+    if constexpr (kF32) {
+      Ring<2> acc;
+      join_sums<1>(bar, ta, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
+    } else {
       ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
       tc_fence_after();
     }
     __syncwarp();
     cluster_arrive_release();  // this CTA's products are done with its stages
     cluster_wait();
-    if (warp >= 4 && quarter * 32 < t.used) {
-      const uint32_t ta = tmem + (uint32_t)(quarter * 32) * 65536u + j * (kTileN / 2);
+    if (work) {
+      const auto send = [&](int c, const float (&v)[16]) {
+        // gated: a CTA's gate columns, then as many up columns
+        const int cc = kMode == kFfnGated ? c : j * (kTileN / 2) + c;
+        const int per = kMode == kFfnGated ? wide / 2 : wide;
+        const int to = cc / per;
+        const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
+        const uint32_t base = cluster_map(smem, to) + (uint32_t)((rank * kTileM + m) * wide * 4);
+        if (m < t.used)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            st_cluster_v4(base + (uint32_t)(((piece + x) ^ (m & 7)) * 16), v[4 * x], v[4 * x + 1],
+                          v[4 * x + 2], v[4 * x + 3]);
+      };
+      if constexpr (kF32) {
+#pragma unroll
+        for (int c = 0; c < kTileN / 2; c += 16) {
+          float v[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] = sum[c + x];
+          send(c, v);
+        }
+      } else {
 #pragma unroll 1
-      for (int c = 0; c < kTileN / 2; c += 32) {
-        uint32_t d[32];
-        if (kb < ke) {
+        for (int c = 0; c < kTileN / 2; c += 32) {
+          uint32_t d[32];
           tmem_load32(ta + c, d);
           tmem_load_wait(d);
-        }
 #pragma unroll
-        for (int q = 0; q < 32; q += 16) {
-          // gated: a CTA's gate columns, then as many up columns
-          const int cc = kMode == kFfnGated ? c + q : j * (kTileN / 2) + c + q;
-          const int per = kMode == kFfnGated ? wide / 2 : wide;
-          const int to = cc / per;
-          const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
-          const uint32_t base = cluster_map(smem, to) + (uint32_t)((rank * kTileM + m) * wide * 4);
-          if (m < t.used)
+          for (int q = 0; q < 32; q += 16) {
+            float v[16];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float v[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                v[y] = kb == ke ? 0.f
-                       : ok     ? __uint_as_float(d[q + 4 * x + y])
-                                : __uint_as_float(0x7fffffffu);
-              st_cluster_v4(base + (uint32_t)(((piece + x) ^ (m & 7)) * 16), v[0], v[1], v[2],
-                            v[3]);
-            }
+            for (int x = 0; x < 16; ++x)
+              v[x] = ok ? __uint_as_float(d[q + x]) : __uint_as_float(0x7fffffffu);
+            send(c + q, v);
+          }
         }
       }
       tc_fence_before();
@@ -618,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_arrive_release();
     cluster_wait();
-    if (warp >= 4 && !(kMode == kFfnWeightGrad && p.accumulate && t.blocks == 0)) {
+    if (!(kAMn && p.accumulate && t.blocks == 0)) {
       const int per = kMode == kFfnGated ? wide / 2 : wide, groups = per / 16;
       const float *in = reinterpret_cast<const float *>(smem);
       for (int i = threadIdx.x - 128; i < t.write * groups; i += 32 * kEpilogueWarps) {
@@ -692,7 +793,26 @@ bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t 
   const cuuint32_t unit[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            PROMO, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of a launch that are resident together, looked up once per kernel and device.
+cudaError_t max_clusters(const void *func, int dev, const cudaLaunchConfig_t &lc, int *out) {
+  struct Entry {
+    const void *func;
+    int device, clusters;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> known;
+  std::lock_guard<std::mutex> g(mu);
+  for (const Entry &e : known)
+    if (e.func == func && e.device == dev) {
+      *out = e.clusters;
+      return cudaSuccess;
+    }
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(out, func, &lc);
+  if (e == cudaSuccess) known.push_back({func, dev, *out});
+  return e;
 }
 
 template <int kMode, int kPair, bool kSplit>
@@ -700,15 +820,14 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
                         cudaStream_t s) {
   using R = Ring_<kPair>;
   const auto kernel = ffn_kernel<kMode, kPair, kSplit>;
-  const size_t cum = kMode == kFfnWeightGrad ? 0 : sizeof(int) * (p.s.E + 1);
+  const size_t cum = weight_grad(kMode) ? 0 : sizeof(int) * (p.s.E + 1);
   const size_t smem = 1024 + (size_t)R::kStages * R::kStageBytes + cum;
   int dev = 0;
   cudaError_t e = launch_geometry(reinterpret_cast<const void *>(kernel), kThreads, smem, &dev,
                                   nullptr);
   if (e != cudaSuccess) return e;
-  const int64_t groups = kSplit ? tiles : std::max<int64_t>(1, std::min<int64_t>(use / share, tiles));
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)(groups * share));
+  lc.gridDim = dim3((unsigned)share);
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
@@ -720,12 +839,24 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = share > 1 ? 2 : 1;
+  int64_t groups = tiles;
+  if (!kSplit) {
+    groups = std::min<int64_t>(use / share, tiles);
+    if (share > 1) {
+      int fit = 0;  // pairs that run at a time: no tile waits for one that does not
+      e = max_clusters(reinterpret_cast<const void *>(kernel), dev, lc, &fit);
+      if (e != cudaSuccess) return e;
+      groups = std::min<int64_t>(groups, fit);
+    }
+    groups = std::max<int64_t>(1, groups);
+  }
+  lc.gridDim.x = (unsigned)(groups * share);
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
 }
 
 template <int kMode>
 cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
-  constexpr bool kAMn = kMode == kFfnWeightGrad;
+  constexpr bool kAMn = weight_grad(kMode);
   FfnParams p = p0;
   Maps maps;
   bool ok = true;
@@ -772,13 +903,16 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
                    static_cast<CUtensorMap *>(p.seg_maps));
     if (e != cudaSuccess) return e;
   }
+  static const int force = getenv("EP_FFN_FORM") ? atoi(getenv("EP_FFN_FORM")) : 0;
+  const bool pair = force ? force == 2 : use > 1;
+  if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM), use, 2, s);
   return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM), use, 1, s);
 }
 
 }  // namespace
 
 size_t ffn_workspace(int mode, const FfnParams &p) {
-  return mode == kFfnWeightGrad && p.s.cnt_e != nullptr ? 2 * sizeof(CUtensorMap) * p.s.E : 0;
+  return weight_grad(mode) && p.s.cnt_e != nullptr ? 2 * sizeof(CUtensorMap) * p.s.E : 0;
 }
 
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s) {
@@ -791,8 +925,10 @@ cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s)
       return launch_mode<kFfnProduct>(p, sm_cap, s);
     case kFfnProductT:
       return launch_mode<kFfnProductT>(p, sm_cap, s);
-    default:
+    case kFfnWeightGrad:
       return launch_mode<kFfnWeightGrad>(p, sm_cap, s);
+    default:
+      return launch_mode<kFfnWeightGrad32>(p, sm_cap, s);
   }
 }
 

@@ -5,7 +5,10 @@
 
 namespace ep {
 
-enum FfnMode { kFfnGated, kFfnGatedGrad, kFfnProduct, kFfnProductT, kFfnWeightGrad };
+// Weight gradients: BF16, and in 32 bits.
+enum FfnMode {
+  kFfnGated, kFfnGatedGrad, kFfnProduct, kFfnProductT, kFfnWeightGrad, kFfnWeightGrad32
+};
 
 // The rows of each expert: of an expanded layout, or (cnt_e NULL, E = 1) all rows.
 struct Segments {
@@ -43,7 +46,7 @@ struct FfnParams {
   uint16_t *out;            // gated: act; gated gradient: of gate_up; else the output
   uint16_t *out2;           // gated: gate_up; gated gradient: act; may be nullptr
   int out32, out2_32;       // every row (and its up half) starts on a 32-byte boundary
-  int f32, accumulate;      // weight gradient: out is fp32; is added to
+  int accumulate;           // weight gradient: out is added to
   int split;                // CTAs that share a tile's reduction
   void *seg_maps;           // workspace: two tensor maps per expert
   unsigned *err;            // the handle's error word (EP_ERRBIT_TIMEOUT), or nullptr

@@ -485,9 +485,8 @@ ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_
   p.N = k;
   p.out = static_cast<uint16_t *>(grad_w);
   p.out32 = ep::rows_on_32(grad_w, k);
-  p.f32 = grad_w_is_fp32;
   p.accumulate = accumulate;
-  return ep::run_ffn(ep::kFfnWeightGrad, p, h, stream);
+  return ep::run_ffn(grad_w_is_fp32 ? ep::kFfnWeightGrad32 : ep::kFfnWeightGrad, p, h, stream);
 }
 
 ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *outs,

@@ -192,6 +192,18 @@ __device__ __forceinline__ void mma_commit_group(uint64_t *bar) {
         : "memory");
 }
 
+// The same on this CTA's barrier only.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit_here(uint64_t *bar) {
+  if constexpr (kCtas == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
 // Tiled TMA load of the map's box at (x, y, z) into this CTA, counted on the
 // barrier at the shared::cluster address `bar`, which a pair's first CTA holds.
 template <int kCtas>
