@@ -60,36 +60,36 @@ constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
 // registers, rounded to nearest: the tensor cores cut off what does not fit, which
 // over 4096 rows is 4.4e-6 of the result, over 512 about an eighth of that.
 constexpr int kJoin = 8;
-// registers of a control and of an epilogue thread where those sums are held:
-// 128 * 72 + 256 * 216 are the 168 * 384 of the launch
+// registers of a control and of an epilogue thread where the latter need more than
+// 168: 128 * 72 + 256 * 216 are the 168 * 384 of the launch
 constexpr int kControlRegs = 72, kEpilogueRegs = 216;
-#ifndef RASTER
-#define RASTER 16
-#endif
-#ifndef PROMO
-#define PROMO CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-#endif
-#ifndef BOXM
-#define BOXM 4
-#endif
-constexpr int kRaster = RASTER;    // row tiles that pass over the columns together
+constexpr int kRaster = 16;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
-
-template <int kPair>
-struct Ring_ {
-  static constexpr int kABytes = kTileM * kBlockK * 2;
-  static constexpr int kBBytes = kTileN / kPair * kBlockK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kPair == 2 ? 6 : 4;
-};
 
 __host__ __device__ constexpr bool weight_grad(int mode) {
   return mode == kFfnWeightGrad || mode == kFfnWeightGrad32;
 }
 
+// A pair's weight gradients leave by TMA, through 8 KB of each epilogue warp: 256 x 4096 x
+// 7168 takes 33 us in 32 bits where 32-byte stores of each thread's row took 39.  The other
+// outputs are stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096
+// takes 281 us as a product where TMA and five stages took 287, 358 as the gated gradient
+// where they took 385.
+template <int kMode, int kPair>
+struct Ring_ {
+  static constexpr int kABytes = kTileM * kBlockK * 2;
+  static constexpr int kBBytes = kTileN / kPair * kBlockK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr bool kTmaOut = kPair == 2 && weight_grad(kMode);
+  static constexpr int kStages = kPair == 1 ? 4 : kTmaOut ? 5 : 6;
+  static constexpr int kOutBytes = kTmaOut ? 8192 : 0;  // of an epilogue warp
+  static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kOutBytes;
+};
+
 struct Maps {
-  CUtensorMap a[kRowMaps], b;
+  CUtensorMap a[kRowMaps], b;  // operands
+  CUtensorMap out;             // a pair's weight gradients
 };
 
 struct __align__(8) Barriers {
@@ -236,7 +236,12 @@ __device__ __forceinline__ void store16_bf16(uint16_t *o, int col, int N, bool w
 }
 
 // 16 BF16 values from column `col` of a row; zeros behind column N.
-__device__ __forceinline__ void load16_bf16(const uint16_t *a, int col, int N, uint4 (&v)[2]) {
+__device__ __forceinline__ void load16_bf16(const uint16_t *a, int col, int N, bool whole,
+                                            uint4 (&v)[2]) {
+  if (whole && col + 16 <= N) {  // a sector at once: in two halves it is fetched twice
+    ld_stream_v8(a, v);
+    return;
+  }
   v[0] = col + 8 <= N ? ld_stream_v4(a) : make_uint4(0, 0, 0, 0);
   v[1] = col + 16 <= N ? ld_stream_v4(a + 8) : make_uint4(0, 0, 0, 0);
 }
@@ -247,8 +252,24 @@ struct Kept {
 };
 __device__ __forceinline__ void load_kept(const FfnParams &p, int64_t row, int col, Kept *k) {
   const uint16_t *h = p.kept + row * 2 * p.N + col;
-  load16_bf16(h, col, p.N, k->g);
-  load16_bf16(h + p.N, col, p.N, k->u);
+  load16_bf16(h, col, p.N, p.kept32, k->g);
+  load16_bf16(h + p.N, col, p.N, p.kept32, k->u);
+}
+
+// dh and act of 16 columns: d the gradient of act.
+__device__ __forceinline__ void gated_grad16(const Kept &k, const float (&v)[16], float (&dg)[16],
+                                             float (&du)[16], float (&a)[16]) {
+  const uint32_t *gw = reinterpret_cast<const uint32_t *>(k.g);
+  const uint32_t *uw = reinterpret_cast<const uint32_t *>(k.u);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float g = i & 1 ? bf16_hi(gw[i / 2]) : bf16_lo(gw[i / 2]);
+    const float up = i & 1 ? bf16_hi(uw[i / 2]) : bf16_lo(uw[i / 2]);
+    const float s = sigmoid(g), silu = g * s;
+    dg[i] = v[i] * up * (s + silu * (1.f - s));
+    du[i] = v[i] * silu;
+    a[i] = silu * up;
+  }
 }
 
 // Writes 16 columns of a row from the accumulated v (gated: gate v, up u).
@@ -271,17 +292,7 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
     }
   } else if constexpr (kMode == kFfnGatedGrad) {
     float dg[16], du[16], a[16];
-    const uint32_t *gw = reinterpret_cast<const uint32_t *>(k.g);
-    const uint32_t *uw = reinterpret_cast<const uint32_t *>(k.u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float g = i & 1 ? bf16_hi(gw[i / 2]) : bf16_lo(gw[i / 2]);
-      const float up = i & 1 ? bf16_hi(uw[i / 2]) : bf16_lo(uw[i / 2]);
-      const float s = sigmoid(g), silu = g * s;
-      dg[i] = v[i] * up * (s + silu * (1.f - s));
-      du[i] = v[i] * silu;
-      a[i] = silu * up;
-    }
+    gated_grad16(k, v, dg, du, a);
     uint16_t *h = p.out + row * 2 * N + col;
     store16_bf16(h, col, N, p.out32, zero, dg);
     store16_bf16(h + N, col, N, p.out32, zero, du);
@@ -321,6 +332,57 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
     store16_bf16(p.out + row * N + col, col, N, p.out32, zero, v);
   }
 }
+
+// What a warp writes by TMA: pieces of 32 rows x 32 columns through a ring in shared
+// memory, in the swizzle of their rows (64 bytes, in 32 bits 128).
+template <bool kF32>
+struct Out {
+  static constexpr int kBytes = kF32 ? 4096 : 2048, kRing = 8192 / kBytes;
+  uint8_t *base;
+  int slot = 0;
+
+  // 16 of the piece's columns, from column 16 * part; all lanes, each its row
+  __device__ __forceinline__ void put16(int part, bool zero, const float (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+    uint8_t *row = base + slot * kBytes + lane * (kF32 ? 128 : 64);
+    if constexpr (kF32) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 w = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        *reinterpret_cast<float4 *>(row + (((part * 4 + c) ^ (lane & 7)) << 4)) = w;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          w[q] = zero ? 0u : cvt_bf16x2(v[8 * c + 2 * q], v[8 * c + 2 * q + 1]);
+        *reinterpret_cast<uint4 *>(row + (((part * 2 + c) ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  // before the first put16 of a piece: its slot is free
+  __device__ __forceinline__ void open() {
+    if (elect_one()) bulk_wait_read<kRing - 1>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void send(const CUtensorMap *map, int x, int y, int z) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+      tma_store_3d(map, x, y, z, base + slot * kBytes);
+      bulk_commit();
+    }
+    if (++slot == kRing) slot = 0;
+  }
+  __device__ __forceinline__ void finish() {
+    if (elect_one()) bulk_wait_all<0>();
+    __syncwarp();
+  }
+};
 
 // An epilogue warp has read an accumulator.
 template <int kPair>
@@ -367,18 +429,19 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int par
 template <int kMode, int kPair, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
-  using R = Ring_<kPair>;
+  using R = Ring_<kMode, kPair>;
   constexpr int kStages = R::kStages;
   constexpr bool kAMn = weight_grad(kMode);
   constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kAMn;
   constexpr bool kF32 = kMode == kFfnWeightGrad32;
+  constexpr bool kMoreRegs = kF32 || (kMode == kFfnGatedGrad && kPair == 2);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[kThreads / 32];
-  // stages on 1024-byte boundaries (the swizzle's period), then cum[E + 1]
+  // stages on 1024-byte boundaries (the swizzle's period), outputs, then cum[E + 1]
   uint8_t *smem = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;
-  int *cum = reinterpret_cast<int *>(smem + kStages * R::kStageBytes);
+  int *cum = reinterpret_cast<int *>(smem + R::kSmem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair == 2 || kSplit ? (int)cluster_rank() : 0;
 
@@ -425,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp < 4) {
-   if constexpr (kF32) setmaxnreg_dec<kControlRegs>();
+   if constexpr (kMoreRegs) setmaxnreg_dec<kControlRegs>();
    if (warp == 0) {
     // ---------------- copies ----------------
     // The warp stays whole and one lane of it issues, so that the copies' addresses
@@ -569,12 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1)
    }
   } else if (!kSplit) {
     // ---------------- the rest of the formula, and output ----------------
-    if constexpr (kF32) setmaxnreg_inc<kEpilogueRegs>();
+    if constexpr (kMoreRegs) setmaxnreg_inc<kEpilogueRegs>();
     const int quarter = warp & 3;       // TMEM lanes of this warp
     const int j = (warp - 4) >> 2;      // half of the columns
     const int m = quarter * 32 + lane;  // row of the CTA's part of the tile
     const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u;
     constexpr int kWarpCols = kCols / 2;
+    Out<kF32> o{smem + kStages * R::kStageBytes + (warp - 4) * R::kOutBytes};
     Ring<2> acc;
     for (int64_t i = first; i < tiles; i += step) {
       const Tile t = tile_at(i);
@@ -587,12 +651,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool work = quarter * 32 < write;  // any row of the warp
       const bool mma = t.blocks > 0;
       const bool zero = !mma || !mine;
+      // all rows of the warp are written, and not added to
+      const bool whole = R::kTmaOut && quarter * 32 + 32 <= write && !p.accumulate;
+      const int row_w = (int)t.row0 + mine0 + quarter * 32;
       if constexpr (kF32) {
         if (!mma && p.accumulate) continue;
         float sum[kWarpCols];
         join_sums<kPair>(bar, taddr + j * kWarpCols, (t.blocks + kJoin - 1) / kJoin, work, acc, ok,
                          sum);
-        if (m < write)
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < kWarpCols; c += 32) {
+            const int col = t.n0 + j * kWarpCols + c;
+            if (col >= p.N) break;
+            o.open();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float v[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) v[x] = sum[c + 16 * q + x];
+              o.put16(q, zero, v);
+            }
+            o.send(&maps.out, col, row_w, t.e);
+          }
+        } else if (m < write)
 #pragma unroll
           for (int c = 0; c < kWarpCols; c += 16) {
             const int col = t.n0 + j * kWarpCols + c;
@@ -612,13 +694,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t ta = taddr + acc.slot * kTileN;
       if (work) {
-        Kept next;
-        if constexpr (kMode == kFfnGatedGrad)
-          if (mine) load_kept(p, row, t.n0 + j * kWarpCols, &next);
+        // the kept values of the next 32 columns are loaded while these are worked on
+        Kept next[2] = {};
+        const auto ahead = [&](int c) {
+          if constexpr (kMode == kFfnGatedGrad)
+            if (mine && c < kWarpCols) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                load_kept(p, row, t.n0 + j * kWarpCols + c + 16 * q, &next[q]);
+            }
+        };
+        ahead(0);
 #pragma unroll 1
         for (int c = 0; c < kWarpCols; c += 32) {
           uint32_t d[32], d2[32];
-          const int c0 = j * kWarpCols + c;
+          const int c0 = j * kWarpCols + c, col = t.n0 + c0;
           if (mma) {
             tmem_load32(ta + c0, d);
             if constexpr (kMode == kFfnGated) tmem_load32(ta + kTileN / 2 + c0, d2);
@@ -630,33 +720,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             release<kPair>(&bar.acc_empty[acc.slot]);
           }
+          const Kept now[2] = {next[0], next[1]};
+          ahead(c + 32);
+          float v[2][16], u[2][16];
 #pragma unroll
-          for (int q = 0; q < 32; q += 16) {
-            float v[16], u[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              v[x] = ok ? __uint_as_float(d[q + x]) : __uint_as_float(0x7fffffffu);
-              u[x] = kMode != kFfnGated ? 0.f
-                     : ok               ? __uint_as_float(d2[q + x])
-                                        : __uint_as_float(0x7fffffffu);
-            }
-            const int col = t.n0 + c0 + q;
-            Kept now = next;
-            if constexpr (kMode == kFfnGatedGrad)
-              if (mine && (c + q + 16 < kWarpCols)) load_kept(p, row, col + 16, &next);
-            if (m < write && col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, u, now);
+          for (int x = 0; x < 32; ++x) {
+            v[x / 16][x % 16] = ok ? __uint_as_float(d[x]) : __uint_as_float(0x7fffffffu);
+            u[x / 16][x % 16] = kMode != kFfnGated ? 0.f
+                                : ok               ? __uint_as_float(d2[x])
+                                                   : __uint_as_float(0x7fffffffu);
           }
+          if constexpr (R::kTmaOut) {
+            if (whole) {
+              if (col < p.N) {
+                o.open();
+                o.put16(0, zero, v[0]);
+                o.put16(1, zero, v[1]);
+                o.send(&maps.out, col, row_w, t.e);
+              }
+              continue;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (m < write && col + 16 * q < p.N)
+              finish16<kMode>(p, row, t.e, col + 16 * q, zero, v[q], u[q], now[q]);
         }
       } else if (mma) {
         release<kPair>(&bar.acc_empty[acc.slot]);
       }
       if (mma) acc.next();
     }
+    if constexpr (R::kTmaOut) o.finish();
     if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
     tc_fence_before();
   } else {
     // ---------------- a tile shared by the cluster ----------------
-    if constexpr (kF32) setmaxnreg_inc<kEpilogueRegs>();
+    if constexpr (kMoreRegs) setmaxnreg_inc<kEpilogueRegs>();
     // Each CTA gets the sums of kCols / split columns from all of them: 16-byte
     // pieces of fp32, rows[source][row][piece ^ row % 8] over the stages.
     const Tile t = tile_at(first);
@@ -780,20 +880,21 @@ __global__ void ffn_segment_maps_kernel(const __grid_constant__ Maps maps, Segme
   }
 }
 
-// A BF16 array [z, y, x] (x contiguous, rows y_stride apart) copied in boxes of
-// 64 x box_y x 1, zeros outside.
+// An array [z, y, x] of BF16 (or fp32), x contiguous, copied in boxes of box_x x box_y x 1
+// in the swizzle of box_x elements; zeros outside.  Strides in elements.
 bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t z,
-              int64_t y_stride, int box_y) {
+              int64_t y_stride, int64_t z_stride, int box_x, int box_y, bool f32 = false) {
   const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
+  const int size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
-  const cuuint64_t strides[2] = {(cuuint64_t)(2 * y_stride),
-                                 (cuuint64_t)(2 * y_stride * (z > 1 ? y : 1))};
-  const cuuint32_t box[3] = {(cuuint32_t)kBlockK, (cuuint32_t)box_y, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)(size * y_stride), (cuuint64_t)(size * z_stride)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
   const cuuint32_t unit[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-            unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            PROMO, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_x * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Clusters of a launch that are resident together, looked up once per kernel and device.
@@ -818,10 +919,10 @@ cudaError_t max_clusters(const void *func, int dev, const cudaLaunchConfig_t &lc
 template <int kMode, int kPair, bool kSplit>
 cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
                         cudaStream_t s) {
-  using R = Ring_<kPair>;
+  using R = Ring_<kMode, kPair>;
   const auto kernel = ffn_kernel<kMode, kPair, kSplit>;
   const size_t cum = weight_grad(kMode) ? 0 : sizeof(int) * (p.s.E + 1);
-  const size_t smem = 1024 + (size_t)R::kStages * R::kStageBytes + cum;
+  const size_t smem = 1024 + (size_t)R::kSmem + cum;
   int dev = 0;
   cudaError_t e = launch_geometry(reinterpret_cast<const void *>(kernel), kThreads, smem, &dev,
                                   nullptr);
@@ -858,21 +959,24 @@ template <int kMode>
 cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   constexpr bool kAMn = weight_grad(kMode);
   FfnParams p = p0;
-  Maps maps;
+  Maps maps{};
   bool ok = true;
+  const auto matrix = [&](int64_t x, int64_t y, int box_y) {
+    return make_map(&maps.b, p.b, x, y, p.s.E, x, x * y, kBlockK, box_y);
+  };
   if constexpr (kAMn) {
-    ok = make_map(&maps.a[0], p.a, p.M, p.s.rows, 1, p.a_stride, 64);
-    for (int i = 1; i < kRowMaps; ++i) maps.a[i] = maps.a[0];
-    ok = ok && make_map(&maps.b, p.b, p.N, p.s.rows, 1, p.b_stride, 64);
+    ok = make_map(&maps.a[0], p.a, p.M, p.s.rows, 1, p.a_stride, p.a_stride, 64, kBlockK);
+    ok = ok && make_map(&maps.b, p.b, p.N, p.s.rows, 1, p.b_stride, p.b_stride, 64, kBlockK);
   } else {
     for (int i = 0; i < kRowMaps; ++i)
-      ok = ok && make_map(&maps.a[i], p.a, p.K, p.s.rows, 1, p.a_stride, kRowStep << i);
+      ok = ok && make_map(&maps.a[i], p.a, p.K, p.s.rows, 1, p.a_stride, p.a_stride, kBlockK,
+                          kRowStep << i);
     if constexpr (kMode == kFfnGated)
-      ok = ok && make_map(&maps.b, p.b, p.K, 2 * (int64_t)p.N, p.s.E, p.K, 128);
+      ok = ok && matrix(p.K, 2 * (int64_t)p.N, 128);
     else if constexpr (kMode == kFfnProduct)
-      ok = ok && make_map(&maps.b, p.b, p.K, p.N, p.s.E, p.K, 128);
+      ok = ok && matrix(p.K, p.N, 128);
     else
-      ok = ok && make_map(&maps.b, p.b, p.N, p.K, p.s.E, p.N, 64);
+      ok = ok && matrix(p.N, p.K, kBlockK);
   }
   if (!ok) return cudaErrorInvalidValue;
   int dev = 0;
@@ -905,6 +1009,10 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   }
   static const int force = getenv("EP_FFN_FORM") ? atoi(getenv("EP_FFN_FORM")) : 0;
   const bool pair = force ? force == 2 : use > 1;
+  if constexpr (kAMn)
+    if (pair && !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32,
+                          kMode == kFfnWeightGrad32))
+      return cudaErrorInvalidValue;
   if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM), use, 2, s);
   return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM), use, 1, s);
 }

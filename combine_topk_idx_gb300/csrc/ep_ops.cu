@@ -438,6 +438,7 @@ ep_status ep_ffn_gated_backward(const ep_handle *h, int64_t rows, int32_t ffn, i
   p.out = static_cast<uint16_t *>(grad_gate_up);
   p.out2 = static_cast<uint16_t *>(act);
   p.out32 = ep::rows_on_32(grad_gate_up, ffn);
+  p.kept32 = ep::rows_on_32(gate_up, ffn);
   p.out2_32 = ep::rows_on_32(act, ffn);
   return ep::run_ffn(ep::kFfnGatedGrad, p, h, stream);
 }

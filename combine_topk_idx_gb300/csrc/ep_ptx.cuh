@@ -14,6 +14,14 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
   return r;
 }
 
+// 32-byte read-only streaming load, a whole sector for one thread.
+__device__ __forceinline__ void ld_stream_v8(const void *p, uint4 (&v)[2]) {
+  asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+        "=r"(v[1].z), "=r"(v[1].w)
+      : "l"(p));
+}
+
 // 16-byte read-only load that may stay cached (small tables reused by many CTAs).
 __device__ __forceinline__ uint4 ld_cached_v4(const void *p) {
   uint4 r;

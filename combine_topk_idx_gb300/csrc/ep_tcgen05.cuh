@@ -223,6 +223,17 @@ __device__ __forceinline__ void tma_load_3d(void *sdst, const CUtensorMap *map, 
         : "memory");
 }
 
+// Tiled TMA store of a box in shared memory to (x, y, z), of this thread's bulk group.
+// What lies outside the tensor is left out.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z,
+                                             const void *ssrc) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(ssrc))
+      : "memory");
+}
+
 // Ends the rows (dimension 1) of a tensor map in global memory at `rows`, and makes
 // the change visible to later readers of the map.
 __device__ __forceinline__ void tma_replace_rows(CUtensorMap *map, uint32_t rows) {
