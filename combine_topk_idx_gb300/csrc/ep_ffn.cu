@@ -49,13 +49,12 @@
 namespace ep {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
+constexpr int kTileM = 128, kBlockK = 64;
 constexpr int kRowStep = 16;   // a tile's rows are copied up to a multiple of this
 constexpr int kRowMaps = 4;    // boxes of 16, 32, 64 and 128 rows
 constexpr int kBoxBytes = 64 * kBlockK * 2;  // 64 columns of a 64-element block
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
 // Blocks that a weight gradient in 32 bits adds up in TMEM before its sums go on in
 // registers, rounded to nearest: the tensor cores cut off what does not fit, which
 // over 4096 rows is 4.4e-6 of the result, over 512 about an eighth of that.
@@ -63,6 +62,7 @@ constexpr int kJoin = 8;
 // registers of a control and of an epilogue thread where the latter need more than
 // 168: 128 * 72 + 256 * 216 are the 168 * 384 of the launch
 constexpr int kControlRegs = 72, kEpilogueRegs = 216;
+constexpr int kMaxSplit = 4;   // CTAs that share a tile's reduction
 constexpr int kRaster = 16;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
@@ -76,19 +76,20 @@ __host__ __device__ constexpr bool weight_grad(int mode) {
 // outputs are stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096
 // takes 281 us as a product where TMA and five stages took 287, 358 as the gated gradient
 // where they took 385.
-template <int kMode, int kPair>
+template <int kMode, int kPair, bool kSplit>
 struct Ring_ {
+  static constexpr int kCols = kSplit ? 128 : 256;  // accumulator columns of a tile
   static constexpr int kABytes = kTileM * kBlockK * 2;
-  static constexpr int kBBytes = kTileN / kPair * kBlockK * 2;
+  static constexpr int kBBytes = kCols / kPair * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr bool kTmaOut = kPair == 2 && weight_grad(kMode);
-  static constexpr int kStages = kPair == 1 ? 4 : kTmaOut ? 5 : 6;
+  static constexpr int kStages = kTmaOut ? 5 : 2 * kABytes == kStageBytes ? 6 : 4;
   static constexpr int kOutBytes = kTmaOut ? 8192 : 0;  // of an epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kOutBytes;
 };
 
 struct Maps {
-  CUtensorMap a[kRowMaps], b;  // operands
+  CUtensorMap a[kRowMaps], b, b_small;  // operands; b in boxes of a split tile's half
   CUtensorMap out;             // a pair's weight gradients
 };
 
@@ -172,10 +173,9 @@ __device__ __forceinline__ void raster(int64_t k, int tr, int tc, int *r, int *c
 }
 
 // Tile i.  Whole warps.
-template <int kMode>
+template <int kMode, int kCols>
 __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, int64_t i,
                                           int rows_per_tile, int tiles_n) {
-  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
   Tile t;
   int r, c;
   if constexpr (weight_grad(kMode)) {
@@ -189,11 +189,16 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
     t.k0 = s.first;
     t.blocks = (int)((s.used + kBlockK - 1) / kBlockK);
   } else {
-    const int lane = threadIdx.x & 31;
-    int lo = -1;  // the last expert with cum[e] * tiles_n <= i
-    for (int e = lane; e - lane < p.s.E; e += 32)
-      lo += __popc(__ballot_sync(0xffffffffu, e < p.s.E && (int64_t)cum[e] * tiles_n <= i));
-    raster(i - (int64_t)cum[lo] * tiles_n, cum[lo + 1] - cum[lo], tiles_n, &r, &c);
+    int lo = 0;
+    if (p.s.cnt_e == nullptr) {
+      raster(i, (int)((p.s.rows + rows_per_tile - 1) / rows_per_tile), tiles_n, &r, &c);
+    } else {
+      const int lane = threadIdx.x & 31;
+      lo = -1;  // the last expert with cum[e] * tiles_n <= i
+      for (int e = lane; e - lane < p.s.E; e += 32)
+        lo += __popc(__ballot_sync(0xffffffffu, e < p.s.E && (int64_t)cum[e] * tiles_n <= i));
+      raster(i - (int64_t)cum[lo] * tiles_n, cum[lo + 1] - cum[lo], tiles_n, &r, &c);
+    }
     const SegmentRows s = segment_rows(p.s, lo);
     const int64_t off = (int64_t)r * rows_per_tile;
     t.e = lo;
@@ -394,21 +399,21 @@ __device__ __forceinline__ void release(uint64_t *acc_empty) {
     mbar_arrive(acc_empty);
 }
 
-// Adds `parts` accumulators, as they become complete, up in sum: kTileN / 2 columns
-// from `taddr` of this warp's lanes.  Rows nobody needs (!work) are not read.
-template <int kPair>
+// Adds `parts` accumulators, as they become complete, up in sum: kHalf columns (half of
+// an accumulator's) from `taddr` of this warp's lanes.  Rows nobody needs (!work) are not read.
+template <int kPair, int kHalf>
 __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int parts, bool work,
-                                          Ring<2> &acc, bool &ok, float (&sum)[kTileN / 2]) {
+                                          Ring<2> &acc, bool &ok, float (&sum)[kHalf]) {
 #pragma unroll
-  for (int c = 0; c < kTileN / 2; ++c) sum[c] = 0.f;
+  for (int c = 0; c < kHalf; ++c) sum[c] = 0.f;
   for (int i = 0; i < parts; ++i) {
     if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
     tc_fence_after();
     if (work) {
 #pragma unroll
-      for (int c = 0; c < kTileN / 2; c += 32) {
+      for (int c = 0; c < kHalf; c += 32) {
         uint32_t d[32];
-        tmem_load32(taddr + acc.slot * kTileN + c, d);
+        tmem_load32(taddr + acc.slot * 2 * kHalf + c, d);
         tmem_load_wait(d);
 #pragma unroll
         for (int x = 0; x < 32; ++x) sum[c + x] += __uint_as_float(d[x]);
@@ -421,7 +426,7 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int par
   }
   if (!ok)
 #pragma unroll
-    for (int c = 0; c < kTileN / 2; ++c) sum[c] = __uint_as_float(0x7fffffffu);
+    for (int c = 0; c < kHalf; ++c) sum[c] = __uint_as_float(0x7fffffffu);
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
@@ -429,8 +434,9 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int par
 template <int kMode, int kPair, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
-  using R = Ring_<kMode, kPair>;
-  constexpr int kStages = R::kStages;
+  using R = Ring_<kMode, kPair, kSplit>;
+  constexpr int kStages = R::kStages, kTileN = R::kCols;
+  constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
   constexpr bool kAMn = weight_grad(kMode);
   constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kAMn;
   constexpr bool kF32 = kMode == kFfnWeightGrad32;
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc_group<kPair>(&tmem_slot, kTmemColumns);
   griddep_wait();
-  if constexpr (!kAMn) count_tiles(p, kTileM * kPair, cum, warp_sum);
+  if (!kAMn && p.s.cnt_e != nullptr) count_tiles(p, kTileM * kPair, cum, warp_sum);
   __syncthreads();
   if constexpr (kPair == 2) {  // the other CTA's barriers are ready
     cluster_arrive_release();
@@ -473,12 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kAMn)
     tiles = (int64_t)p.s.E * ((p.M + kTileM * kPair - 1) / (kTileM * kPair)) * tiles_n;
   else
-    tiles = (int64_t)cum[p.s.E] * tiles_n;
+    tiles = (p.s.cnt_e == nullptr ? (p.s.rows + kTileM * kPair - 1) / (kTileM * kPair)
+                                  : (int64_t)cum[p.s.E]) * tiles_n;
   // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
   const int share = kSplit ? p.split : kPair;
   const int64_t first = blockIdx.x / share, step = gridDim.x / share;
   const auto tile_at = [&](int64_t i) {
-    return find_tile<kMode>(p, cum, i, kTileM * kPair, tiles_n);
+    return find_tile<kMode, kCols>(p, cum, i, kTileM * kPair, tiles_n);
   };
   // this CTA's part of a tile's reduction
   const auto part = [&](int blocks, int r) {
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows1 = kPair == 1 ? 0 : kAMn ? kTileM : up(t.used - half);
       const int rows = half_rank ? rows1 : rows0;
       const uint32_t bytes = (uint32_t)((rows0 + rows1 + kTileN) * kBlockK * 2);
-      const CUtensorMap *ma = &maps.a[0], *mb = &maps.b;
+      const CUtensorMap *ma = &maps.a[0], *mb = kSplit && !kBMn ? &maps.b_small : &maps.b;
       if (kAMn && p.seg_maps != nullptr) {
         ma = reinterpret_cast<const CUtensorMap *>(p.seg_maps) + 2 * t.e;
         mb = ma + 1;
@@ -549,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kTileN / kPair / 64; ++j)
               tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, kAMn ? 0 : t.e, full);
           } else {
-            // 128 rows of the matrix per box: gate and up, or two neighbours
+            // kTileN / 2 rows of the matrix per box: gate and up, or two neighbours
             const int far = kMode == kFfnGated ? p.N : kTileN / 2;
 #pragma unroll
             for (int j = 0; j < 2 / kPair; ++j)
-              tma_load_3d<kPair>(b + 2 * j * kBoxBytes, mb, k * kBlockK,
+              tma_load_3d<kPair>(b + j * (R::kBBytes * kPair / 2), mb, k * kBlockK,
                                  t.n0 + (half_rank + j) * far, t.e, full);
           }
         }
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kF32) {
         if (!mma && p.accumulate) continue;
         float sum[kWarpCols];
-        join_sums<kPair>(bar, taddr + j * kWarpCols, (t.blocks + kJoin - 1) / kJoin, work, acc, ok,
+        join_sums<kPair, kTileN / 2>(bar, taddr + j * kWarpCols, (t.blocks + kJoin - 1) / kJoin, work, acc, ok,
                          sum);
         if (whole) {
 #pragma unroll
@@ -757,8 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- a tile shared by the cluster ----------------
     if constexpr (kMoreRegs) setmaxnreg_inc<kEpilogueRegs>();
-    // Each CTA gets the sums of kCols / split columns from all of them: 16-byte
-    // pieces of fp32, rows[source][row][piece ^ row % 8] over the stages.
+    // Each CTA gets the sums of kTileN / split columns from all of them, in shared memory
+    // over the stages: [source][4 columns][row][4], so that a warp writes 512 bytes in a row
+    // (rows apart, a tile of 128 rows took 25 us to change hands).
     const Tile t = tile_at(first);
     const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
     const int kb = part(t.blocks, rank), ke = part(t.blocks, rank + 1);
@@ -768,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum[kF32 ? kTileN / 2 : 1];
     if constexpr (kF32) {
       Ring<2> acc;
-      join_sums<1>(bar, ta, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
+      join_sums<1, kTileN / 2>(bar, ta, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
     } else {
       ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
       tc_fence_after();
@@ -783,11 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int per = kMode == kFfnGated ? wide / 2 : wide;
         const int to = cc / per;
         const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
-        const uint32_t base = cluster_map(smem, to) + (uint32_t)((rank * kTileM + m) * wide * 4);
+        const uint32_t base =
+            cluster_map(smem, to) + (uint32_t)(((rank * (wide / 4) + piece) * kTileM + m) * 16);
         if (m < t.used)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            st_cluster_v4(base + (uint32_t)(((piece + x) ^ (m & 7)) * 16), v[4 * x], v[4 * x + 1],
+            st_cluster_v4(base + (uint32_t)(x * kTileM * 16), v[4 * x], v[4 * x + 1],
                           v[4 * x + 2], v[4 * x + 3]);
       };
       if constexpr (kF32) {
@@ -821,30 +830,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait();
     if (!(kAMn && p.accumulate && t.blocks == 0)) {
       const int per = kMode == kFfnGated ? wide / 2 : wide, groups = per / 16;
-      const float *in = reinterpret_cast<const float *>(smem);
+      const float4 *in = reinterpret_cast<const float4 *>(smem);
       for (int i = threadIdx.x - 128; i < t.write * groups; i += 32 * kEpilogueWarps) {
-        const int r = i / groups, g = i - r * groups;
+        const int g = i / t.write, r = i - g * t.write;
         const int col = t.n0 + rank * per + g * 16;
         if (col >= p.N) continue;
         const bool zero = r >= t.used || t.blocks == 0;
         float v[16], u[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) v[x] = u[x] = 0.f;
-        if (!zero)
-          for (int s = 0; s < S; ++s) {
-            const float *from = in + (int64_t)(s * kTileM + r) * wide;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float4 a =
-                  *reinterpret_cast<const float4 *>(from + (((g * 4 + x) ^ (r & 7)) * 4));
-              v[4 * x] += a.x, v[4 * x + 1] += a.y, v[4 * x + 2] += a.z, v[4 * x + 3] += a.w;
-              if constexpr (kMode == kFfnGated) {
-                const float4 b = *reinterpret_cast<const float4 *>(
-                    from + (((per / 4 + g * 4 + x) ^ (r & 7)) * 4));
-                u[4 * x] += b.x, u[4 * x + 1] += b.y, u[4 * x + 2] += b.z, u[4 * x + 3] += b.w;
-              }
+        for (int s = 0; s < kMaxSplit; ++s) {
+          if (zero || s >= S) continue;
+          const float4 *from = in + (s * (wide / 4) + g * 4) * kTileM + r;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 a = from[x * kTileM];
+            v[4 * x] += a.x, v[4 * x + 1] += a.y, v[4 * x + 2] += a.z, v[4 * x + 3] += a.w;
+            if constexpr (kMode == kFfnGated) {
+              const float4 b = from[(per / 4 + x) * kTileM];
+              u[4 * x] += b.x, u[4 * x + 1] += b.y, u[4 * x + 2] += b.z, u[4 * x + 3] += b.w;
             }
           }
+        }
         Kept k{};
         if constexpr (kMode == kFfnGatedGrad)
           if (!zero) load_kept(p, t.row0 + r, col, &k);
@@ -897,29 +905,30 @@ bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of a launch that are resident together, looked up once per kernel and device.
-cudaError_t max_clusters(const void *func, int dev, const cudaLaunchConfig_t &lc, int *out) {
+// Clusters of `share` CTAs that are resident together, looked up once per kernel and device.
+cudaError_t max_clusters(const void *func, int dev, int share, const cudaLaunchConfig_t &lc,
+                         int *out) {
   struct Entry {
     const void *func;
-    int device, clusters;
+    int device, share, clusters;
   };
   static std::mutex mu;
   static std::vector<Entry> known;
   std::lock_guard<std::mutex> g(mu);
   for (const Entry &e : known)
-    if (e.func == func && e.device == dev) {
+    if (e.func == func && e.device == dev && e.share == share) {
       *out = e.clusters;
       return cudaSuccess;
     }
   const cudaError_t e = cudaOccupancyMaxActiveClusters(out, func, &lc);
-  if (e == cudaSuccess) known.push_back({func, dev, *out});
+  if (e == cudaSuccess) known.push_back({func, dev, share, *out});
   return e;
 }
 
 template <int kMode, int kPair, bool kSplit>
 cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
-                        cudaStream_t s) {
-  using R = Ring_<kMode, kPair>;
+                        cudaStream_t s, bool *fits) {
+  using R = Ring_<kMode, kPair, kSplit>;
   const auto kernel = ffn_kernel<kMode, kPair, kSplit>;
   const size_t cum = weight_grad(kMode) ? 0 : sizeof(int) * (p.s.E + 1);
   const size_t smem = 1024 + (size_t)R::kSmem + cum;
@@ -940,16 +949,17 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = share > 1 ? 2 : 1;
-  int64_t groups = tiles;
-  if (!kSplit) {
-    groups = std::min<int64_t>(use / share, tiles);
-    if (share > 1) {
-      int fit = 0;  // pairs that run at a time: no tile waits for one that does not
-      e = max_clusters(reinterpret_cast<const void *>(kernel), dev, lc, &fit);
-      if (e != cudaSuccess) return e;
-      groups = std::min<int64_t>(groups, fit);
-    }
-    groups = std::max<int64_t>(1, groups);
+  int64_t groups = std::min<int64_t>(use / share, tiles);
+  if (share > 1) {
+    int fit = 0;  // clusters that run at a time: no tile waits for one that does not
+    e = max_clusters(reinterpret_cast<const void *>(kernel), dev, share, lc, &fit);
+    if (e != cudaSuccess) return e;
+    groups = std::min<int64_t>(groups, fit);
+  }
+  groups = std::max<int64_t>(1, groups);
+  if constexpr (kSplit) {  // a cluster for every tile, or not this way
+    *fits = groups == tiles;
+    if (!*fits) return cudaSuccess;
   }
   lc.gridDim.x = (unsigned)(groups * share);
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
@@ -961,8 +971,9 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   FfnParams p = p0;
   Maps maps{};
   bool ok = true;
-  const auto matrix = [&](int64_t x, int64_t y, int box_y) {
-    return make_map(&maps.b, p.b, x, y, p.s.E, x, x * y, kBlockK, box_y);
+  const auto matrix = [&](int64_t x, int64_t y, bool rows = true) {
+    return make_map(&maps.b, p.b, x, y, p.s.E, x, x * y, kBlockK, rows ? 128 : kBlockK) &&
+           (!rows || make_map(&maps.b_small, p.b, x, y, p.s.E, x, x * y, kBlockK, 64));
   };
   if constexpr (kAMn) {
     ok = make_map(&maps.a[0], p.a, p.M, p.s.rows, 1, p.a_stride, p.a_stride, 64, kBlockK);
@@ -972,35 +983,35 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
       ok = ok && make_map(&maps.a[i], p.a, p.K, p.s.rows, 1, p.a_stride, p.a_stride, kBlockK,
                           kRowStep << i);
     if constexpr (kMode == kFfnGated)
-      ok = ok && matrix(p.K, 2 * (int64_t)p.N, 128);
+      ok = ok && matrix(p.K, 2 * (int64_t)p.N);
     else if constexpr (kMode == kFfnProduct)
-      ok = ok && matrix(p.K, p.N, 128);
+      ok = ok && matrix(p.K, p.N);
     else
-      ok = ok && matrix(p.N, p.K, kBlockK);
+      ok = ok && matrix(p.N, p.K, false);
   }
   if (!ok) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int use = sms_to_use(dev, sm_cap);
-  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
-  const int64_t tiles_n = (p.N + kCols - 1) / kCols;
   // at most this many row tiles of `m` rows hold rows (every expert's last one may be partial)
-  const auto tiles_of = [&](int m) {
+  const auto tiles_of = [&](int m, int n) {
+    if (kMode == kFfnGated) n /= 2;
+    const int64_t tiles_n = (p.N + n - 1) / n;
     const int64_t r = kAMn ? (int64_t)p.s.E * ((p.M + m - 1) / m)
                            : std::min<int64_t>(p.max_segments, p.s.E) + (p.s.rows - 1) / m;
     return r * tiles_n;
   };
   if (p.s.cnt_e == nullptr) {
-    // Few tiles: clusters of 2, 4 or 8 share each one's reduction, as many as there
-    // are SMs for.
-    const int64_t tiles = tiles_of(kTileM);
+    // Few tiles: smaller ones, and clusters of 2 or 4 share each one's reduction, as long as
+    // all of them run at once.
+    const int64_t tiles = tiles_of(kTileM, 128);
     const int64_t blocks = ((kAMn ? p.s.rows : p.K) + kBlockK - 1) / kBlockK;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= use && blocks >= split * 4) split *= 2;
-    if (split > 1) {
-      p.split = split;
-      return launch_form<kMode, 1, true>(maps, p, tiles, use, split, s);
+    for (p.split = kMaxSplit; p.split > 1; p.split /= 2) {
+      if (tiles * p.split > use || blocks < p.split * 4) continue;
+      bool fits = false;
+      e = launch_form<kMode, 1, true>(maps, p, tiles, use, p.split, s, &fits);
+      if (e != cudaSuccess || fits) return e;
     }
   } else if constexpr (kAMn) {
     e = launch_pdl(ffn_segment_maps_kernel, (unsigned)(2 * p.s.E), 32, 0, s, maps, p.s,
@@ -1013,8 +1024,8 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
     if (pair && !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32,
                           kMode == kFfnWeightGrad32))
       return cudaErrorInvalidValue;
-  if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM), use, 2, s);
-  return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM), use, 1, s);
+  if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM, 256), use, 2, s, nullptr);
+  return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM, 256), use, 1, s, nullptr);
 }
 
 }  // namespace

@@ -511,11 +511,17 @@ ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *ou
   const int sms = ep::device_sm_count(dev);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *ws = nullptr;
-  cudaError_t e = ep::workspace_alloc(ep::clip_workspace(l, sms), s, &ws);
-  if (e != cudaSuccess) return ep::cuda_status(e);
+  cudaError_t e = cudaSuccess;
+  if (const size_t bytes = ep::clip_workspace(l, sms); bytes > 0) {
+    e = ep::workspace_alloc(bytes, s, &ws);
+    if (e != cudaSuccess) return ep::cuda_status(e);
+  }
   e = ep::launch_clip(l, max_norm, norm, ws, sms, s);
-  const cudaError_t f = ep::workspace_free(ws, s);
-  return ep::cuda_status(e != cudaSuccess ? e : f);
+  if (ws != nullptr) {
+    const cudaError_t f = ep::workspace_free(ws, s);
+    if (e == cudaSuccess) e = f;
+  }
+  return ep::cuda_status(e);
 }
 
 }  // extern "C"

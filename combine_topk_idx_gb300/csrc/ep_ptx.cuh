@@ -342,6 +342,16 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t local, uint32_t cta) {
   return v;
 }
 
+__device__ __forceinline__ double ld_cluster_f64(uint32_t local, uint32_t cta) {
+  double v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+      "ld.shared::cluster.f64 %0, [ra];\n\t}"
+      : "=d"(v)
+      : "r"(local), "r"(cta));
+  return v;
+}
+
 __device__ __forceinline__ int ld_acquire_gpu(const int32_t *p) {
   int v;
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");

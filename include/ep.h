@@ -575,7 +575,7 @@ EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n,
  * count: tensors; grads, numels, is_fp32 and outs are HOST arrays of that length,
  *   read before the call returns.  Tensor i: numels[i] elements, fp32 or BF16,
  *   contiguous, aligned to its element's size; empty ones are skipped.
- *   norm = sqrt(sum of all squares), fp32 sums of at most 32 squares joined in fp64;
+ *   norm = sqrt(sum of all squares), fp32 sums of at most 66 squares joined in fp64;
  *     finite whenever fp32 holds it, though the squares may not be.
  *   c = 1 if norm + 1e-6 <= max_norm, else max_norm / (norm + 1e-6): a norm that is
  *     infinite makes c zero, one that is NaN makes it NaN.
@@ -583,7 +583,8 @@ EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n,
  *   (and is then not written if c = 1), else overlaps no gradient and no other
  *   output.  outs NULL: the norm only.
  * norm: device fp32, or NULL if outs is given.  max_norm: >= 0, or infinite.
- * Uses a stream-ordered workspace of 8 bytes per CTA.  The same bits each time.
+ * More than 2 MB, or 64 tensors, use a stream-ordered workspace of 8 bytes per CTA.  The
+ * same bits each time.
  */
 EP_API ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *outs,
                                const int64_t *numels, const uint8_t *is_fp32, float max_norm,

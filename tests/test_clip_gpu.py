@@ -9,9 +9,9 @@ from oracle import ops_oracle as P
 from tests.ops_harness import f64
 
 pytestmark = pytest.mark.gpu
-# fp32 sums of 32 squares (each rounding 2^-24, at most 34 of them), halved by the
-# root, one rounding to fp32; then the factor's rounding and the product's
-NORM = 18 * 2.0 ** -24
+# fp32 sums of at most 66 squares (each rounding 2^-24), halved by the root, one
+# rounding to fp32; then the factor's rounding and the product's
+NORM = 34 * 2.0 ** -24
 CLIP = NORM + 2 * 2.0 ** -24
 
 
