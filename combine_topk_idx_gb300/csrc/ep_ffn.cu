@@ -338,18 +338,18 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
   }
 }
 
-// What a warp writes by TMA: pieces of 32 rows x 32 columns through a ring in shared
-// memory, in the swizzle of their rows (64 bytes, in 32 bits 128).
+// What a warp writes by TMA: pieces of 32 rows x 128 bytes through a ring in shared
+// memory, in the swizzle of their rows.
 template <bool kF32>
 struct Out {
-  static constexpr int kBytes = kF32 ? 4096 : 2048, kRing = 8192 / kBytes;
+  static constexpr int kCols = kF32 ? 32 : 64, kBytes = 4096, kRing = 2;
   uint8_t *base;
   int slot = 0;
 
   // 16 of the piece's columns, from column 16 * part; all lanes, each its row
   __device__ __forceinline__ void put16(int part, bool zero, const float (&v)[16]) {
     const int lane = threadIdx.x & 31;
-    uint8_t *row = base + slot * kBytes + lane * (kF32 ? 128 : 64);
+    uint8_t *row = base + slot * kBytes + lane * 128;
     if constexpr (kF32) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -364,7 +364,7 @@ struct Out {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           w[q] = zero ? 0u : cvt_bf16x2(v[8 * c + 2 * q], v[8 * c + 2 * q + 1]);
-        *reinterpret_cast<uint4 *>(row + (((part * 2 + c) ^ ((lane >> 1) & 3)) << 4)) =
+        *reinterpret_cast<uint4 *>(row + (((part * 2 + c) ^ (lane & 7)) << 4)) =
             make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
@@ -739,12 +739,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (R::kTmaOut) {
             if (whole) {
-              if (col < p.N) {
-                o.open();
-                o.put16(0, zero, v[0]);
-                o.put16(1, zero, v[1]);
-                o.send(&maps.out, col, row_w, t.e);
-              }
+              const int part = c % 64 / 16;
+              if (part == 0) o.open();
+              o.put16(part, zero, v[0]);
+              o.put16(part + 1, zero, v[1]);
+              if (part != 0 && col - 32 < p.N) o.send(&maps.out, col - 32, row_w, t.e);
               continue;
             }
           }
@@ -888,8 +887,8 @@ __global__ void ffn_segment_maps_kernel(const __grid_constant__ Maps maps, Segme
   }
 }
 
-// An array [z, y, x] of BF16 (or fp32), x contiguous, copied in boxes of box_x x box_y x 1
-// in the swizzle of box_x elements; zeros outside.  Strides in elements.
+// An array [z, y, x] of BF16 (or fp32), x contiguous, copied in boxes of box_x (128 bytes)
+// x box_y x 1 in 128-byte swizzle; zeros outside.  Strides in elements.
 bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t z,
               int64_t y_stride, int64_t z_stride, int box_x, int box_y, bool f32 = false) {
   const EncodeTiled fn = encode_tiled();
@@ -901,7 +900,7 @@ bool make_map(CUtensorMap *map, const void *base, int64_t x, int64_t y, int64_t 
   const cuuint32_t unit[3] = {1, 1, 1};
   return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
             const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_x * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1021,7 +1020,8 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   static const int force = getenv("EP_FFN_FORM") ? atoi(getenv("EP_FFN_FORM")) : 0;
   const bool pair = force ? force == 2 : use > 1;
   if constexpr (kAMn)
-    if (pair && !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32,
+    if (pair && !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M,
+                          kMode == kFfnWeightGrad32 ? 32 : 64, 32,
                           kMode == kFfnWeightGrad32))
       return cudaErrorInvalidValue;
   if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM, 256), use, 2, s, nullptr);
