@@ -60,8 +60,9 @@ constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 // over 4096 rows is 4.4e-6 of the result, over 512 about an eighth of that.
 constexpr int kJoin = 8;
 // registers of a control and of an epilogue thread where the latter need more than
-// 168: 128 * 72 + 256 * 216 are the 168 * 384 of the launch
-constexpr int kControlRegs = 72, kEpilogueRegs = 216;
+// 168: 128 * 88 + 256 * 208 are the 168 * 384 of the launch.  With 72 the copies' loop
+// spills: 690 cycles a block instead of 430, and a block's products take 512.
+constexpr int kControlRegs = 88, kEpilogueRegs = 208;
 constexpr int kMaxSplit = 4;   // CTAs that share a tile's reduction
 constexpr int kRaster = 16;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
@@ -71,18 +72,18 @@ __host__ __device__ constexpr bool weight_grad(int mode) {
   return mode == kFfnWeightGrad || mode == kFfnWeightGrad32;
 }
 
-// A pair's weight gradients leave by TMA, through 8 KB of each epilogue warp: 256 x 4096 x
-// 7168 takes 33 us in 32 bits where 32-byte stores of each thread's row took 39.  The other
-// outputs are stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096
-// takes 281 us as a product where TMA and five stages took 287, 358 as the gated gradient
-// where they took 385.
+// A pair's weight gradients in 32 bits leave by TMA, through 8 KB of each epilogue warp: 256
+// x 4096 x 7168 takes 33 us where 32-byte stores of each thread's row took 39.  What is BF16
+// is stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096 takes 281 us
+// as a product where TMA and five stages took 287, 358 as the gated gradient where they took
+// 385.
 template <int kMode, int kPair, bool kSplit>
 struct Ring_ {
   static constexpr int kCols = kSplit ? 128 : 256;  // accumulator columns of a tile
   static constexpr int kABytes = kTileM * kBlockK * 2;
   static constexpr int kBBytes = kCols / kPair * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr bool kTmaOut = kPair == 2 && weight_grad(kMode);
+  static constexpr bool kTmaOut = kPair == 2 && kMode == kFfnWeightGrad32;
   static constexpr int kStages = kTmaOut ? 5 : 2 * kABytes == kStageBytes ? 6 : 4;
   static constexpr int kOutBytes = kTmaOut ? 8192 : 0;  // of an epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kOutBytes;
@@ -90,7 +91,7 @@ struct Ring_ {
 
 struct Maps {
   CUtensorMap a[kRowMaps], b, b_small;  // operands; b in boxes of a split tile's half
-  CUtensorMap out;             // a pair's weight gradients
+  CUtensorMap out;             // a pair's weight gradients in 32 bits
 };
 
 struct __align__(8) Barriers {
@@ -125,6 +126,7 @@ struct Tile {
   int used;      // rows of the tile with a result
   int write;     // rows to write: the used ones, then zeros
   int n0;        // first column
+  int cols;      // columns: of a whole tile, or of half of one
   int64_t k0;    // weight gradient: first row of the sum
   int blocks;    // blocks of the reduction
 };
@@ -162,10 +164,15 @@ __device__ __forceinline__ void count_tiles(const FfnParams &p, int rows_per_til
   __syncthreads();
 }
 
+// a / b, of 32 bits where they suffice (they nearly always do, and 64 take 100 cycles more).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // (row, column) of tile k of tr x tc: kRaster row tiles pass over the columns together.
 __device__ __forceinline__ void raster(int64_t k, int tr, int tc, int *r, int *c) {
   const int64_t per = (int64_t)kRaster * tc;
-  const int g = (int)(k / per) * kRaster;
+  const int g = (int)divide(k, per) * kRaster;
   const int n = min(kRaster, tr - g);
   const int u = (int)(k - (int64_t)g * tc);
   *c = u / n;
@@ -181,7 +188,7 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
   if constexpr (weight_grad(kMode)) {
     const int tr = (p.M + rows_per_tile - 1) / rows_per_tile;
     const int64_t per = (int64_t)tr * tiles_n;
-    t.e = (int)(i / per);
+    t.e = (int)divide(i, per);
     raster(i - t.e * per, tr, tiles_n, &r, &c);
     const SegmentRows s = segment_rows(p.s, t.e);
     t.row0 = (int64_t)r * rows_per_tile;
@@ -209,7 +216,14 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
     t.blocks = t.used > 0 ? (p.K + kBlockK - 1) / kBlockK : 0;
   }
   t.n0 = c * kCols;
+  t.cols = kCols;
   return t;
+}
+
+// Columns of a tile's accumulator.
+template <int kMode>
+__device__ __forceinline__ int acc_columns(const Tile &t) {
+  return kMode == kFfnGated ? 2 * t.cols : t.cols;
 }
 
 // Rows of a tile that CTA `rank` of a pair takes: from which, and how many of n.
@@ -307,15 +321,28 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
     if constexpr (kMode == kFfnWeightGrad32) {
       float *o = reinterpret_cast<float *>(p.out) + at;
 #pragma unroll
-      for (int q = 0; q < 16; q += 4) {
-        if (col + q + 4 > N) break;
-        float4 r = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-        if (zero) r = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < 16; q += 8) {
+        if (col + q + 8 > N) break;
+        float r[8];
         if (p.accumulate) {
-          const float4 b = *reinterpret_cast<const float4 *>(o + q);
-          r = make_float4(r.x + b.x, r.y + b.y, r.z + b.z, r.w + b.w);
+          const float4 b0 = *reinterpret_cast<const float4 *>(o + q);
+          const float4 b1 = *reinterpret_cast<const float4 *>(o + q + 4);
+          const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+          for (int x = 0; x < 8; ++x) r[x] = b[x] + (zero ? 0.f : v[q + x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) r[x] = zero ? 0.f : v[q + x];
         }
-        __stcs(reinterpret_cast<float4 *>(o + q), r);
+        uint32_t w[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(r[x]);
+        if (p.out32) {
+          st_stream_v8(o + q, w);
+        } else {
+          st_stream_v4(o + q, make_uint4(w[0], w[1], w[2], w[3]));
+          st_stream_v4(o + q + 4, make_uint4(w[4], w[5], w[6], w[7]));
+        }
       }
     } else {
       uint16_t *o = p.out + at;
@@ -338,11 +365,10 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
   }
 }
 
-// What a warp writes by TMA: pieces of 32 rows x 128 bytes through a ring in shared
+// What a warp writes by TMA: pieces of 32 rows x 32 fp32 columns through a ring in shared
 // memory, in the swizzle of their rows.
-template <bool kF32>
 struct Out {
-  static constexpr int kCols = kF32 ? 32 : 64, kBytes = 4096, kRing = 2;
+  static constexpr int kBytes = 4096, kRing = 2;
   uint8_t *base;
   int slot = 0;
 
@@ -350,23 +376,11 @@ struct Out {
   __device__ __forceinline__ void put16(int part, bool zero, const float (&v)[16]) {
     const int lane = threadIdx.x & 31;
     uint8_t *row = base + slot * kBytes + lane * 128;
-    if constexpr (kF32) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 w = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-        *reinterpret_cast<float4 *>(row + (((part * 4 + c) ^ (lane & 7)) << 4)) = w;
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          w[q] = zero ? 0u : cvt_bf16x2(v[8 * c + 2 * q], v[8 * c + 2 * q + 1]);
-        *reinterpret_cast<uint4 *>(row + (((part * 2 + c) ^ (lane & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    for (int c = 0; c < 4; ++c) {
+      const float4 w = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      *reinterpret_cast<float4 *>(row + (((part * 4 + c) ^ (lane & 7)) << 4)) = w;
     }
   }
   // before the first put16 of a piece: its slot is free
@@ -399,11 +413,13 @@ __device__ __forceinline__ void release(uint64_t *acc_empty) {
     mbar_arrive(acc_empty);
 }
 
-// Adds `parts` accumulators, as they become complete, up in sum: kHalf columns (half of
-// an accumulator's) from `taddr` of this warp's lanes.  Rows nobody needs (!work) are not read.
+// Adds `parts` accumulators of 2 * kHalf columns, as they become complete, up in sum: `cols`
+// (64 or 128) columns from `taddr` of this warp's lanes.  Rows nobody needs (!work) are not
+// read.
 template <int kPair, int kHalf>
-__device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int parts, bool work,
-                                          Ring<2> &acc, bool &ok, float (&sum)[kHalf]) {
+__device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int cols, int parts,
+                                          bool work, Ring<2> &acc, bool &ok,
+                                          float (&sum)[kHalf]) {
 #pragma unroll
   for (int c = 0; c < kHalf; ++c) sum[c] = 0.f;
   for (int i = 0; i < parts; ++i) {
@@ -411,12 +427,13 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int par
     tc_fence_after();
     if (work) {
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t d[32];
-        tmem_load32(taddr + acc.slot * 2 * kHalf + c, d);
-        tmem_load_wait(d);
+      for (int c = 0; c < kHalf; c += 64) {
+        if (c >= cols) break;
+        uint32_t d[64];
+        tmem_load64(taddr + acc.slot * 2 * kHalf + c, d);
+        tmem_load_wait64(d);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) sum[c + x] += __uint_as_float(d[x]);
+        for (int x = 0; x < 64; ++x) sum[c + x] += __uint_as_float(d[x]);
       }
       tc_fence_before();
       __syncwarp();
@@ -484,8 +501,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
   const int share = kSplit ? p.split : kPair;
   const int64_t first = blockIdx.x / share, step = gridDim.x / share;
+  // The tiles of the last round, where they are at most half as many as there are pairs,
+  // are halved, so that the round takes half as long.
+  const int64_t last = kPair == 2 ? tiles % step : 0;
+  const int64_t whole_tiles = tiles - (2 * last <= step ? last : 0);
+  const int64_t items = whole_tiles + 2 * (tiles - whole_tiles);
   const auto tile_at = [&](int64_t i) {
-    return find_tile<kMode, kCols>(p, cum, i, kTileM * kPair, tiles_n);
+    if (kPair != 2 || i < whole_tiles)
+      return find_tile<kMode, kCols>(p, cum, i, kTileM * kPair, tiles_n);
+    const int h = (int)(i - whole_tiles);
+    Tile t = find_tile<kMode, kCols>(p, cum, whole_tiles + (h >> 1), kTileM * kPair, tiles_n);
+    t.cols = kCols / 2;
+    t.n0 += (h & 1) * t.cols;
+    if (t.n0 >= p.N) t.used = t.write = t.blocks = 0;
+    return t;
   };
   // this CTA's part of a tile's reduction
   const auto part = [&](int blocks, int r) {
@@ -503,12 +532,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stage's two copies took 540 cycles to issue, longer than its products run.
     Ring<kStages> st;
     int issued = 0;  // stages filled, counted up to kStages
+    int acquired = -1;  // the expert whose maps were last made visible
     const uint32_t full0 = kPair == 2 ? cluster_map(&bar.full[0], 0) : smem_u32(&bar.full[0]);
     const int half_rank = kPair == 2 ? rank : 0;
-    for (int64_t i = first; i < tiles && ok; i += step) {
-      const Tile t = tile_at(i);
+    Tile next;
+    if (first < items) next = tile_at(first);
+    for (int64_t i = first; i < items && ok; i += step) {
+      const Tile t = next;
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
-      if (kb == ke) continue;
+      if (kb == ke) {
+        if (i + step < items) next = tile_at(i + step);
+        continue;
+      }
       const int half = half_of<kMode, kPair>(t);
       // rows copied: up to a multiple of kRowStep; of both CTAs of a pair
       const int left = kPair == 2 ? min(half, t.used) : t.used;
@@ -516,13 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows0 = kAMn ? kTileM : up(left);
       const int rows1 = kPair == 1 ? 0 : kAMn ? kTileM : up(t.used - half);
       const int rows = half_rank ? rows1 : rows0;
-      const uint32_t bytes = (uint32_t)((rows0 + rows1 + kTileN) * kBlockK * 2);
-      const CUtensorMap *ma = &maps.a[0], *mb = kSplit && !kBMn ? &maps.b_small : &maps.b;
+      const int width = acc_columns<kMode>(t);
+      const uint32_t bytes = (uint32_t)((rows0 + rows1 + width) * kBlockK * 2);
+      const CUtensorMap *ma = &maps.a[0], *mb = width == 128 && !kBMn ? &maps.b_small : &maps.b;
       if (kAMn && p.seg_maps != nullptr) {
         ma = reinterpret_cast<const CUtensorMap *>(p.seg_maps) + 2 * t.e;
         mb = ma + 1;
-        tma_acquire_map(ma);
-        tma_acquire_map(mb);
+        if (t.e != acquired) {
+          tma_acquire_map(ma);
+          tma_acquire_map(mb);
+          acquired = t.e;
+        }
       }
       const int a_row = (int)t.row0 + half_rank * half;
       for (int k = kb; k < ke; ++k) {
@@ -551,13 +590,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (kBMn) {
             const int y = kAMn ? (int)(t.k0 + (int64_t)k * kBlockK) : k * kBlockK;
-            const int x = t.n0 + half_rank * (kTileN / 2);
+            const int x = t.n0 + half_rank * (width / 2);
 #pragma unroll
             for (int j = 0; j < kTileN / kPair / 64; ++j)
-              tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, kAMn ? 0 : t.e, full);
+              if (j < width / kPair / 64)
+                tma_load_3d<kPair>(b + j * kBoxBytes, mb, x + 64 * j, y, kAMn ? 0 : t.e, full);
           } else {
-            // kTileN / 2 rows of the matrix per box: gate and up, or two neighbours
-            const int far = kMode == kFfnGated ? p.N : kTileN / 2;
+            // half of the tile's rows of the matrix per box: gate and up, or two neighbours
+            const int far = kMode == kFfnGated ? p.N : width / 2;
 #pragma unroll
             for (int j = 0; j < 2 / kPair; ++j)
               tma_load_3d<kPair>(b + j * (R::kBBytes * kPair / 2), mb, k * kBlockK,
@@ -567,6 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         st.next();
         if (issued < kStages) ++issued;
+        // while the ring is full: where the next tile's copies come from
+        if (k == min(kb + kStages, ke) - 1 && i + step < items) next = tile_at(i + step);
       }
     }
     if (lane == 0) {
@@ -588,15 +630,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
    } else if (warp == 1 && (kPair == 1 || rank == 0)) {
     // ---------------- products ----------------
-    constexpr uint32_t idesc = idesc_bf16(kTileM * kPair, kTileN, kAMn, kBMn);
     constexpr int kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
     Ring<kStages> st;
     Ring<2> acc;
     const uint32_t smem0 = smem_u32(smem);
-    for (int64_t i = first; i < tiles && ok; i += step) {
+    for (int64_t i = first; i < items && ok; i += step) {
       const Tile t = tile_at(i);
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
       if (kb == ke) continue;
+      const uint32_t idesc = idesc_bf16(kTileM * kPair, acc_columns<kMode>(t), kAMn, kBMn);
       for (int k = kb; k < ke && ok; ++k) {
         // an accumulator takes the whole sum, or kJoin blocks of it
         const bool begins = kF32 ? (k - kb) % kJoin == 0 : k == kb;
@@ -644,10 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j = (warp - 4) >> 2;      // half of the columns
     const int m = quarter * 32 + lane;  // row of the CTA's part of the tile
     const uint32_t taddr = tmem + (uint32_t)(quarter * 32) * 65536u;
-    constexpr int kWarpCols = kCols / 2;
-    Out<kF32> o{smem + kStages * R::kStageBytes + (warp - 4) * R::kOutBytes};
+    constexpr int kMostCols = kCols / 2;  // of a warp
+    Out o{smem + kStages * R::kStageBytes + (warp - 4) * R::kOutBytes};
     Ring<2> acc;
-    for (int64_t i = first; i < tiles; i += step) {
+    for (int64_t i = first; i < items; i += step) {
       const Tile t = tile_at(i);
       const int half = half_of<kMode, kPair>(t);
       const int mine0 = kPair == 2 ? rank * half : 0;
@@ -657,20 +699,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = m < used;
       const bool work = quarter * 32 < write;  // any row of the warp
       const bool mma = t.blocks > 0;
+      const int cols = t.cols / 2;  // of this warp
       const bool zero = !mma || !mine;
       // all rows of the warp are written, and not added to
       const bool whole = R::kTmaOut && quarter * 32 + 32 <= write && !p.accumulate;
       const int row_w = (int)t.row0 + mine0 + quarter * 32;
       if constexpr (kF32) {
         if (!mma && p.accumulate) continue;
-        float sum[kWarpCols];
-        join_sums<kPair, kTileN / 2>(bar, taddr + j * kWarpCols, (t.blocks + kJoin - 1) / kJoin, work, acc, ok,
-                         sum);
+        float sum[kMostCols];
+        join_sums<kPair, kMostCols>(bar, taddr + j * cols, cols, (t.blocks + kJoin - 1) / kJoin,
+                                    work, acc, ok, sum);
         if (whole) {
 #pragma unroll
-          for (int c = 0; c < kWarpCols; c += 32) {
-            const int col = t.n0 + j * kWarpCols + c;
-            if (col >= p.N) break;
+          for (int c = 0; c < kMostCols; c += 32) {
+            const int col = t.n0 + j * cols + c;
+            if (c >= cols || col >= p.N) break;
             o.open();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -683,12 +726,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else if (m < write)
 #pragma unroll
-          for (int c = 0; c < kWarpCols; c += 16) {
-            const int col = t.n0 + j * kWarpCols + c;
+          for (int c = 0; c < kMostCols; c += 16) {
+            const int col = t.n0 + j * cols + c;
             float v[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) v[x] = sum[c + x];
-            if (col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, v, Kept{});
+            if (c < cols && col < p.N) finish16<kMode>(p, row, t.e, col, zero, v, v, Kept{});
           }
         continue;
       }
@@ -705,24 +748,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         Kept next[2] = {};
         const auto ahead = [&](int c) {
           if constexpr (kMode == kFfnGatedGrad)
-            if (mine && c < kWarpCols) {
+            if (mine && c < cols) {
 #pragma unroll
               for (int q = 0; q < 2; ++q)
-                load_kept(p, row, t.n0 + j * kWarpCols + c + 16 * q, &next[q]);
+                load_kept(p, row, t.n0 + j * cols + c + 16 * q, &next[q]);
             }
         };
         ahead(0);
 #pragma unroll 1
-        for (int c = 0; c < kWarpCols; c += 32) {
+        for (int c = 0; c < cols; c += 32) {
           uint32_t d[32], d2[32];
-          const int c0 = j * kWarpCols + c, col = t.n0 + c0;
+          const int c0 = j * cols + c, col = t.n0 + c0;
           if (mma) {
             tmem_load32(ta + c0, d);
-            if constexpr (kMode == kFfnGated) tmem_load32(ta + kTileN / 2 + c0, d2);
+            if constexpr (kMode == kFfnGated) tmem_load32(ta + t.cols + c0, d2);
             tmem_load_wait(d);
             if constexpr (kMode == kFfnGated) tmem_load_wait(d2);
           }
-          if (mma && c + 32 == kWarpCols) {  // read: a later tile may overwrite it
+          if (mma && c + 32 == cols) {  // read: a later tile may overwrite it
             tc_fence_before();
             __syncwarp();
             release<kPair>(&bar.acc_empty[acc.slot]);
@@ -736,16 +779,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[x / 16][x % 16] = kMode != kFfnGated ? 0.f
                                 : ok               ? __uint_as_float(d2[x])
                                                    : __uint_as_float(0x7fffffffu);
-          }
-          if constexpr (R::kTmaOut) {
-            if (whole) {
-              const int part = c % 64 / 16;
-              if (part == 0) o.open();
-              o.put16(part, zero, v[0]);
-              o.put16(part + 1, zero, v[1]);
-              if (part != 0 && col - 32 < p.N) o.send(&maps.out, col - 32, row_w, t.e);
-              continue;
-            }
           }
 #pragma unroll
           for (int q = 0; q < 2; ++q)
@@ -775,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum[kF32 ? kTileN / 2 : 1];
     if constexpr (kF32) {
       Ring<2> acc;
-      join_sums<1, kTileN / 2>(bar, ta, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
+      join_sums<1, kTileN / 2>(bar, ta, kTileN / 2, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
     } else {
       ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
       tc_fence_after();
@@ -948,7 +981,8 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = share > 1 ? 2 : 1;
-  int64_t groups = std::min<int64_t>(use / share, tiles);
+  // (a pair's last tiles may be halved)
+  int64_t groups = std::min<int64_t>(use / share, kPair == 2 ? 2 * tiles : tiles);
   if (share > 1) {
     int fit = 0;  // clusters that run at a time: no tile waits for one that does not
     e = max_clusters(reinterpret_cast<const void *>(kernel), dev, share, lc, &fit);
@@ -1019,10 +1053,9 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   }
   static const int force = getenv("EP_FFN_FORM") ? atoi(getenv("EP_FFN_FORM")) : 0;
   const bool pair = force ? force == 2 : use > 1;
-  if constexpr (kAMn)
-    if (pair && !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M,
-                          kMode == kFfnWeightGrad32 ? 32 : 64, 32,
-                          kMode == kFfnWeightGrad32))
+  if constexpr (kMode == kFfnWeightGrad32)
+    if (pair &&
+        !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32, true))
       return cudaErrorInvalidValue;
   if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM, 256), use, 2, s, nullptr);
   return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM, 256), use, 1, s, nullptr);

@@ -485,7 +485,7 @@ ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_
   p.M = n;
   p.N = k;
   p.out = static_cast<uint16_t *>(grad_w);
-  p.out32 = ep::rows_on_32(grad_w, k);
+  p.out32 = ep::aligned(grad_w, 32) && k % (grad_w_is_fp32 ? 8 : 16) == 0;
   p.accumulate = accumulate;
   return ep::run_ffn(grad_w_is_fp32 ? ep::kFfnWeightGrad32 : ep::kFfnWeightGrad, p, h, stream);
 }
