@@ -37,7 +37,6 @@
 // hold NaN.  However it ends, the CTA waits (bounded) for what it has in flight,
 // frees its TMEM and returns.
 #include <algorithm>
-#include <cstdlib>
 #include <mutex>
 #include <vector>
 
@@ -735,6 +734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         continue;
       }
+      // the kept values of the next 32 columns are loaded while these are worked on
+      Kept next[2] = {};
+      const auto ahead = [&](int c) {
+        if constexpr (kMode == kFfnGatedGrad)
+          if (mine && c < cols) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              load_kept(p, row, t.n0 + j * cols + c + 16 * q, &next[q]);
+          }
+      };
+      ahead(0);
       if (mma) {
         // after a wait that gave up, the rest is walked without waiting
         if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
@@ -744,17 +754,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t ta = taddr + acc.slot * kTileN;
       if (work) {
-        // the kept values of the next 32 columns are loaded while these are worked on
-        Kept next[2] = {};
-        const auto ahead = [&](int c) {
-          if constexpr (kMode == kFfnGatedGrad)
-            if (mine && c < cols) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                load_kept(p, row, t.n0 + j * cols + c + 16 * q, &next[q]);
-            }
-        };
-        ahead(0);
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
           uint32_t d[32], d2[32];
@@ -998,6 +997,14 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
 }
 
+// Rows per expert, on average, above which pairs of CTAs take the tiles of a layout.  With 64
+// experts of 4096 x 4096, a gated product of 128 rows each takes 366 us by single CTAs and 370
+// by pairs (half of their 256 rows are empty), of 192 rows 430 and 385, of 1024 1450 and 1310;
+// a weight gradient in BF16 of 128 rows 448 and 650 us (all of it stores, which two CTAs wait
+// for together), of 1024 1570 and 1415, in 32 bits 895 and 840.
+template <int kMode>
+constexpr int64_t kPairRows = kMode == kFfnWeightGrad ? 384 : kMode == kFfnWeightGrad32 ? 0 : 160;
+
 template <int kMode>
 cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   constexpr bool kAMn = weight_grad(kMode);
@@ -1051,8 +1058,7 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
                    static_cast<CUtensorMap *>(p.seg_maps));
     if (e != cudaSuccess) return e;
   }
-  static const int force = getenv("EP_FFN_FORM") ? atoi(getenv("EP_FFN_FORM")) : 0;
-  const bool pair = force ? force == 2 : use > 1;
+  const bool pair = use > 1 && (p.s.cnt_e == nullptr || p.max_segments > kPairRows<kMode> * p.s.E);
   if constexpr (kMode == kFfnWeightGrad32)
     if (pair &&
         !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32, true))
