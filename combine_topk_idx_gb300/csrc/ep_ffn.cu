@@ -904,18 +904,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Tensor maps of an expert's rows for the weight gradient: the given ones with
-// their rows ending at the expert's last.  A block per map: 2 * e + (0: a, 1: b).
-__global__ void ffn_segment_maps_kernel(const __grid_constant__ Maps maps, Segments s,
-                                        CUtensorMap *out) {
-  const int e = blockIdx.x >> 1;
+// their rows ending at the expert's last.  Map 2 * e + (0: a, 1: b); a warp each.
+__global__ void __launch_bounds__(32) ffn_segment_maps_kernel(const __grid_constant__ Maps maps,
+                                                              Segments s, CUtensorMap *out) {
   griddep_wait();
-  const uint4 *from = reinterpret_cast<const uint4 *>(blockIdx.x & 1 ? &maps.b : &maps.a[0]);
-  uint4 *to = reinterpret_cast<uint4 *>(out + blockIdx.x);
-  if (threadIdx.x < sizeof(CUtensorMap) / 16) to[threadIdx.x] = from[threadIdx.x];
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const SegmentRows r = segment_rows(s, e);
-    tma_replace_rows(out + blockIdx.x, (uint32_t)max((int64_t)1, r.first + r.used));
+  for (int i = blockIdx.x; i < 2 * s.E; i += gridDim.x) {
+    const uint4 *from = reinterpret_cast<const uint4 *>(i & 1 ? &maps.b : &maps.a[0]);
+    uint4 *to = reinterpret_cast<uint4 *>(out + i);
+    if (threadIdx.x < sizeof(CUtensorMap) / 16) to[threadIdx.x] = from[threadIdx.x];
+    __syncwarp();
+    if (threadIdx.x == 0) {
+      const SegmentRows r = segment_rows(s, i >> 1);
+      tma_replace_rows(out + i, (uint32_t)max((int64_t)1, r.first + r.used));
+    }
   }
 }
 
@@ -1054,7 +1055,7 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
       if (e != cudaSuccess || fits) return e;
     }
   } else if constexpr (kAMn) {
-    e = launch_pdl(ffn_segment_maps_kernel, (unsigned)(2 * p.s.E), 32, 0, s, maps, p.s,
+    e = launch_pdl(ffn_segment_maps_kernel, (unsigned)std::min(2 * p.s.E, 8 * use), 32, 0, s, maps, p.s,
                    static_cast<CUtensorMap *>(p.seg_maps));
     if (e != cudaSuccess) return e;
   }
