@@ -6,10 +6,12 @@
 
 The experts are frozen FP8 weights (e4m3, one scale per 128x128 block); the
 norm's gain, the router and everything before the block train.  What the
-backward pass needs of the experts' inputs is kept in 8 bits.
+backward pass needs of the experts' inputs is kept in 8 bits.  With --shared a
+BF16 feed-forward block that every token passes trains beside the experts: its
+output joins theirs in the combine, and all gradients can be clipped together.
 
     python examples/moe_layer.py [--tokens T] [--hidden H] [--ffn F]
-                                 [--experts E] [--topk K]
+                                 [--experts E] [--topk K] [--shared F] [--clip NORM]
 
 prints how far the outputs and gradients are from a plain fp32 evaluation and
 the time of a forward and of a forward and backward pass.
@@ -49,9 +51,9 @@ def dequantise_weights(q: torch.Tensor, sf: torch.Tensor) -> torch.Tensor:
 
 class MoeHalf:
     """Weights and one forward's saved state.  All sizes fixed at construction;
-    hidden and ffn are multiples of 128."""
+    hidden and ffn are multiples of 128, shared (0: no shared expert) of 8."""
 
-    def __init__(self, hidden, ffn, experts, topk, ranks=1, eps=1e-6, seed=0):
+    def __init__(self, hidden, ffn, experts, topk, ranks=1, eps=1e-6, seed=0, shared=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, std):
@@ -69,6 +71,10 @@ class MoeHalf:
         self.w_in_t_sf = self.w_in_sf.transpose(1, 2).contiguous()
         self.w_out_t = self.w_out.transpose(1, 2).contiguous()
         self.w_out_t_sf = self.w_out_sf.transpose(1, 2).contiguous()
+        self.shared = shared
+        if shared:
+            self.s_in = normal(2 * shared, hidden, std=hidden ** -0.5).bfloat16()
+            self.s_out = normal(hidden, shared, std=shared ** -0.5).bfloat16()
 
     def forward(self, x, residual, keep=False):
         """(block output, residual stream); with ``keep`` what backward needs is saved."""
@@ -93,14 +99,22 @@ class MoeHalf:
             ckpt_sf = torch.empty(rows, 2 * self.ffn // 128, device="cuda")
         ep.ep_swiglu(h, gate_up, act_fp8=act, act_sf=act_sf, ckpt=ckpt, ckpt_sf=ckpt_sf)
         y = ep.ep_expert_gemm(h, act, act_sf, self.w_out, self.w_out_sf)
-        out = ep.ep_combine(h, y, w)
+        s_gate_up = s_y = None
+        if self.shared:
+            if keep:
+                s_gate_up = torch.empty(T, 2 * self.shared, dtype=torch.bfloat16, device="cuda")
+            s_act = ep.ep_ffn_gated(None, n["y"], self.s_in, gate_up=s_gate_up)
+            s_y = ep.ep_ffn_product(None, s_act, self.s_out)
+        out = ep.ep_combine(h, y, w, bias_0=s_y)
         if keep:
-            self.saved = (h, n, probs, w, idx, ckpt, ckpt_sf, y)
+            self.saved = (h, n, probs, w, idx, ckpt, ckpt_sf, y, s_gate_up)
         return out, n["residual_out"]
 
-    def backward(self, grad_out, grad_residual):
-        """(gradient of x and of the residual, of gamma, of the router)."""
-        h, n, probs, w, idx, ckpt, ckpt_sf, y = self.saved
+    def backward(self, grad_out, grad_residual, max_norm=None):
+        """(gradient of x and of the residual, of gamma, of the router); with a shared
+        expert also of its two matrices.  With ``max_norm`` all but the first are
+        clipped to that norm together; ``self.grad_norm`` is theirs before."""
+        h, n, probs, w, idx, ckpt, ckpt_sf, y, s_gate_up = self.saved
         gw = torch.empty_like(w)
         gy, gy_sf = ep.alloc_fp8(h, self.hidden)
         ep.ep_combine_weighted_backward(h, grad_out, y, w, grad_y_fp8=gy, grad_y_sf=gy_sf,
@@ -114,9 +128,20 @@ class MoeHalf:
         gp = torch.zeros_like(probs).scatter_(1, idx, gw)
         gl = (probs * (gp - (gp * probs).sum(1, keepdim=True))).bfloat16()
         grad_norm = grad_norm + gl @ self.router
+        grads = []
+        if self.shared:
+            s_act = torch.empty(s_gate_up.shape[0], self.shared, dtype=torch.bfloat16,
+                                device="cuda")
+            s_grad = ep.ep_ffn_gated_backward(None, grad_out, self.s_out, s_gate_up, act=s_act)
+            grads = [ep.ep_ffn_weight_grad(None, s_grad, n["y"]),
+                     ep.ep_ffn_weight_grad(None, grad_out, s_act)]
+            grad_norm = grad_norm + ep.ep_ffn_product(None, s_grad, self.s_in, transposed=True)
         grad_x, grad_gamma = ep.ep_rmsnorm_backward(grad_norm, n["residual_out"], self.gamma,
                                                     n["rstd"], grad_residual)
-        return grad_x, grad_gamma, gl.t() @ n["y"]
+        grads = [grad_gamma, gl.t() @ n["y"]] + grads
+        if max_norm is not None:
+            self.grad_norm = ep.ep_clip_grads(grads, max_norm)
+        return (grad_x, *grads)
 
 
 def rounded(v: torch.Tensor) -> torch.Tensor:
@@ -146,9 +171,16 @@ def plain(m: MoeHalf, x, residual, grad_out, grad_residual, idx, eight_bit=False
         g, u = (hold(y[t]) @ w_in[e].t()).chunk(2, dim=1)
         rows = hold(torch.nn.functional.silu(g) * u) @ w_out[e].t()
         out = out.index_add(0, t, rows * w[t, k, None])
+    more = {}
+    if m.shared:
+        s_in, s_out = m.s_in.float().requires_grad_(), m.s_out.float().requires_grad_()
+        g, u = (y @ s_in.t()).chunk(2, dim=1)
+        out = out + (torch.nn.functional.silu(g) * u) @ s_out.t()
+        more = {"grad shared in": s_in, "grad shared out": s_out}
     torch.autograd.backward([out, s], [grad_out.float(), grad_residual.float()])
     return {"out": out.detach(), "residual": s.detach(), "grad x": xs.grad,
-            "grad gamma": gamma.grad, "grad router": router.grad}
+            "grad gamma": gamma.grad, "grad router": router.grad,
+            **{k: v.grad for k, v in more.items()}}
 
 
 def compare(m: MoeHalf, tokens: int, seed=1, eight_bit=False) -> dict:
@@ -157,25 +189,26 @@ def compare(m: MoeHalf, tokens: int, seed=1, eight_bit=False) -> dict:
     x, res, go, gr = (torch.randn((tokens, m.hidden), generator=g, device="cuda").bfloat16()
                       for _ in range(4))
     out, stream = m.forward(x, res, keep=True)
-    gx, gg, gt = m.backward(go, gr)
+    grads = m.backward(go, gr)
     want = plain(m, x, res, go, gr, m.saved[4], eight_bit)
-    got = {"out": out, "residual": stream, "grad x": gx, "grad gamma": gg, "grad router": gt}
+    got = dict(zip(want, (out, stream, *grads)))
     return {k: float((got[k].float() - v).norm() / v.norm()) for k, v in want.items()}
 
 
 def main():
     a = argparse.ArgumentParser()
     for name, value in (("tokens", 1024), ("hidden", 1024), ("ffn", 512), ("experts", 32),
-                        ("topk", 4)):
+                        ("topk", 4), ("shared", 0)):
         a.add_argument("--" + name, type=int, default=value)
+    a.add_argument("--clip", type=float, default=None)
     a = a.parse_args()
-    m = MoeHalf(a.hidden, a.ffn, a.experts, a.topk)
+    m = MoeHalf(a.hidden, a.ffn, a.experts, a.topk, shared=a.shared)
     for k, v in compare(m, a.tokens).items():
-        print(f"{k:12s} relative error {v:.4f}")
+        print(f"{k:15s} relative error {v:.4f}")
     x, res, go, gr = (torch.randn(a.tokens, a.hidden, device="cuda").bfloat16() for _ in range(4))
     for name, step in (("forward", lambda: m.forward(x, res)),
                        ("forward and backward",
-                        lambda: (m.forward(x, res, keep=True), m.backward(go, gr)))):
+                        lambda: (m.forward(x, res, keep=True), m.backward(go, gr, a.clip)))):
         for _ in range(3):
             step()
         torch.cuda.synchronize()
