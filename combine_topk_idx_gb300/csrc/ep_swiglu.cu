@@ -36,17 +36,6 @@ constexpr int kThreads = 256;
 constexpr int kTileElems = 32768;  // of F per tile, at most
 constexpr int kMaxTileRows = 64;
 
-// 1 / (1 + e^-g) of a pair: relative error about 2^-21 plus the rounding of g's
-// exponent (|g| 2^-24); 0 where 1 + e^-g passes 2^126 (g below -87.3), for a
-// subnormal reciprocal counts as 0.
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
-  const float c = -1.4426950408889634f;
-  const uint64_t x = f32x2_mul_rn(g, f32x2_pack(c, c));
-  const uint64_t y = f32x2_add_rn(f32x2_pack(exp2_approx(f32x2_lo(x)), exp2_approx(f32x2_hi(x))),
-                                  f32x2_pack(1.f, 1.f));
-  return f32x2_pack(rcp_approx(f32x2_lo(y)), rcp_approx(f32x2_hi(y)));
-}
-
 struct TileRow {
   int64_t row;  // -1: nothing to do
   float w;
