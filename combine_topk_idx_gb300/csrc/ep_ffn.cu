@@ -1116,6 +1116,11 @@ size_t ffn_workspace(int mode, const FfnParams &p) {
 }
 
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s) {
+  if (ffn_few_rows(mode, p)) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : launch_ffn_rows(mode, p, sms_to_use(dev, sm_cap), s);
+  }
   switch (mode) {
     case kFfnGated:
       return launch_mode<kFfnGated>(p, sm_cap, s);

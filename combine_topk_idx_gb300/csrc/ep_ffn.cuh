@@ -56,4 +56,10 @@ struct FfnParams {
 size_t ffn_workspace(int mode, const FfnParams &p);
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s);
 
+// Few rows and one matrix, without tensor cores: whether a call is one of these, and its
+// launch.
+constexpr int kFfnFewRows = 16;
+bool ffn_few_rows(int mode, const FfnParams &p);
+cudaError_t launch_ffn_rows(int mode, const FfnParams &p, int sms, cudaStream_t s);
+
 }  // namespace ep

@@ -19,7 +19,7 @@ def ep():
 
 # rows, n (ffn), k: single rows, ends inside a tile, a block and a 16-byte group,
 # few and many tiles, a long reduction
-DENSE = [(1, 128, 64), (1, 8, 8), (1, 520, 1032), (2, 256, 4096), (16, 136, 200), (17, 264, 128),
+DENSE = [(1, 128, 64), (1, 8, 8), (8, 24, 40), (9, 40, 2056), (4, 2504, 104), (1, 520, 1032), (2, 256, 4096), (16, 136, 200), (17, 264, 128),
          (127, 128, 64), (128, 256, 256), (129, 248, 264), (300, 392, 72), (1000, 1000, 328),
          (513, 2056, 192), (64, 512, 7168), (2500, 16, 24)]
 
@@ -123,7 +123,8 @@ def calls(ep, h, rows, n, k, seed=9):
     }
 
 
-@pytest.mark.parametrize("form", ["few_rows", "dense", "layout", "layout_many_rows"])
+@pytest.mark.parametrize("form", ["single", "few_rows", "tens", "dense", "layout",
+                                  "layout_many_rows"])
 @pytest.mark.parametrize("op", OPS)
 def test_streams_and_graphs(ep, op, form):
     """The same bits on the current stream, on another one, in a graph that is replayed, and
@@ -132,7 +133,7 @@ def test_streams_and_graphs(ep, op, form):
     if form.startswith("layout"):
         T, E = (300, 8) if form == "layout" else (1200, 2)
         h = make_handle(ep, T, 2, E, 1, T, 16)
-    rows = {"few_rows": 40, "dense": 1500}.get(form) or h.rows_alloc
+    rows = {"single": 1, "few_rows": 11, "tens": 40, "dense": 1500}.get(form) or h.rows_alloc
     call, outputs = calls(ep, h, rows, 264, 328)[op]
     want, side, first, second = (outputs() for _ in range(4))
     call(want, None)
@@ -179,7 +180,7 @@ def test_allocated_outputs_belong_to_the_stream(ep, op):
             assert seg["stream"] == side.cuda_stream
 
 
-@pytest.mark.parametrize("rows", [30, 700])
+@pytest.mark.parametrize("rows", [1, 11, 30, 700])
 def test_strided_rows(ep, rows):
     """Arrays of rows inside wider ones."""
     g = torch.Generator().manual_seed(4)
@@ -197,7 +198,7 @@ def test_strided_rows(ep, rows):
                            ep.ep_ffn_weight_grad(None, gc, xc, dtype=kind))
 
 
-@pytest.mark.parametrize("rows", [30, 700])
+@pytest.mark.parametrize("rows", [3, 11, 30, 700])
 @pytest.mark.parametrize("op", OPS)
 def test_alignment_of_outputs(ep, op, rows):
     """Outputs that start on 16 bytes, not 32, hold the same; what lies around them stays."""
@@ -245,7 +246,7 @@ def test_other_experts_weights(ep, op, T):
 def test_values_that_are_not_finite(ep):
     """They stay in their row and column."""
     g = torch.Generator().manual_seed(8)
-    for rows in (20, 900):
+    for rows in (5, 12, 20, 900):
         x, w = normal(g, rows, 64).cuda(), normal(g, 256, 64).cuda()
         want = ep.ep_ffn_product(None, x, w)
         x[3, 5], w[7, 9] = float("nan"), float("inf")
