@@ -24,8 +24,18 @@
 //   kPair 1   persistent, a CTA per SM
 //   kPair 2   persistent, two CTAs on a 256 x 256 tile: each holds its 128 rows and
 //             half of the columns' operand
-//   kSplit    few tiles: a cluster per tile, its CTAs share the reduction and add
-//             up through each other's shared memory, in a fixed order
+//   kSplit    few tiles: 128 x 128 ones, a cluster per tile, its CTAs share the
+//             reduction and add up through each other's shared memory, in a fixed order
+// Up to 16 rows through one matrix are ep_ffn_rows.cu's.
+//
+// What bounds it (times move by 8 % with the GPU and what it ran before: the power cap sets
+// its clock).  Large tiles, the tensor cores: a block of a 256 x 256 tile takes 521 cycles
+// where its products need 512; 8192 x 8192 x 4096 takes 276 us, 2.0 PFLOP/s, and 264 as a
+// library's product.  What an epilogue reads and writes competes with the operands for L2:
+// the gated gradient of that size moves 670 MB more and takes 353 us.  128 rows per expert,
+// the weights' bytes: 256 experts of 4096 x 7168, 2.46 ms for 15.9 GB, 6.5 TB/s.  Few rows
+// through one matrix, latency: 128 x 2048 x 7168 takes 10.3 us, of them 1.2 before the first
+// copy and 3 from the last product to the end.
 //
 // Rows that are not an expert's own never reach its results: in the row products
 // they are other rows of the accumulator; in the weight gradient, where they
@@ -56,11 +66,11 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 // Blocks that a weight gradient in 32 bits adds up in TMEM before its sums go on in
 // registers, rounded to nearest: the tensor cores cut off what does not fit, which
-// over 4096 rows is 4.4e-6 of the result, over 512 about an eighth of that.
+// over 4096 rows is 4.4e-6 of the result, over 512 at a time 4.7e-7.
 constexpr int kJoin = 8;
 // registers of a control and of an epilogue thread where the latter need more than
 // 168: 128 * 88 + 256 * 208 are the 168 * 384 of the launch.  With 72 the copies' loop
-// spills: 690 cycles a block instead of 430, and a block's products take 512.
+// spilt and took 690 cycles a block, whose products take 512.
 constexpr int kControlRegs = 88, kEpilogueRegs = 208;
 constexpr int kMaxSplit = 4;   // CTAs that share a tile's reduction
 constexpr int kRaster = 16;    // row tiles that pass over the columns together
@@ -73,9 +83,9 @@ __host__ __device__ constexpr bool weight_grad(int mode) {
 
 // A pair's weight gradients in 32 bits leave by TMA, through 8 KB of each epilogue warp: 256
 // x 4096 x 7168 takes 33 us where 32-byte stores of each thread's row took 39.  What is BF16
-// is stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096 takes 281 us
+// is stored from registers, and the memory is a sixth stage: 8192 x 8192 x 4096 took 281 us
 // as a product where TMA and five stages took 287, 358 as the gated gradient where they took
-// 385.
+// 385 (all measured on the same GPU).
 template <int kMode, int kPair, bool kSplit>
 struct Ring_ {
   static constexpr int kCols = kSplit ? 128 : 256;  // accumulator columns of a tile
