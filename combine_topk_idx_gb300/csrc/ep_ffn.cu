@@ -26,7 +26,7 @@
 //             half of the columns' operand
 //   kSplit    few tiles: 128 x 128 ones, a cluster per tile, its CTAs share the
 //             reduction and add up through each other's shared memory, in a fixed order
-// Up to 16 rows through one matrix are ep_ffn_rows.cu's.
+// Up to 16 rows in all are ep_ffn_rows.cu's, if gated or a product on W's rows.
 //
 // What bounds it (times move by 8 % with the GPU and what it ran before: the power cap sets
 // its clock).  Large tiles, the tensor cores: a block of a 256 x 256 tile takes 521 cycles

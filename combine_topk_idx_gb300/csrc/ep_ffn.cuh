@@ -36,7 +36,7 @@ __device__ __forceinline__ SegmentRows segment_rows(const Segments &s, int e) {
 
 struct FfnParams {
   Segments s;
-  int64_t max_segments;     // experts that can have rows
+  int64_t max_segments;     // experts that can have rows; of a layout, its slots
   // a: the rows [rows, K] (weight gradient: the gradient [rows, M]); b: the matrix of
   // each expert (weight gradient: the rows [rows, N]); strides of rows, in elements
   const uint16_t *a, *b;
@@ -56,8 +56,7 @@ struct FfnParams {
 size_t ffn_workspace(int mode, const FfnParams &p);
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s);
 
-// Few rows and one matrix, without tensor cores: whether a call is one of these, and its
-// launch.
+// Few rows, weights streamed into registers: whether a call is one of these, and its launch.
 constexpr int kFfnFewRows = 16;
 bool ffn_few_rows(int mode, const FfnParams &p);
 cudaError_t launch_ffn_rows(int mode, const FfnParams &p, int sms, cudaStream_t s);

@@ -1,7 +1,7 @@
-// The gated product and the product of a few rows with one matrix: a decode step.
+// The gated product and the product of a few rows: a decode step.
 //
-// Every weight is read once, for at most 16 rows of x, so the time is that of reading the
-// matrix.  A CTA takes 16 rows of the matrix (gated: 8 of the gate, the 8 of up beside them);
+// At most 16 rows, with one matrix or in a layout, each with its expert's.  Every weight is
+// read once, so the time is that of reading the matrices.  A CTA takes 16 rows of the matrix (gated: 8 of the gate, the 8 of up beside them);
 // its warps share the reduction in chunks of 32 elements, each lane reading 16 bytes of a row,
 // several chunks ahead, straight into registers.  There 16 x 8 x 16 products of a warp take
 // them as they lie: a lane's eight elements are not the ones that the fragment's layout names,
@@ -12,7 +12,9 @@
 // so short a call.  Weights read from HBM, 7168 x 4096 gated (58.7 MB, 8.8 us at what a copy
 // reaches): 10.5 us for 1 row, 10.9 for 8, 12.3 for 16, where that form takes 14.5; 2048 x
 // 7168 as a product 6.6, 6.8 and 8.9 us for 10.4.  What a row more costs is reading x in every
-// CTA.  Half or twice as many warps, CTAs per SM or loads ahead change nothing.
+// CTA.  Half or twice as many warps, CTAs per SM or loads ahead change nothing.  One token
+// through 2 of 8 experts (4096 x 4096 gated): 14.4 us, by tcgen05 27; through 8 of 256 (7168 x
+// 4096) 76 and 79.
 #include <algorithm>
 
 #include "ep_ffn.cuh"
@@ -33,29 +35,50 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kN: groups of 8 rows of x.
-template <bool kGated, int kN>
+// kN: groups of 8 rows of x; kLayout: the rows are a layout's.
+template <bool kGated, int kN, bool kLayout>
 __global__ void __launch_bounds__(kThreads, kPerSm) ffn_rows_kernel(const __grid_constant__ FfnParams p) {
   constexpr int kAhead = 8 / kN;                    // chunks of a warp in flight
   __shared__ float part[kWarps][kUnit][8 * kN];
-  const int T = (int)p.s.rows, K = p.K, N = p.N;
+  __shared__ int busy[kFfnFewRows], found[kWarps];
+  const int K = p.K, N = p.N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   constexpr int kOut = kGated ? kUnit / 2 : kUnit;  // columns of the output of a CTA
-  const int units = (N + kOut - 1) / kOut;
+  const int units = (N + kOut - 1) / kOut;          // of an expert
   griddep_wait();
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int n0 = unit * kOut;
+  // the experts with rows, in order, at most as many as there are rows
+  int count = kLayout ? 0 : 1;
+  for (int e0 = 0; kLayout && e0 < p.s.E; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    const bool has = e < p.s.E && segment_rows(p.s, e).used > 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) found[warp] = __popc(all);
+    __syncthreads();
+    int at = count + __popc(all & lanemask_lt());
+    for (int v = 0; v < kWarps; ++v) {
+      at += v < warp ? found[v] : 0;
+      count += found[v];
+    }
+    if (has) busy[at] = e;
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < count * units; item += gridDim.x) {
+    const int e = kLayout ? busy[item / units] : 0, n0 = (kLayout ? item % units : item) * kOut;
+    const SegmentRows rows = kLayout ? segment_rows(p.s, e) : SegmentRows{0, p.s.rows, p.s.rows};
+    const int T = (int)rows.used;
+    const uint16_t *matrix = p.b + (int64_t)e * (kGated ? 2 : 1) * N * K;
     // this lane's rows of the matrix, in the upper and the lower half of the products' 16;
     // behind the last column any row will do
     const uint16_t *w[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int c = min(n0 + (kGated ? 0 : r * 8) + g, N - 1);
-      w[r] = p.b + (int64_t)(kGated && r ? N + c : c) * K + 8 * t;
+      w[r] = matrix + (int64_t)(kGated && r ? N + c : c) * K + 8 * t;
     }
     const uint16_t *x[kN];
 #pragma unroll
-    for (int q = 0; q < kN; ++q) x[q] = p.a + (int64_t)(8 * q + g) * p.a_stride + 8 * t;
+    for (int q = 0; q < kN; ++q)
+      x[q] = p.a + (rows.first + 8 * q + g) * p.a_stride + 8 * t;
     float d[kN][4] = {};
     for (int k0 = 32 * warp; k0 < K; k0 += 32 * kWarps * kAhead) {
       uint4 a[kAhead][2], b[kAhead][kN];
@@ -85,47 +108,60 @@ __global__ void __launch_bounds__(kThreads, kPerSm) ffn_rows_kernel(const __grid
       for (int i = 0; i < 4; ++i)
         part[warp][8 * (i >> 1) + g][8 * q + 2 * t + (i & 1)] = d[q][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < kOut * 8 * kN; i += kThreads) {
-      const int c = i % kOut, row = i / kOut, col = n0 + c;
-      if (row >= T || col >= N) continue;
-      float s = 0.f, u = 0.f;
+    // the sums, then zeros in alignment padding
+    for (int i = threadIdx.x; i < kOut * (int)rows.write; i += kThreads) {
+      const int c = i % kOut, r = i / kOut, col = n0 + c;
+      if (col >= N) continue;
+      const int64_t row = rows.first + r;
+      float v = 0.f, u = 0.f;
+      if (r < T) {
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        s += part[v][c][row];
-        if constexpr (kGated) u += part[v][8 + c][row];
+        for (int q = 0; q < kWarps; ++q) {
+          v += part[q][c][r];
+          if constexpr (kGated) u += part[q][8 + c][r];
+        }
       }
       if constexpr (kGated) {
-        const float act = s * f32x2_lo(sigmoid2(f32x2_pack(s, s))) * u;
-        if (p.out != nullptr) p.out[(int64_t)row * N + col] = (uint16_t)cvt_bf16x2(act, 0.f);
+        const float act = v * f32x2_lo(sigmoid2(f32x2_pack(v, v))) * u;
+        if (p.out != nullptr) p.out[row * N + col] = (uint16_t)cvt_bf16x2(act, 0.f);
         if (p.out2 != nullptr) {
-          p.out2[(int64_t)row * 2 * N + col] = (uint16_t)cvt_bf16x2(s, 0.f);
-          p.out2[(int64_t)row * 2 * N + N + col] = (uint16_t)cvt_bf16x2(u, 0.f);
+          p.out2[row * 2 * N + col] = (uint16_t)cvt_bf16x2(v, 0.f);
+          p.out2[row * 2 * N + N + col] = (uint16_t)cvt_bf16x2(u, 0.f);
         }
       } else {
-        p.out[(int64_t)row * N + col] = (uint16_t)cvt_bf16x2(s, 0.f);
+        p.out[row * N + col] = (uint16_t)cvt_bf16x2(v, 0.f);
       }
     }
   }
 }
 
-template <bool kGated, int kN>
+template <bool kGated, int kN, bool kLayout>
 cudaError_t launch(const FfnParams &p, int sms, cudaStream_t s) {
   constexpr int kOut = kGated ? kUnit / 2 : kUnit;
-  const int grid = std::min(sms * kPerSm, (p.N + kOut - 1) / kOut);
-  return launch_pdl(ffn_rows_kernel<kGated, kN>, (unsigned)grid, kThreads, 0, s, p);
+  const int64_t experts = std::min<int64_t>(p.max_segments, p.s.E);
+  const int64_t grid = std::min<int64_t>(sms * kPerSm, experts * ((p.N + kOut - 1) / kOut));
+  return launch_pdl(ffn_rows_kernel<kGated, kN, kLayout>, (unsigned)grid, kThreads, 0, s, p);
+}
+
+// Rows in use, at most: of one matrix all, of a layout its slots.
+int64_t most_rows(const FfnParams &p) {
+  return p.s.cnt_e == nullptr ? p.s.rows : p.max_segments;
 }
 
 }  // namespace
 
 bool ffn_few_rows(int mode, const FfnParams &p) {
-  return p.s.cnt_e == nullptr && (mode == kFfnGated || mode == kFfnProduct) &&
-         p.s.rows <= kFfnFewRows;
+  return (mode == kFfnGated || mode == kFfnProduct) && most_rows(p) <= kFfnFewRows;
 }
 
 cudaError_t launch_ffn_rows(int mode, const FfnParams &p, int sms, cudaStream_t s) {
-  if (p.s.rows <= 8)
-    return mode == kFfnGated ? launch<true, 1>(p, sms, s) : launch<false, 1>(p, sms, s);
-  return mode == kFfnGated ? launch<true, 2>(p, sms, s) : launch<false, 2>(p, sms, s);
+  const bool layout = p.s.cnt_e != nullptr, gated = mode == kFfnGated;
+  if (most_rows(p) <= 8) {
+    if (layout) return gated ? launch<true, 1, true>(p, sms, s) : launch<false, 1, true>(p, sms, s);
+    return gated ? launch<true, 1, false>(p, sms, s) : launch<false, 1, false>(p, sms, s);
+  }
+  if (layout) return gated ? launch<true, 2, true>(p, sms, s) : launch<false, 2, true>(p, sms, s);
+  return gated ? launch<true, 2, false>(p, sms, s) : launch<false, 2, false>(p, sms, s);
 }
 
 }  // namespace ep

@@ -34,6 +34,11 @@ def test_one_matrix(ep, op, rows, n, k):
 LAYOUTS = {
     "one_row": (1, 1, 1, 1, 1, 1, True, True, False, 0.0, 256, 128),
     "one_token": (1, 8, 64, 8, 1, 1, True, True, False, 0.0, 512, 1024),
+    "few_slots": (5, 3, 16, 4, 2, 16, True, True, False, 0.1, 136, 264),
+    "few_slots_bound": (2, 4, 300, 4, 1, 100, True, False, False, 0.2, 72, 520),
+    "few_slots_unpadded": (3, 2, 8, 2, 2, 8, False, True, False, 0.0, 40, 1032),
+    "few_slots_fixed": (6, 2, 8, 2, 3, 1, False, False, True, 0.0, 200, 72),
+    "sixteen_slots_one_expert": (16, 1, 1, 1, 16, 32, True, True, False, 0.0, 264, 328),
     "aligned": (300, 4, 16, 4, 75, 128, True, True, False, 0.1, 384, 512),
     "align_256": (90, 2, 4, 2, 45, 256, True, True, False, 0.1, 256, 384),
     "unaligned_rows": (333, 4, 16, 4, 90, 1, True, True, False, 0.1, 640, 256),
