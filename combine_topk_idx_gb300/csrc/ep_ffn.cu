@@ -253,128 +253,201 @@ __device__ __forceinline__ uint64_t join(uint32_t lo, uint32_t hi) {
   return f32x2_pack(__uint_as_float(lo), __uint_as_float(hi));
 }
 
-__device__ __forceinline__ void store16(uint16_t *o, int col, int N, bool whole,
-                                        const uint32_t (&w)[8]) {
-  if (whole && col + 16 <= N) {
-    st_stream_v8(o, w);
-  } else {
-    if (col + 8 <= N) st_stream_v4(o, make_uint4(w[0], w[1], w[2], w[3]));
-    if (col + 16 <= N) st_stream_v4(o + 8, make_uint4(w[4], w[5], w[6], w[7]));
-  }
-}
-__device__ __forceinline__ void store16_bf16(uint16_t *o, int col, int N, bool whole,
-                                             const Pairs &v) {
-  uint32_t w[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) w[q] = cvt_bf16x2(f32x2_lo(v[q]), f32x2_hi(v[q]));
-  store16(o, col, N, whole, w);
+__device__ __forceinline__ bool on_32(const void *p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31) == 0;
 }
 
-// 16 BF16 values from column `col` of a row; zeros behind column N.
-__device__ __forceinline__ void load16_bf16(const uint16_t *a, int col, int N, bool whole,
-                                            uint4 (&v)[2]) {
-  if (whole && col + 16 <= N) {  // a sector at once: in two halves it is fetched twice
+// 16 columns of a row from `o` on (16-byte aligned), of which `left` are in the row.
+__device__ __forceinline__ void store16(uint16_t *o, int left, const uint32_t (&w)[8]) {
+  if (left >= 16 && on_32(o)) {
+    st_stream_v8(o, w);
+  } else {
+    if (left >= 8) st_stream_v4(o, make_uint4(w[0], w[1], w[2], w[3]));
+    if (left >= 16) st_stream_v4(o + 8, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+
+// A row's output, 16 columns after another.  Where the row starts in the middle of a sector
+// (every second row of 8 more than a multiple of 16 columns), each piece's last 8 columns wait
+// for the next one's first 8, so that sectors are still stored whole: the gated gradient of
+// 8192 x 6776 x 2048 takes 225 us, 347 in half sectors (of the loads too, see RowIn) and 171
+// at 6784 columns.
+struct RowOut {
+  uint16_t *o;
+  int left;       // columns in the row
+  bool odd, has;  // starts in the middle of a sector; 8 columns wait
+  uint4 rest;
+  __device__ __forceinline__ void begin(uint16_t *at, int columns) {
+    o = at;
+    left = columns;
+    odd = !on_32(at);
+    has = false;
+  }
+  __device__ __forceinline__ void put(const uint32_t (&w)[8]) {
+    if (!odd) {
+      store16(o, left, w);
+    } else if (left >= 8) {
+      if (has) {
+        const uint32_t v[8] = {rest.x, rest.y, rest.z, rest.w, w[0], w[1], w[2], w[3]};
+        st_stream_v8(o - 8, v);
+      } else {
+        st_stream_v4(o, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      has = left >= 16;
+      rest = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    o += 16;
+    left -= 16;
+  }
+  __device__ __forceinline__ void end() {
+    if (has) st_stream_v4(o - 8, rest);
+  }
+};
+
+// 16 BF16 values from `a` on, of which `left` are there; zeros behind them.  A sector at once
+// where it starts there: in two halves it is fetched twice.
+__device__ __forceinline__ void load16(const uint16_t *a, int left, uint4 &lo, uint4 &hi) {
+  if (left >= 16 && on_32(a)) {
+    uint4 v[2];
     ld_stream_v8(a, v);
+    lo = v[0], hi = v[1];
     return;
   }
-  v[0] = col + 8 <= N ? ld_stream_v4(a) : make_uint4(0, 0, 0, 0);
-  v[1] = col + 16 <= N ? ld_stream_v4(a + 8) : make_uint4(0, 0, 0, 0);
+  lo = left >= 8 ? ld_stream_v4(a) : make_uint4(0, 0, 0, 0);
+  hi = left >= 16 ? ld_stream_v4(a + 8) : make_uint4(0, 0, 0, 0);
+}
+
+// A row's input, 32 columns after another, each loaded while the ones before are worked on.
+// In a row that starts in the middle of a sector the loads are 8 columns ahead of their use.
+template <bool kShifted>  // else no row does
+struct RowIn {
+  uint4 r[4], first;
+  bool odd;
+  __device__ __forceinline__ void begin(const uint16_t *at, int left) {
+    odd = kShifted && !on_32(at);
+    first = odd && left >= 8 ? ld_stream_v4(at) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const uint16_t *at, int left) {
+    const int skip = odd ? 8 : 0;
+    load16(at + skip, left - skip, r[0], r[1]);
+    load16(at + skip + 16, left - skip - 16, r[2], r[3]);
+  }
+  // the 32 columns loaded last
+  __device__ __forceinline__ void take(uint4 (&v)[4]) {
+    v[0] = odd ? first : r[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) v[i] = odd ? r[i - 1] : r[i];
+    first = r[3];
+  }
+};
+
+// Pair i of 8 BF16 values.
+__device__ __forceinline__ uint64_t pair_of(const uint4 &h, int i) {
+  const uint32_t w = i == 0 ? h.x : i == 1 ? h.y : i == 2 ? h.z : h.w;
+  return f32x2_pack(bf16_lo(w), bf16_hi(w));
 }
 
 // Gate and up of the forward at 16 columns of a row.
 struct Kept {
   uint4 g[2], u[2];
 };
-__device__ __forceinline__ void load_kept(const FfnParams &p, int64_t row, int col, Kept *k) {
-  const uint16_t *h = p.kept + row * 2 * p.N + col;
-  load16_bf16(h, col, p.N, p.kept32, k->g);
-  load16_bf16(h + p.N, col, p.N, p.kept32, k->u);
-}
 
-// Pair i of 16 BF16 values.
-__device__ __forceinline__ uint64_t pair_of(const uint4 (&v)[2], int i) {
-  const uint4 h = v[i >> 2];
-  const uint32_t w = (i & 3) == 0 ? h.x : (i & 3) == 1 ? h.y : (i & 3) == 2 ? h.z : h.w;
-  return f32x2_pack(bf16_lo(w), bf16_hi(w));
-}
-
-// 16 columns of a row of zeros: alignment padding, a weight's gradient without rows.
+// What is written of a row's 16 columns.  Gated: act, gate, up; gated gradient: of gate, of
+// up, act; else one.
 template <int kMode>
-__device__ __forceinline__ void zero16(const FfnParams &p, int64_t row, int e, int col) {
-  const uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int N = p.N;
-  if constexpr (weight_grad(kMode)) {
-    const int64_t at = ((int64_t)e * p.M + row) * N + col;
-    if constexpr (kMode == kFfnWeightGrad32) {
-      // pairs of BF16 columns are as wide as one in 32 bits
-      store16(p.out + 2 * at, 2 * col, 2 * N, p.out32, w);
-      if (col + 8 < N) store16(p.out + 2 * at + 16, 2 * col + 16, 2 * N, p.out32, w);
-    } else {
-      store16(p.out + at, col, N, p.out32, w);
-    }
-    return;
-  }
-  constexpr bool kTwin = kMode == kFfnGatedGrad;  // out is gate and up, out2 one of them
-  if (p.out != nullptr) {
-    uint16_t *o = p.out + row * (kTwin ? 2 : 1) * N + col;
-    store16(o, col, N, p.out32, w);
-    if (kTwin) store16(o + N, col, N, p.out32, w);
-  }
-  if (p.out2 != nullptr) {
-    uint16_t *o = p.out2 + row * (kTwin ? 1 : 2) * N + col;
-    store16(o, col, N, p.out2_32, w);
-    if (!kTwin) store16(o + N, col, N, p.out2_32, w);
-  }
-}
-
-// Writes 16 columns of a row from the accumulated v (gated: gate v, up u).
+constexpr int kOuts = kMode == kFfnGated || kMode == kFfnGatedGrad ? 3 : 1;
 template <int kMode>
-__device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e, int col,
-                                         const Pairs &v, const Pairs &u, const Kept &k) {
-  const int N = p.N;
+struct Words {
+  uint32_t w[kOuts<kMode>][8];
+};
+
+// The row's output i (of a weight gradient in BF16: within expert e's matrix), from its first
+// column on; nullptr: not asked for.
+template <int kMode>
+__device__ __forceinline__ uint16_t *out_row(const FfnParams &p, int i, int64_t row, int e) {
+  const int64_t N = p.N;
   if constexpr (kMode == kFfnGated) {
-    if (p.out != nullptr) {
-      Pairs a;
+    if (i == 0) return p.out == nullptr ? nullptr : p.out + row * N;
+    return p.out2 == nullptr ? nullptr : p.out2 + row * 2 * N + (i == 2 ? N : 0);
+  } else if constexpr (kMode == kFfnGatedGrad) {
+    if (i < 2) return p.out + row * 2 * N + (i == 1 ? N : 0);
+    return p.out2 == nullptr ? nullptr : p.out2 + row * N;
+  } else if constexpr (weight_grad(kMode)) {
+    return p.out + ((int64_t)e * p.M + row) * N;
+  } else {
+    return p.out + row * N;
+  }
+}
+
+// From 16 columns' accumulated v (gated: gate v, up u).
+template <int kMode>
+__device__ __forceinline__ void compute16(const FfnParams &p, const Pairs &v, const Pairs &u,
+                                          const Kept &k, Words<kMode> &o) {
+  if constexpr (kMode == kFfnGated) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        a[i] = f32x2_mul_rn(f32x2_mul_rn(v[i], sigmoid2(v[i])), u[i]);
-      store16_bf16(p.out + row * N + col, col, N, p.out32, a);
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t a = f32x2_mul_rn(f32x2_mul_rn(v[i], sigmoid2(v[i])), u[i]);
+      o.w[0][i] = cvt_bf16x2(f32x2_lo(a), f32x2_hi(a));
     }
     if (p.out2 != nullptr) {
-      uint16_t *h = p.out2 + row * 2 * N + col;
-      store16_bf16(h, col, N, p.out2_32, v);
-      store16_bf16(h + N, col, N, p.out2_32, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o.w[1][i] = cvt_bf16x2(f32x2_lo(v[i]), f32x2_hi(v[i]));
+        o.w[2][i] = cvt_bf16x2(f32x2_lo(u[i]), f32x2_hi(u[i]));
+      }
     }
   } else if constexpr (kMode == kFfnGatedGrad) {
     // one column at a time: in packed pairs 8192 x 8192 x 4096 took 376 us instead of 353
-    float r[3][16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint64_t g2 = pair_of(k.g, i / 2), u2 = pair_of(k.u, i / 2);
-      const float g = i & 1 ? f32x2_hi(g2) : f32x2_lo(g2);
-      const float up = i & 1 ? f32x2_hi(u2) : f32x2_lo(u2);
-      const float d = i & 1 ? f32x2_hi(v[i / 2]) : f32x2_lo(v[i / 2]);
-      const float s = rcp_approx(1.f + exp2_approx(-1.4426950408889634f * g)), silu = g * s;
-      r[0][i] = d * up * (s + silu * (1.f - s));
-      r[1][i] = d * silu;
-      r[2][i] = silu * up;
-    }
-    Pairs dg, du, a;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      dg[i] = f32x2_pack(r[0][2 * i], r[0][2 * i + 1]);
-      du[i] = f32x2_pack(r[1][2 * i], r[1][2 * i + 1]);
-      a[i] = f32x2_pack(r[2][2 * i], r[2][2 * i + 1]);
+      const uint64_t g2 = pair_of(k.g[i >> 2], i & 3), u2 = pair_of(k.u[i >> 2], i & 3);
+      float r[2][3];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float g = q ? f32x2_hi(g2) : f32x2_lo(g2), up = q ? f32x2_hi(u2) : f32x2_lo(u2);
+        const float d = q ? f32x2_hi(v[i]) : f32x2_lo(v[i]);
+        const float s = rcp_approx(1.f + exp2_approx(-1.4426950408889634f * g)), silu = g * s;
+        r[q][0] = d * up * (s + silu * (1.f - s));
+        r[q][1] = d * silu;
+        r[q][2] = silu * up;
+      }
+#pragma unroll
+      for (int x = 0; x < 3; ++x) o.w[x][i] = cvt_bf16x2(r[0][x], r[1][x]);
     }
-    uint16_t *h = p.out + row * 2 * N + col;
-    store16_bf16(h, col, N, p.out32, dg);
-    store16_bf16(h + N, col, N, p.out32, du);
-    if (p.out2 != nullptr) store16_bf16(p.out2 + row * N + col, col, N, p.out2_32, a);
-  } else if constexpr (kMode == kFfnWeightGrad32) {
-    float *o = reinterpret_cast<float *>(p.out) + ((int64_t)e * p.M + row) * N + col;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.w[0][i] = cvt_bf16x2(f32x2_lo(v[i]), f32x2_hi(v[i]));
+  }
+}
+
+// 16 columns of a row, zeros: alignment padding, a weight's gradient without rows.
+template <int kMode>
+__device__ __forceinline__ void zero16(const FfnParams &p, int64_t row, int e, int col) {
+  const uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const int left = p.N - col;
+  if constexpr (kMode == kFfnWeightGrad32) {
+    uint16_t *o = p.out + 2 * (((int64_t)e * p.M + row) * p.N + col);  // two of these a column
+    store16(o, 16, w);
+    if (left >= 16) store16(o + 16, 16, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOuts<kMode>; ++i) {
+      uint16_t *o = out_row<kMode>(p, i, row, e);
+      if (o != nullptr) store16(o + col, left, w);
+    }
+  }
+}
+
+// Writes 16 columns of a row by themselves.
+template <int kMode>
+__device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e, int col,
+                                         const Pairs &v, const Pairs &u, const Kept &k) {
+  const int left = p.N - col;
+  if constexpr (kMode == kFfnWeightGrad32) {
+    float *o = reinterpret_cast<float *>(p.out) + ((int64_t)e * p.M + row) * p.N + col;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      if (col + 8 * q + 8 > N) break;
+      if (left < 8 * q + 8) break;
       uint32_t w[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x)
@@ -386,23 +459,27 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
         for (int x = 0; x < 8; ++x)
           w[x] = __float_as_uint(__uint_as_float(w[x]) + __uint_as_float(b[x]));
       }
-      store16(reinterpret_cast<uint16_t *>(o + 8 * q), 0, 16, p.out32, w);
-    }
-  } else if constexpr (kMode == kFfnWeightGrad) {
-    uint16_t *o = p.out + ((int64_t)e * p.M + row) * N + col;
-    if (p.accumulate) {
-      uint4 b[2];
-      b[0] = col + 8 <= N ? ld_plain_v4(o) : make_uint4(0, 0, 0, 0);
-      b[1] = col + 16 <= N ? ld_plain_v4(o + 8) : make_uint4(0, 0, 0, 0);
-      Pairs s;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = f32x2_add_rn(v[i], pair_of(b, i));
-      store16_bf16(o, col, N, p.out32, s);
-    } else {
-      store16_bf16(o, col, N, p.out32, v);
+      store16(reinterpret_cast<uint16_t *>(o + 8 * q), 16, w);
     }
   } else {
-    store16_bf16(p.out + row * N + col, col, N, p.out32, v);
+    Pairs s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = v[i];
+    if constexpr (kMode == kFfnWeightGrad)
+      if (p.accumulate) {
+        const uint16_t *b = out_row<kMode>(p, 0, row, e) + col;
+        const uint4 lo = ld_plain_v4(b);
+        const uint4 hi = left >= 16 ? ld_plain_v4(b + 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = f32x2_add_rn(s[i], pair_of(i < 4 ? lo : hi, i & 3));
+      }
+    Words<kMode> words;
+    compute16<kMode>(p, s, u, k, words);
+#pragma unroll
+    for (int i = 0; i < kOuts<kMode>; ++i) {
+      uint16_t *o = out_row<kMode>(p, i, row, e);
+      if (o != nullptr) store16(o + col, left, words.w[i]);
+    }
   }
 }
 
@@ -489,7 +566,10 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int col
 
 // ---- the kernel ---------------------------------------------------------------------------
 
-template <int kMode, int kPair, bool kSplit>
+// kShifted: rows of the output (or of `kept`) may start in the middle of a sector.  A variant of
+// its own, as RowOut costs the others instructions: 8192 x 6784 x 256 gated takes 71 us, with
+// it 82.
+template <int kMode, int kPair, bool kSplit, bool kShifted>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
   using R = Ring_<kMode, kPair, kSplit>;
@@ -498,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kAMn = weight_grad(kMode);
   constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kAMn;
   constexpr bool kF32 = kMode == kFfnWeightGrad32;
-  constexpr bool kMoreRegs = kF32 || (kMode == kFfnGatedGrad && kPair == 2);
+  constexpr bool kMoreRegs = kF32 || (kMode == kFfnGatedGrad && !kSplit);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
   __shared__ uint32_t tmem_slot;
@@ -777,15 +857,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // the kept values of the next 32 columns are loaded while these are worked on
-      Kept next[2] = {};
+      const int col_w = t.n0 + j * cols, left_w = min(cols, p.N - col_w);
+      RowIn<kShifted> gates, ups;
+      const uint16_t *kept = p.kept + row * 2 * p.N + col_w;
       const auto ahead = [&](int c) {
         if constexpr (kMode == kFfnGatedGrad)
-          if (mine && c < cols) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              load_kept(p, row, t.n0 + j * cols + c + 16 * q, &next[q]);
+          if (mine && c < left_w) {
+            gates.load(kept + c, left_w - c);
+            ups.load(kept + p.N + c, left_w - c);
           }
       };
+      if constexpr (kMode == kFfnGatedGrad)
+        if (mine && left_w > 0) {
+          gates.begin(kept, left_w);
+          ups.begin(kept + p.N, left_w);
+        }
       ahead(0);
       if (mma) {
         // after a wait that gave up, the rest is walked without waiting
@@ -796,6 +882,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t ta = taddr + acc.slot * kTileN;
       if (work) {
+        RowOut outs[kOuts<kMode>];
+        const bool stream =
+            kShifted && m < write && !zero && left_w > 0 && !(kAMn && p.accumulate);
+        if (kShifted)
+#pragma unroll
+          for (int i = 0; i < kOuts<kMode>; ++i) {
+            uint16_t *at = out_row<kMode>(p, i, row, t.e);
+            outs[i].begin(at == nullptr ? nullptr : at + col_w, at == nullptr ? 0 : left_w);
+          }
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
           uint32_t d[32], d2[32];
@@ -811,7 +906,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             release<kPair>(&bar.acc_empty[acc.slot]);
           }
-          const Kept now[2] = {next[0], next[1]};
+          uint4 g4[4], u4[4];
+          if constexpr (kMode == kFfnGatedGrad) {
+            gates.take(g4);
+            ups.take(u4);
+          }
           ahead(c + 32);
           if (!ok) {
 #pragma unroll
@@ -830,9 +929,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[x] = join(d[16 * q + 2 * x], d[16 * q + 2 * x + 1]);
               u[x] = kMode == kFfnGated ? join(d2[16 * q + 2 * x], d2[16 * q + 2 * x + 1]) : 0;
             }
-            finish16<kMode>(p, row, t.e, col + 16 * q, v, u, now[q]);
+            Kept k;
+            if constexpr (kMode == kFfnGatedGrad)
+              k = {{g4[2 * q], g4[2 * q + 1]}, {u4[2 * q], u4[2 * q + 1]}};
+            if (stream) {
+              Words<kMode> words;
+              compute16<kMode>(p, v, u, k, words);
+#pragma unroll
+              for (int i = 0; i < kOuts<kMode>; ++i)
+                if (outs[i].left > 0) outs[i].put(words.w[i]);
+            } else {
+              finish16<kMode>(p, row, t.e, col + 16 * q, v, u, k);
+            }
           }
         }
+        if (stream)
+#pragma unroll
+          for (int i = 0; i < kOuts<kMode>; ++i) outs[i].end();
       } else if (mma) {
         release<kPair>(&bar.acc_empty[acc.slot]);
       }
@@ -856,7 +969,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum[kF32 ? kTileN / 2 : 1];
     if constexpr (kF32) {
       Ring<2> acc;
-      join_sums<1, kTileN / 2>(bar, ta, kTileN / 2, (ke - kb + kJoin - 1) / kJoin, work, acc, ok, sum);
+      join_sums<1, kTileN / 2>(bar, ta, kTileN / 2, (ke - kb + kJoin - 1) / kJoin, work, acc, ok,
+                               sum);
     } else {
       ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
       tc_fence_after();
@@ -938,7 +1052,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         up[x] = f32x2_pack(u[2 * x], u[2 * x + 1]);
       }
       Kept k{};
-      if constexpr (kMode == kFfnGatedGrad) load_kept(p, t.row0 + r, col, &k);
+      if constexpr (kMode == kFfnGatedGrad) {
+        const uint16_t *kept = p.kept + (t.row0 + r) * 2 * p.N + col;
+        load16(kept, p.N - col, k.g[0], k.g[1]);
+        load16(kept + p.N, p.N - col, k.u[0], k.u[1]);
+      }
       finish16<kMode>(p, t.row0 + r, t.e, col, vp, up, k);
     }
     if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
@@ -1008,11 +1126,11 @@ cudaError_t max_clusters(const void *func, int dev, int share, const cudaLaunchC
   return e;
 }
 
-template <int kMode, int kPair, bool kSplit>
+template <int kMode, int kPair, bool kSplit, bool kShifted = false>
 cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
                         cudaStream_t s, bool *fits) {
   using R = Ring_<kMode, kPair, kSplit>;
-  const auto kernel = ffn_kernel<kMode, kPair, kSplit>;
+  const auto kernel = ffn_kernel<kMode, kPair, kSplit, kShifted>;
   const size_t cum = weight_grad(kMode) ? 0 : sizeof(int) * (p.s.E + 1);
   const size_t smem = 1024 + (size_t)R::kSmem + cum;
   int dev = 0;
@@ -1106,8 +1224,8 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
       if (e != cudaSuccess || fits) return e;
     }
   } else if constexpr (kAMn) {
-    e = launch_pdl(ffn_segment_maps_kernel, (unsigned)std::min(2 * p.s.E, 8 * use), 32, 0, s, maps, p.s,
-                   static_cast<CUtensorMap *>(p.seg_maps));
+    e = launch_pdl(ffn_segment_maps_kernel, (unsigned)std::min(2 * p.s.E, 8 * use), 32, 0, s,
+                   maps, p.s, static_cast<CUtensorMap *>(p.seg_maps));
     if (e != cudaSuccess) return e;
   }
   const bool pair = use > 1 && (p.s.cnt_e == nullptr || p.max_segments > kPairRows<kMode> * p.s.E);
@@ -1115,8 +1233,15 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
     if (pair &&
         !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32, true))
       return cudaErrorInvalidValue;
-  if (pair) return launch_form<kMode, 2, false>(maps, p, tiles_of(2 * kTileM, 256), use, 2, s, nullptr);
-  return launch_form<kMode, 1, false>(maps, p, tiles_of(kTileM, 256), use, 1, s, nullptr);
+  const int64_t tiles = tiles_of(pair ? 2 * kTileM : kTileM, 256);
+  if constexpr (kMode != kFfnWeightGrad32) {
+    const auto on_32 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
+    if (p.N % 16 != 0 || !on_32(p.out) || !on_32(p.out2) || !on_32(p.kept))
+      return pair ? launch_form<kMode, 2, false, true>(maps, p, tiles, use, 2, s, nullptr)
+                  : launch_form<kMode, 1, false, true>(maps, p, tiles, use, 1, s, nullptr);
+  }
+  return pair ? launch_form<kMode, 2, false>(maps, p, tiles, use, 2, s, nullptr)
+              : launch_form<kMode, 1, false>(maps, p, tiles, use, 1, s, nullptr);
 }
 
 }  // namespace

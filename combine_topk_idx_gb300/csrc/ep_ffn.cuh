@@ -45,7 +45,6 @@ struct FfnParams {
   const uint16_t *kept;     // gated gradient: [rows, 2N] gate | up of the forward
   uint16_t *out;            // gated: act; gated gradient: of gate_up; else the output
   uint16_t *out2;           // gated: gate_up; gated gradient: act; may be nullptr
-  int out32, out2_32, kept32;  // every row (and its up half) starts on a 32-byte boundary
   int accumulate;           // weight gradient: out is added to
   int split;                // CTAs that share a tile's reduction
   void *seg_maps;           // workspace: two tensor maps per expert

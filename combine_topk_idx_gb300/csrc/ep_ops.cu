@@ -106,8 +106,6 @@ FfnParams ffn_params(const ep_handle *h, int64_t rows) {
   return p;
 }
 
-bool rows_on_32(const void *p, int64_t n) { return aligned(p, 32) && n % 16 == 0; }
-
 ep_status run_ffn(int mode, FfnParams &p, const ep_handle *h, ep_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const size_t bytes = ffn_workspace(mode, p);
@@ -413,8 +411,6 @@ ep_status ep_ffn_gated(const ep_handle *h, int64_t rows, int32_t ffn, int32_t k,
   p.K = k;
   p.out = static_cast<uint16_t *>(act);
   p.out2 = static_cast<uint16_t *>(gate_up);
-  p.out32 = ep::rows_on_32(act, ffn);
-  p.out2_32 = ep::rows_on_32(gate_up, ffn);
   return ep::run_ffn(ep::kFfnGated, p, h, stream);
 }
 
@@ -437,9 +433,6 @@ ep_status ep_ffn_gated_backward(const ep_handle *h, int64_t rows, int32_t ffn, i
   p.kept = static_cast<const uint16_t *>(gate_up);
   p.out = static_cast<uint16_t *>(grad_gate_up);
   p.out2 = static_cast<uint16_t *>(act);
-  p.out32 = ep::rows_on_32(grad_gate_up, ffn);
-  p.kept32 = ep::rows_on_32(gate_up, ffn);
-  p.out2_32 = ep::rows_on_32(act, ffn);
   return ep::run_ffn(ep::kFfnGatedGrad, p, h, stream);
 }
 
@@ -457,7 +450,6 @@ ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
   p.N = n;
   p.K = k;
   p.out = static_cast<uint16_t *>(out);
-  p.out32 = ep::rows_on_32(out, n);
   return ep::run_ffn(transposed ? ep::kFfnProductT : ep::kFfnProduct, p, h, stream);
 }
 
@@ -485,7 +477,6 @@ ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_
   p.M = n;
   p.N = k;
   p.out = static_cast<uint16_t *>(grad_w);
-  p.out32 = ep::aligned(grad_w, 32) && k % (grad_w_is_fp32 ? 8 : 16) == 0;
   p.accumulate = accumulate;
   return ep::run_ffn(grad_w_is_fp32 ? ep::kFfnWeightGrad32 : ep::kFfnWeightGrad, p, h, stream);
 }

@@ -221,6 +221,49 @@ def test_alignment_of_outputs(ep, op, rows):
             assert (flat[name][:off] == 7).all() and (flat[name][off + t.numel():] == 7).all()
 
 
+@pytest.mark.parametrize("width", [264, 272])
+@pytest.mark.parametrize("form", ["dense", "layout", "layout_many_rows"])
+@pytest.mark.parametrize("op", ["gated", "gated_bwd"])
+def test_alignment_of_one_output(ep, op, form, width):
+    """One of two outputs starts on 16 bytes, not 32, the other where it is allocated."""
+    h = None
+    if form != "dense":
+        T, E = (300, 8) if form == "layout" else (1200, 2)
+        h = make_handle(ep, T, 2, E, 1, T, 16)
+    rows = 900 if h is None else h.rows_alloc
+    call, outputs = calls(ep, h, rows, width, 144)[op]
+    want = outputs()
+    call(want, None)
+    for moved in want:
+        got = outputs()
+        flat = torch.full((got[moved].numel() + 48,), 7.0, dtype=torch.bfloat16, device="cuda")
+        n = got[moved].numel()
+        flat[8:8 + n] = 0
+        got[moved] = flat[8:8 + n].view(want[moved].shape)
+        call(got, None)
+        for name, t in want.items():
+            assert torch.equal(got[name], t)
+        assert (flat[:8] == 7).all() and (flat[8 + n:] == 7).all()
+
+
+@pytest.mark.parametrize("form", ["dense", "layout", "layout_many_rows"])
+def test_alignment_of_the_kept_values(ep, form):
+    h = None
+    if form != "dense":
+        T, E = (300, 8) if form == "layout" else (1200, 2)
+        h = make_handle(ep, T, 2, E, 1, T, 16)
+    rows, n = 900 if h is None else h.rows_alloc, 272
+    g = torch.Generator().manual_seed(12)
+    gy, gu = normal(g, rows, n).cuda(), normal(g, rows, 2 * n).cuda()
+    w = normal(g, *(() if h is None else (h.E,)), n, n, std=0.05).cuda()
+    moved = torch.empty(gu.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(gu.shape)
+    moved.copy_(gu)
+    want, got = (torch.zeros_like(gu) for _ in range(2))
+    ep.ep_ffn_gated_backward(h, gy, w, gu, grad_gate_up=want)
+    ep.ep_ffn_gated_backward(h, gy, w, moved, grad_gate_up=got)
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("op", ["gated", "gated_bwd", "product", "product_t"])
 @pytest.mark.parametrize("T", [60, 1000])
 def test_other_experts_weights(ep, op, T):
