@@ -306,31 +306,39 @@ struct RowOut {
 
 // 16 BF16 values from `a` on, of which `left` are there; zeros behind them.  A sector at once
 // where it starts there: in two halves it is fetched twice.
+template <bool kReadOnly>
+__device__ __forceinline__ uint4 load8(const uint16_t *a) {
+  return kReadOnly ? ld_stream_v4(a) : ld_plain_v4(a);
+}
+template <bool kReadOnly>
 __device__ __forceinline__ void load16(const uint16_t *a, int left, uint4 &lo, uint4 &hi) {
   if (left >= 16 && on_32(a)) {
     uint4 v[2];
-    ld_stream_v8(a, v);
+    if (kReadOnly)
+      ld_stream_v8(a, v);
+    else
+      ld_plain_v8(a, v);
     lo = v[0], hi = v[1];
     return;
   }
-  lo = left >= 8 ? ld_stream_v4(a) : make_uint4(0, 0, 0, 0);
-  hi = left >= 16 ? ld_stream_v4(a + 8) : make_uint4(0, 0, 0, 0);
+  lo = left >= 8 ? load8<kReadOnly>(a) : make_uint4(0, 0, 0, 0);
+  hi = left >= 16 ? load8<kReadOnly>(a + 8) : make_uint4(0, 0, 0, 0);
 }
 
 // A row's input, 32 columns after another, each loaded while the ones before are worked on.
 // In a row that starts in the middle of a sector the loads are 8 columns ahead of their use.
-template <bool kShifted>  // else no row does
+template <bool kShifted, bool kReadOnly>  // not shifted: no row does; not written by the kernel
 struct RowIn {
   uint4 r[4], first;
   bool odd;
   __device__ __forceinline__ void begin(const uint16_t *at, int left) {
     odd = kShifted && !on_32(at);
-    first = odd && left >= 8 ? ld_stream_v4(at) : make_uint4(0, 0, 0, 0);
+    first = odd && left >= 8 ? load8<kReadOnly>(at) : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void load(const uint16_t *at, int left) {
     const int skip = odd ? 8 : 0;
-    load16(at + skip, left - skip, r[0], r[1]);
-    load16(at + skip + 16, left - skip - 16, r[2], r[3]);
+    load16<kReadOnly>(at + skip, left - skip, r[0], r[1]);
+    load16<kReadOnly>(at + skip + 16, left - skip - 16, r[2], r[3]);
   }
   // the 32 columns loaded last
   __device__ __forceinline__ void take(uint4 (&v)[4]) {
@@ -441,7 +449,8 @@ __device__ __forceinline__ void zero16(const FfnParams &p, int64_t row, int e, i
 // Writes 16 columns of a row by themselves.
 template <int kMode>
 __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e, int col,
-                                         const Pairs &v, const Pairs &u, const Kept &k) {
+                                         const Pairs &v, const Pairs &u, const Kept &k,
+                                         bool add) {
   const int left = p.N - col;
   if constexpr (kMode == kFfnWeightGrad32) {
     float *o = reinterpret_cast<float *>(p.out) + ((int64_t)e * p.M + row) * p.N + col;
@@ -452,7 +461,7 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
 #pragma unroll
       for (int x = 0; x < 8; ++x)
         w[x] = (uint32_t)(v[4 * q + x / 2] >> (x & 1 ? 32 : 0));
-      if (p.accumulate) {
+      if (add) {
         const uint4 b0 = ld_plain_v4(o + 8 * q), b1 = ld_plain_v4(o + 8 * q + 4);
         const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -466,7 +475,7 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = v[i];
     if constexpr (kMode == kFfnWeightGrad)
-      if (p.accumulate) {
+      if (add) {
         const uint16_t *b = out_row<kMode>(p, 0, row, e) + col;
         const uint4 lo = ld_plain_v4(b);
         const uint4 hi = left >= 16 ? ld_plain_v4(b + 8) : make_uint4(0, 0, 0, 0);
@@ -506,11 +515,14 @@ struct Out {
     if (elect_one()) bulk_wait_read<kRing - 1>();
     __syncwarp();
   }
-  __device__ __forceinline__ void send(const CUtensorMap *map, int x, int y, int z) {
+  __device__ __forceinline__ void send(const CUtensorMap *map, int x, int y, int z, bool add) {
     fence_proxy_async_smem();
     __syncwarp();
     if (elect_one()) {
-      tma_store_3d(map, x, y, z, base + slot * kBytes);
+      if (add)
+        tma_add_3d(map, x, y, z, base + slot * kBytes);
+      else
+        tma_store_3d(map, x, y, z, base + slot * kBytes);
       bulk_commit();
     }
     if (++slot == kRing) slot = 0;
@@ -822,23 +834,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mma = t.blocks > 0;
       const int cols = t.cols / 2;  // of this warp
       const bool zero = !mma || !mine;
-      // all rows of the warp are written, and not added to
-      const bool whole = R::kTmaOut && quarter * 32 + 32 <= write && !p.accumulate;
       const int row_w = (int)t.row0 + mine0 + quarter * 32;
       if constexpr (kF32) {
         if (!mma && p.accumulate) continue;
         float sum[kMostCols];
         join_sums<kPair, kMostCols>(bar, taddr + j * cols, cols, (t.blocks + kJoin - 1) / kJoin,
                                     work, acc, ok, sum);
-        if (whole) {
+        if (R::kTmaOut) {
 #pragma unroll
           for (int c = 0; c < kMostCols; c += 32) {
             const int col = t.n0 + j * cols + c;
-            if (c >= cols || col >= p.N) break;
+            if (c >= cols || col >= p.N || !work) break;
             o.open();
 #pragma unroll
             for (int q = 0; q < 2; ++q) o.put16(q, zero, sum + c + 16 * q);
-            o.send(&maps.out, col, row_w, t.e);
+            o.send(&maps.out, col, row_w, t.e, p.accumulate);
           }
         } else if (m < write)
 #pragma unroll
@@ -851,27 +861,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (zero && !p.accumulate)
                 zero16<kMode>(p, row, t.e, col);
               else
-                finish16<kMode>(p, row, t.e, col, v, v, Kept{});
+                finish16<kMode>(p, row, t.e, col, v, v, Kept{}, p.accumulate);
             }
           }
         continue;
       }
       // the kept values of the next 32 columns are loaded while these are worked on
       const int col_w = t.n0 + j * cols, left_w = min(cols, p.N - col_w);
-      RowIn<kShifted> gates, ups;
-      const uint16_t *kept = p.kept + row * 2 * p.N + col_w;
+      RowIn<kShifted, kMode != kFfnWeightGrad> gates, ups;
+      const uint16_t *kept = kMode == kFfnWeightGrad ? out_row<kMode>(p, 0, row, t.e) + col_w
+                                                     : p.kept + row * 2 * p.N + col_w;
+      const bool adds = kMode == kFfnWeightGrad && p.accumulate;
+      const bool loads = mine && (kMode == kFfnGatedGrad || adds);
       const auto ahead = [&](int c) {
-        if constexpr (kMode == kFfnGatedGrad)
-          if (mine && c < left_w) {
-            gates.load(kept + c, left_w - c);
-            ups.load(kept + p.N + c, left_w - c);
-          }
-      };
-      if constexpr (kMode == kFfnGatedGrad)
-        if (mine && left_w > 0) {
-          gates.begin(kept, left_w);
-          ups.begin(kept + p.N, left_w);
+        if (loads && c < left_w) {
+          gates.load(kept + c, left_w - c);
+          if (kMode == kFfnGatedGrad) ups.load(kept + p.N + c, left_w - c);
         }
+      };
+      if (loads && left_w > 0) {
+        gates.begin(kept, left_w);
+        if (kMode == kFfnGatedGrad) ups.begin(kept + p.N, left_w);
+      }
       ahead(0);
       if (mma) {
         // after a wait that gave up, the rest is walked without waiting
@@ -883,8 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ta = taddr + acc.slot * kTileN;
       if (work) {
         RowOut outs[kOuts<kMode>];
-        const bool stream =
-            kShifted && m < write && !zero && left_w > 0 && !(kAMn && p.accumulate);
+        const bool stream = kShifted && m < write && !zero && left_w > 0;
         if (kShifted)
 #pragma unroll
           for (int i = 0; i < kOuts<kMode>; ++i) {
@@ -907,10 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             release<kPair>(&bar.acc_empty[acc.slot]);
           }
           uint4 g4[4], u4[4];
-          if constexpr (kMode == kFfnGatedGrad) {
-            gates.take(g4);
-            ups.take(u4);
-          }
+          if (kMode == kFfnGatedGrad || adds) gates.take(g4);
+          if constexpr (kMode == kFfnGatedGrad) ups.take(u4);
           ahead(c + 32);
           if (!ok) {
 #pragma unroll
@@ -932,6 +940,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Kept k;
             if constexpr (kMode == kFfnGatedGrad)
               k = {{g4[2 * q], g4[2 * q + 1]}, {u4[2 * q], u4[2 * q + 1]}};
+            if (adds)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                v[x] = f32x2_add_rn(v[x], pair_of(g4[2 * q + (x >> 2)], x & 3));
             if (stream) {
               Words<kMode> words;
               compute16<kMode>(p, v, u, k, words);
@@ -939,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < kOuts<kMode>; ++i)
                 if (outs[i].left > 0) outs[i].put(words.w[i]);
             } else {
-              finish16<kMode>(p, row, t.e, col + 16 * q, v, u, k);
+              finish16<kMode>(p, row, t.e, col + 16 * q, v, u, k, false);
             }
           }
         }
@@ -1054,10 +1066,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Kept k{};
       if constexpr (kMode == kFfnGatedGrad) {
         const uint16_t *kept = p.kept + (t.row0 + r) * 2 * p.N + col;
-        load16(kept, p.N - col, k.g[0], k.g[1]);
-        load16(kept + p.N, p.N - col, k.u[0], k.u[1]);
+        load16<true>(kept, p.N - col, k.g[0], k.g[1]);
+        load16<true>(kept + p.N, p.N - col, k.u[0], k.u[1]);
       }
-      finish16<kMode>(p, t.row0 + r, t.e, col, vp, up, k);
+      finish16<kMode>(p, t.row0 + r, t.e, col, vp, up, k, p.accumulate);
     }
     if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
   }

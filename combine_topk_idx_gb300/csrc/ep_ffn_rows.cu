@@ -1,12 +1,12 @@
 // The gated product and the product of a few rows: a decode step.
 //
 // At most 16 rows, with one matrix or in a layout, each with its expert's.  Every weight is
-// read once, so the time is that of reading the matrices.  A CTA takes 16 rows of the matrix (gated: 8 of the gate, the 8 of up beside them);
-// its warps share the reduction in chunks of 32 elements, each lane reading 16 bytes of a row,
-// several chunks ahead, straight into registers.  There 16 x 8 x 16 products of a warp take
-// them as they lie: a lane's eight elements are not the ones that the fragment's layout names,
-// but the same ones of the matrix and of x, and a sum has no order.  The warps' sums meet in
-// shared memory, in a fixed order.
+// read once, so the time is that of reading the matrices.  A CTA takes 16 rows of the matrix
+// (gated: 8 of the gate, the 8 of up beside them); its warps share the reduction in chunks of
+// 32 elements, each lane reading 16 bytes of a row, several chunks ahead, straight into
+// registers.  There 16 x 8 x 16 products of a warp take them as they lie: a lane's eight
+// elements are not the ones that the fragment's layout names, but the same ones of the matrix
+// and of x, and a sum has no order.  The warps' sums meet in shared memory, in a fixed order.
 //
 // No stages, no cluster, no TMEM: what the tcgen05 form does around its products is a third of
 // so short a call.  Weights read from HBM, 7168 x 4096 gated (58.7 MB, 8.8 us at what a copy
@@ -37,7 +37,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // kN: groups of 8 rows of x; kLayout: the rows are a layout's.
 template <bool kGated, int kN, bool kLayout>
-__global__ void __launch_bounds__(kThreads, kPerSm) ffn_rows_kernel(const __grid_constant__ FfnParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    ffn_rows_kernel(const __grid_constant__ FfnParams p) {
   constexpr int kAhead = 8 / kN;                    // chunks of a warp in flight
   __shared__ float part[kWarps][kUnit][8 * kN];
   __shared__ int busy[kFfnFewRows], found[kWarps];

@@ -42,6 +42,14 @@ __device__ __forceinline__ uint4 ld_plain_v4(const void *p) {
   return r;
 }
 
+__device__ __forceinline__ void ld_plain_v8(const void *p, uint4 (&v)[2]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                 "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+               : "l"(p)
+               : "memory");
+}
+
 // 16-byte streaming store (written once, not re-read by this kernel).
 __device__ __forceinline__ void st_stream_v4(void *p, uint4 v) {
   asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y),

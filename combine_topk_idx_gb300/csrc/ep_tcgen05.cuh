@@ -234,6 +234,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int 
       : "memory");
 }
 
+// Adds the box of fp32 values to what lies there; subnormal sums may become zeros.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, int x, int y, int z,
+                                           const void *ssrc) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
+      "[%0, {%1, %2, %3}], [%4];" ::"l"(map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(ssrc))
+      : "memory");
+}
+
 // Ends the rows (dimension 1) of a tensor map in global memory at `rows`, and makes
 // the change visible to later readers of the map.
 __device__ __forceinline__ void tma_replace_rows(CUtensorMap *map, uint32_t rows) {
