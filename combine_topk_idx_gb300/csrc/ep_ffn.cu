@@ -48,6 +48,7 @@
 // frees its TMEM and returns.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "ep_ffn.cuh"
@@ -580,8 +581,9 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int col
 
 // kShifted: rows of the output (or of `kept`) may start in the middle of a sector.  A variant of
 // its own, as RowOut costs the others instructions: 8192 x 6784 x 256 gated takes 71 us, with
-// it 82.
-template <int kMode, int kPair, bool kSplit, bool kShifted>
+// it 82.  kAdds: a weight's gradient in BF16 is added to what is there (64 experts of 2048 x
+// 4096, 4096 tokens, top-8, 408 us without adding; with 512 tokens 198, with this code too 239).
+template <int kMode, int kPair, bool kSplit, bool kShifted, bool kAdds>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
   using R = Ring_<kMode, kPair, kSplit>;
@@ -871,24 +873,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       RowIn<kShifted, kMode != kFfnWeightGrad> gates, ups;
       const uint16_t *kept = kMode == kFfnWeightGrad ? out_row<kMode>(p, 0, row, t.e) + col_w
                                                      : p.kept + row * 2 * p.N + col_w;
-      const bool adds = kMode == kFfnWeightGrad && p.accumulate;
-      const bool loads = mine && (kMode == kFfnGatedGrad || adds);
+      const bool loads = mine && (kMode == kFfnGatedGrad || kAdds);
+      // gate and up 32 columns ahead; of the values that are added to, 64: every second 32
+      // each (see kAdds: 578 us, 32 ahead 655; 8192 x 8192 x 4104, shifted, 405 and 376)
+      constexpr bool kFar = kAdds && !kShifted;
       const auto ahead = [&](int c) {
-        if (loads && c < left_w) {
-          gates.load(kept + c, left_w - c);
-          if (kMode == kFfnGatedGrad) ups.load(kept + p.N + c, left_w - c);
+        if (!loads || c >= left_w) return;
+        if (kFar && (c & 32)) {
+          ups.load(kept + c, left_w - c);
+          return;
         }
+        gates.load(kept + c, left_w - c);
+        if constexpr (kMode == kFfnGatedGrad) ups.load(kept + p.N + c, left_w - c);
       };
       if (loads && left_w > 0) {
         gates.begin(kept, left_w);
-        if (kMode == kFfnGatedGrad) ups.begin(kept + p.N, left_w);
+        ups.begin(kMode == kFfnGatedGrad ? kept + p.N : kept, left_w);
       }
       ahead(0);
+      if (kFar) ahead(32);
       if (mma) {
         // after a wait that gave up, the rest is walked without waiting
         if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
         tc_fence_after();
-      } else if (kAMn && p.accumulate) {
+      } else if (kAdds) {
         continue;
       }
       const uint32_t ta = taddr + acc.slot * kTileN;
@@ -917,9 +925,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             release<kPair>(&bar.acc_empty[acc.slot]);
           }
           uint4 g4[4], u4[4];
-          if (kMode == kFfnGatedGrad || adds) gates.take(g4);
+          if constexpr (kMode == kFfnGatedGrad || kAdds) {
+            if (kFar && (c & 32))
+              ups.take(g4);
+            else
+              gates.take(g4);
+          }
           if constexpr (kMode == kFfnGatedGrad) ups.take(u4);
-          ahead(c + 32);
+          ahead(c + (kFar ? 64 : 32));
           if (!ok) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) d[x] = d2[x] = 0x7fffffffu;
@@ -940,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Kept k;
             if constexpr (kMode == kFfnGatedGrad)
               k = {{g4[2 * q], g4[2 * q + 1]}, {u4[2 * q], u4[2 * q + 1]}};
-            if (adds)
+            if constexpr (kAdds)
 #pragma unroll
               for (int x = 0; x < 8; ++x)
                 v[x] = f32x2_add_rn(v[x], pair_of(g4[2 * q + (x >> 2)], x & 3));
@@ -1138,11 +1151,11 @@ cudaError_t max_clusters(const void *func, int dev, int share, const cudaLaunchC
   return e;
 }
 
-template <int kMode, int kPair, bool kSplit, bool kShifted = false>
+template <int kMode, int kPair, bool kSplit, bool kShifted = false, bool kAdds = false>
 cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
                         cudaStream_t s, bool *fits) {
   using R = Ring_<kMode, kPair, kSplit>;
-  const auto kernel = ffn_kernel<kMode, kPair, kSplit, kShifted>;
+  const auto kernel = ffn_kernel<kMode, kPair, kSplit, kShifted, kAdds>;
   const size_t cum = weight_grad(kMode) ? 0 : sizeof(int) * (p.s.E + 1);
   const size_t smem = 1024 + (size_t)R::kSmem + cum;
   int dev = 0;
@@ -1246,14 +1259,22 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
         !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32, true))
       return cudaErrorInvalidValue;
   const int64_t tiles = tiles_of(pair ? 2 * kTileM : kTileM, 256);
+  const auto launch = [&](auto shifted, auto adds) {
+    constexpr bool kShifted = decltype(shifted)::value, kAdds = decltype(adds)::value;
+    return pair
+               ? launch_form<kMode, 2, false, kShifted, kAdds>(maps, p, tiles, use, 2, s, nullptr)
+               : launch_form<kMode, 1, false, kShifted, kAdds>(maps, p, tiles, use, 1, s, nullptr);
+  };
+  const std::true_type yes;
+  const std::false_type no;
   if constexpr (kMode != kFfnWeightGrad32) {
     const auto on_32 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
-    if (p.N % 16 != 0 || !on_32(p.out) || !on_32(p.out2) || !on_32(p.kept))
-      return pair ? launch_form<kMode, 2, false, true>(maps, p, tiles, use, 2, s, nullptr)
-                  : launch_form<kMode, 1, false, true>(maps, p, tiles, use, 1, s, nullptr);
+    const bool shifted = p.N % 16 != 0 || !on_32(p.out) || !on_32(p.out2) || !on_32(p.kept);
+    if constexpr (kMode == kFfnWeightGrad)
+      if (p.accumulate) return shifted ? launch(yes, yes) : launch(no, yes);
+    if (shifted) return launch(yes, no);
   }
-  return pair ? launch_form<kMode, 2, false>(maps, p, tiles, use, 2, s, nullptr)
-              : launch_form<kMode, 1, false>(maps, p, tiles, use, 1, s, nullptr);
+  return launch(no, no);
 }
 
 }  // namespace

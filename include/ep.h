@@ -561,7 +561,8 @@ EP_API ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int
  * grad: BF16 [rows, n], gradient of the projection's output; a: BF16 [rows, k], its input.
  * grad_w: fp32 or BF16 [E, n, k]: sum over the rows r of expert e of
  *   grad[r, i] * a[r, j]; with `accumulate` added to what grad_w holds (in fp32, then
- *   rounded).  An expert without rows has zeros, or is left as it is.
+ *   rounded; a subnormal value may count as zero).  An expert without rows has zeros, or
+ *   is left as it is.
  * With a handle it uses a stream-ordered workspace of 256 bytes per expert.
  */
 EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
