@@ -121,7 +121,9 @@ def ep_ffn_weight_grad(handle: Optional[Handle], grad: torch.Tensor, a: torch.Te
 class GradPlan:
     """Gradients and where their clipped values go, listed once for many calls of
     :func:`ep_clip_grads`: a trainer's gradients stay where they are from step to
-    step.  Holds the tensors, and reads nothing of them but on the GPU."""
+    step.  Holds the tensors and their memory, and reads nothing of them but on the
+    GPU.  A tensor that is given other memory (``set_``, ``.data``, a storage that is
+    resized) needs a new plan: this one goes on with what it listed."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
                  out: Optional[Sequence[torch.Tensor]] = None):
@@ -146,6 +148,7 @@ class GradPlan:
                 raise ValueError(f"output {i} is {o.dtype} {tuple(o.shape)}, its gradient "
                                  f"{g.dtype} {tuple(g.shape)}")
         n = len(self.grads)
+        self._memory = [t.untyped_storage() for t in self.grads + self.out]
         self._grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
         self._out = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
         self._numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])

@@ -126,12 +126,15 @@ __device__ __forceinline__ float squares(const void *base, int len, float scale,
 
 template <int kT>
 __device__ __forceinline__ double piece_squares(const char *g, const Piece &q, int tid) {
-  float s = q.bf16 ? squares<true, kT>(g, q.len, 1.f, tid) : squares<false, kT>(g, q.len, 1.f, tid);
+  const auto sum = [&](float scale) {
+    return q.bf16 ? squares<true, kT>(g, q.len, scale, tid)
+                  : squares<false, kT>(g, q.len, scale, tid);
+  };
+  float s = sum(1.f);
   double w = 1.0;
   if (!(s > 1e-30f && s < INFINITY)) {
     const bool big = !(s <= 1e-30f);
-    const float scale = big ? 0x1p-80f : 0x1p90f;
-    s = q.bf16 ? squares<true, kT>(g, q.len, scale, tid) : squares<false, kT>(g, q.len, scale, tid);
+    s = sum(big ? 0x1p-80f : 0x1p90f);
     w = big ? 0x1p160 : 0x1p-180;
   }
   return (double)s * w;
@@ -418,7 +421,10 @@ cudaError_t allow_cluster() {
   std::lock_guard<std::mutex> g(mu);
   if (std::find(done.begin(), done.end(), dev) != done.end()) return cudaSuccess;
   e = cudaFuncSetAttribute(grad_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done.push_back(dev);
+  if (e == cudaSuccess) try {
+      done.push_back(dev);
+    } catch (...) {  // no memory: opted in again
+    }
   return e;
 }
 

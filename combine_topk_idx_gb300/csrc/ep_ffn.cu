@@ -1147,7 +1147,10 @@ cudaError_t max_clusters(const void *func, int dev, int share, const cudaLaunchC
       return cudaSuccess;
     }
   const cudaError_t e = cudaOccupancyMaxActiveClusters(out, func, &lc);
-  if (e == cudaSuccess) known.push_back({func, dev, share, *out});
+  if (e == cudaSuccess) try {
+      known.push_back({func, dev, share, *out});
+    } catch (...) {  // no memory: looked up again
+    }
   return e;
 }
 

@@ -158,7 +158,8 @@ bool ffn_few_rows(int mode, const FfnParams &p) {
 cudaError_t launch_ffn_rows(int mode, const FfnParams &p, int sms, cudaStream_t s) {
   const bool layout = p.s.cnt_e != nullptr, gated = mode == kFfnGated;
   if (most_rows(p) <= 8) {
-    if (layout) return gated ? launch<true, 1, true>(p, sms, s) : launch<false, 1, true>(p, sms, s);
+    if (layout)
+      return gated ? launch<true, 1, true>(p, sms, s) : launch<false, 1, true>(p, sms, s);
     return gated ? launch<true, 1, false>(p, sms, s) : launch<false, 1, false>(p, sms, s);
   }
   if (layout) return gated ? launch<true, 2, true>(p, sms, s) : launch<false, 2, true>(p, sms, s);

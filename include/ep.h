@@ -511,6 +511,7 @@ EP_API ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const 
  * (infinities and NaN too) reaches no other row and no weight's gradient.
  * Matrices are BF16, dense; arrays of rows that the products read (x, grad_out, a,
  * grad) may be row-strided (elements, a multiple of 8, at least the row's length).
+ * Outputs overlap neither each other nor an input.
  * Sizes n, k, ffn: multiples of 8, at most EP_MAX_GEMM (ffn: half of that).
  * 16-byte aligned.  Sums are fp32, each output is rounded once.  The same call gives
  * the same bits each time.  A device-side wait that gives up leaves NaN in the tiles

@@ -154,6 +154,25 @@ def test_plan_is_used_again(ep):
         assert float(n) > 0.5 and abs(float(after) - 0.5) < 0.5 * 2 ** -7
 
 
+def test_plan_keeps_the_memory_it_listed(ep):
+    """A tensor that is given other memory: the plan works on the memory of before, which stays
+    allocated, and on nobody else's."""
+    grads = tensors([70000, 33], 14)
+    first = list(grads)
+    plan = ep.plan_grads(grads)
+    want = float(ep.ep_grad_norm(plan))
+    old = first[0].data
+    at = old.data_ptr()
+    first[0].data = torch.zeros_like(old)
+    del old
+    others = [torch.full_like(first[0], 9.0) for _ in range(8)]
+    assert all(t.data_ptr() != at for t in others)
+    assert float(ep.ep_clip_grads(plan, 0.5)) == want
+    assert (first[0] == 0).all() and all((t == 9).all() for t in others)
+    fresh = ep.plan_grads(grads)
+    assert float(ep.ep_grad_norm(fresh)) < want
+
+
 def test_same_bits(ep):
     grads = tensors([123457, 1000, 7, 300000], 17)
     got = []
