@@ -534,12 +534,14 @@ struct Out {
   }
 };
 
-// An epilogue warp has read an accumulator.
+// An epilogue warp has read an accumulator: what it loaded is in registers (the loads were
+// waited for), so nothing needs a release, which in a pair would wait for all its stores:
+// 1,600 cycles at the end of each tile.
 template <int kPair>
 __device__ __forceinline__ void release(uint64_t *acc_empty) {
   if ((threadIdx.x & 31) != 0) return;
   if constexpr (kPair == 2)
-    mbar_arrive_cluster(cluster_map(acc_empty, 0));
+    mbar_arrive_cluster_relaxed(cluster_map(acc_empty, 0));
   else
     mbar_arrive(acc_empty);
 }
@@ -619,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   if (!kAMn && p.s.cnt_e != nullptr) count_tiles(p, kTileM * kPair, cum, warp_sum);
   __syncthreads();
-  if constexpr (kPair == 2) {  // the other CTA's barriers are ready
-    cluster_arrive_release();
+  if constexpr (kPair == 2) {  // the other CTA's barriers are ready (fenced by its thread 0)
+    cluster_arrive_relaxed();
     cluster_wait();
   }
   tc_fence_after();
@@ -1090,8 +1092,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (kPair == 2) {
     // neither CTA leaves while the other may still arrive on its barriers, read
-    // its operands or write into its TMEM
-    cluster_arrive_release();
+    // its operands or write into its TMEM (relaxed: no wait for the output's stores)
+    cluster_arrive_relaxed();
     cluster_wait();
   }
   if (warp == 1) tmem_dealloc_group<kPair>(tmem, kTmemColumns);
