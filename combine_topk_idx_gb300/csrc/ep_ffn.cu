@@ -174,32 +174,32 @@ __device__ __forceinline__ void count_tiles(const FfnParams &p, int rows_per_til
   __syncthreads();
 }
 
-// a / b, of 32 bits where they suffice (they nearly always do, and 64 take 100 cycles more).
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+// a / b with b's Reciprocal: at most one short before the correction.  (Divisions by registers
+// take a few hundred cycles, and a tile's place several of them, before the first copy.)
+__device__ __forceinline__ uint32_t divide(uint32_t a, Reciprocal b) {
+  const uint32_t q = __umulhi(a, b.magic);
+  return q + (a - q * b.of >= b.of ? 1 : 0);
 }
 
 // (row, column) of tile k of tr x tc: kRaster row tiles pass over the columns together.
-__device__ __forceinline__ void raster(int64_t k, int tr, int tc, int *r, int *c) {
-  const int64_t per = (int64_t)kRaster * tc;
-  const int g = (int)divide(k, per) * kRaster;
-  const int n = min(kRaster, tr - g);
-  const int u = (int)(k - (int64_t)g * tc);
-  *c = u / n;
+__device__ __forceinline__ void raster(int k, int tr, int tc, Reciprocal per, int *r, int *c) {
+  const int g = (int)divide((uint32_t)k, per) * kRaster;
+  const int n = min(kRaster, tr - g), u = k - g * tc;
+  // u < 2^14, n <= 16: (u + 1/2) / n lies 1/32 off every whole number, fp32 2^-9 off at most
+  *c = (int)(((float)u + 0.5f) * rcp_approx((float)n));
   *r = g + u - *c * n;
 }
 
 // Tile i.  Whole warps.
 template <int kMode, int kCols>
-__device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, int64_t i,
+__device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, int i,
                                           int rows_per_tile, int tiles_n) {
   Tile t;
   int r, c;
   if constexpr (weight_grad(kMode)) {
     const int tr = (p.M + rows_per_tile - 1) / rows_per_tile;
-    const int64_t per = (int64_t)tr * tiles_n;
-    t.e = (int)divide(i, per);
-    raster(i - t.e * per, tr, tiles_n, &r, &c);
+    t.e = (int)divide((uint32_t)i, p.expert_tiles);
+    raster(i - t.e * (int)p.expert_tiles.of, tr, tiles_n, p.raster_tiles, &r, &c);
     const SegmentRows s = segment_rows(p.s, t.e);
     t.row0 = (int64_t)r * rows_per_tile;
     t.used = t.write = min(rows_per_tile, p.M - (int)t.row0);
@@ -208,13 +208,14 @@ __device__ __forceinline__ Tile find_tile(const FfnParams &p, const int *cum, in
   } else {
     int lo = 0;
     if (p.s.cnt_e == nullptr) {
-      raster(i, (int)((p.s.rows + rows_per_tile - 1) / rows_per_tile), tiles_n, &r, &c);
+      raster(i, (int)((p.s.rows + rows_per_tile - 1) / rows_per_tile), tiles_n, p.raster_tiles,
+             &r, &c);
     } else {
       const int lane = threadIdx.x & 31;
       lo = -1;  // the last expert with cum[e] * tiles_n <= i
       for (int e = lane; e - lane < p.s.E; e += 32)
-        lo += __popc(__ballot_sync(0xffffffffu, e < p.s.E && (int64_t)cum[e] * tiles_n <= i));
-      raster(i - (int64_t)cum[lo] * tiles_n, cum[lo + 1] - cum[lo], tiles_n, &r, &c);
+        lo += __popc(__ballot_sync(0xffffffffu, e < p.s.E && cum[e] * tiles_n <= i));
+      raster(i - cum[lo] * tiles_n, cum[lo + 1] - cum[lo], tiles_n, p.raster_tiles, &r, &c);
     }
     const SegmentRows s = segment_rows(p.s, lo);
     const int64_t off = (int64_t)r * rows_per_tile;
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair == 2 || kSplit ? (int)cluster_rank() : 0;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar.full[s], 1);
       mbar_init(&bar.empty[s], 1);
@@ -620,39 +621,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc_group<kPair>(&tmem_slot, kTmemColumns);
   griddep_wait();
   if (!kAMn && p.s.cnt_e != nullptr) count_tiles(p, kTileM * kPair, cum, warp_sum);
+  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
+  const int tiles_n = (p.N + kCols - 1) / kCols;
+  int tiles;
+  if constexpr (kAMn)
+    tiles = p.s.E * (int)p.expert_tiles.of;
+  else
+    tiles = (p.s.cnt_e == nullptr ? (int)((p.s.rows + kTileM * kPair - 1) / (kTileM * kPair))
+                                  : cum[p.s.E]) * tiles_n;
+  // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
+  const int first = (int)blockIdx.x >> (kSplit ? p.split >> 1 : kPair - 1);
+  const int step = (int)p.groups.of;
+  // The tiles of the last round, where they are at most half as many as there are pairs,
+  // are halved, so that the round takes half as long.
+  const int last = kPair == 2 ? tiles - (int)divide((uint32_t)tiles, p.groups) * step : 0;
+  const int whole_tiles = tiles - (2 * last <= step ? last : 0);
+  const int items = whole_tiles + 2 * (tiles - whole_tiles);
+  const auto tile_at = [&](int i) {
+    const int h = i - whole_tiles;
+    const bool half = kPair == 2 && h >= 0;
+    Tile t = find_tile<kMode, kCols>(p, cum, half ? whole_tiles + (h >> 1) : i, kTileM * kPair,
+                                     tiles_n);
+    if (half) {
+      t.cols = kCols / 2;
+      t.n0 += (h & 1) * t.cols;
+      if (t.n0 >= p.N) t.used = t.write = t.blocks = 0;
+    }
+    return t;
+  };
+  Tile tile0;  // while the barriers and TMEM are got ready
+  if (first < items) tile0 = tile_at(first);
   __syncthreads();
-  if constexpr (kPair == 2) {  // the other CTA's barriers are ready (fenced by its thread 0)
+  if constexpr (kPair == 2) {  // the other CTA's barriers are ready (it fenced them)
     cluster_arrive_relaxed();
     cluster_wait();
   }
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  constexpr int kCols = kMode == kFfnGated ? kTileN / 2 : kTileN;
-  const int tiles_n = (p.N + kCols - 1) / kCols;
-  int64_t tiles;
-  if constexpr (kAMn)
-    tiles = (int64_t)p.s.E * ((p.M + kTileM * kPair - 1) / (kTileM * kPair)) * tiles_n;
-  else
-    tiles = (p.s.cnt_e == nullptr ? (p.s.rows + kTileM * kPair - 1) / (kTileM * kPair)
-                                  : (int64_t)cum[p.s.E]) * tiles_n;
-  // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
-  const int share = kSplit ? p.split : kPair;
-  const int64_t first = blockIdx.x / share, step = gridDim.x / share;
-  // The tiles of the last round, where they are at most half as many as there are pairs,
-  // are halved, so that the round takes half as long.
-  const int64_t last = kPair == 2 ? tiles % step : 0;
-  const int64_t whole_tiles = tiles - (2 * last <= step ? last : 0);
-  const int64_t items = whole_tiles + 2 * (tiles - whole_tiles);
-  const auto tile_at = [&](int64_t i) {
-    if (kPair != 2 || i < whole_tiles)
-      return find_tile<kMode, kCols>(p, cum, i, kTileM * kPair, tiles_n);
-    const int h = (int)(i - whole_tiles);
-    Tile t = find_tile<kMode, kCols>(p, cum, whole_tiles + (h >> 1), kTileM * kPair, tiles_n);
-    t.cols = kCols / 2;
-    t.n0 += (h & 1) * t.cols;
-    if (t.n0 >= p.N) t.used = t.write = t.blocks = 0;
-    return t;
-  };
   // this CTA's part of a tile's reduction
   const auto part = [&](int blocks, int r) {
     return kSplit ? (int)((int64_t)blocks * r / p.split) : (r == 0 ? 0 : blocks);
@@ -672,9 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acquired = -1;  // the expert whose maps were last made visible
     const uint32_t full0 = kPair == 2 ? cluster_map(&bar.full[0], 0) : smem_u32(&bar.full[0]);
     const int half_rank = kPair == 2 ? rank : 0;
-    Tile next;
-    if (first < items) next = tile_at(first);
-    for (int64_t i = first; i < items && ok; i += step) {
+    Tile next = tile0;
+    for (int i = first; i < items && ok; i += step) {
       const Tile t = next;
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
       if (kb == ke) {
@@ -771,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kStages> st;
     Ring<2> acc;
     const uint32_t smem0 = smem_u32(smem);
-    for (int64_t i = first; i < items && ok; i += step) {
-      const Tile t = tile_at(i);
+    for (int i = first; i < items && ok; i += step) {
+      const Tile t = i == first ? tile0 : tile_at(i);
       const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
       if (kb == ke) continue;
       const uint32_t idesc = idesc_bf16(kTileM * kPair, acc_columns<kMode>(t), kAMn, kBMn);
@@ -826,8 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kMostCols = kCols / 2;  // of a warp
     Out o{smem + kStages * R::kStageBytes + (warp - 4) * R::kOutBytes};
     Ring<2> acc;
-    for (int64_t i = first; i < items; i += step) {
-      const Tile t = tile_at(i);
+    for (int i = first; i < items; i += step) {
+      const Tile t = i == first ? tile0 : tile_at(i);
       const int half = half_of<kMode, kPair>(t);
       const int mine0 = kPair == 2 ? rank * half : 0;
       const int used = kPair == 2 ? max(0, min(half, t.used - mine0)) : t.used;
@@ -987,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each CTA gets the sums of kTileN / split columns from all of them, in shared memory
     // over the stages: [source][4 columns][row][4], so that a warp writes 512 bytes in a row
     // (rows apart, a tile of 128 rows took 25 us to change hands).
-    const Tile t = tile_at(first);
+    const Tile t = tile0;
     const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
     const int kb = part(t.blocks, rank), ke = part(t.blocks, rank + 1);
     const int quarter = warp & 3, j = (warp - 4) >> 2, m = quarter * 32 + lane;
@@ -1157,7 +1161,7 @@ cudaError_t max_clusters(const void *func, int dev, int share, const cudaLaunchC
 }
 
 template <int kMode, int kPair, bool kSplit, bool kShifted = false, bool kAdds = false>
-cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int use, int share,
+cudaError_t launch_form(const Maps &maps, FfnParams p, int64_t tiles, int use, int share,
                         cudaStream_t s, bool *fits) {
   using R = Ring_<kMode, kPair, kSplit>;
   const auto kernel = ffn_kernel<kMode, kPair, kSplit, kShifted, kAdds>;
@@ -1194,6 +1198,13 @@ cudaError_t launch_form(const Maps &maps, const FfnParams &p, int64_t tiles, int
     if (!*fits) return cudaSuccess;
   }
   lc.gridDim.x = (unsigned)(groups * share);
+  constexpr int kCols = kMode == kFfnGated ? R::kCols / 2 : R::kCols;
+  const int64_t tiles_n = (p.N + kCols - 1) / kCols;
+  const int64_t expert = (p.M + kTileM * kPair - 1) / (kTileM * kPair) * tiles_n;
+  if (2 * tiles > 0x7fffffffLL) return cudaErrorInvalidValue;  // (more than memory holds)
+  p.groups = Reciprocal((uint32_t)groups);
+  p.raster_tiles = Reciprocal((uint32_t)(kRaster * tiles_n));
+  p.expert_tiles = Reciprocal((uint32_t)std::max<int64_t>(1, expert));
   return cudaLaunchKernelEx(&lc, kernel, maps, p);
 }
 

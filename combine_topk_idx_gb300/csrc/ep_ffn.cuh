@@ -34,6 +34,13 @@ __device__ __forceinline__ SegmentRows segment_rows(const Segments &s, int e) {
   return {r0, used, s.zero_padding ? min((int64_t)__ldg(s.psum_e + e + 1) - r0, left) : used};
 }
 
+// A divisor, and 2^32 / it rounded down.
+struct Reciprocal {
+  uint32_t of, magic;
+  Reciprocal() = default;
+  explicit Reciprocal(uint32_t b) : of(b), magic((uint32_t)(0xffffffffull / b)) {}
+};
+
 struct FfnParams {
   Segments s;
   int64_t max_segments;     // experts that can have rows; of a layout, its slots
@@ -47,6 +54,9 @@ struct FfnParams {
   uint16_t *out2;           // gated: gate_up; gated gradient: act; may be nullptr
   int accumulate;           // weight gradient: out is added to
   int split;                // CTAs that share a tile's reduction
+  // filled in by the launch: CTAs, pairs or clusters that take tiles; tiles of kRaster rows
+  // of tiles; weight gradient: of an expert's matrix
+  Reciprocal groups, raster_tiles, expert_tiles;
   void *seg_maps;           // workspace: two tensor maps per expert
   unsigned *err;            // the handle's error word (EP_ERRBIT_TIMEOUT), or nullptr
 };
