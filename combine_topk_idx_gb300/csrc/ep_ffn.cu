@@ -24,8 +24,9 @@
 //   kPair 1   persistent, a CTA per SM
 //   kPair 2   persistent, two CTAs on a 256 x 256 tile: each holds its 128 rows and
 //             half of the columns' operand
-//   kSplit    few tiles: 128 x 128 ones, a cluster per tile, its CTAs share the
-//             reduction and add up through each other's shared memory, in a fixed order
+//   kSplit    few tiles: 128 x 128 ones (of pairs 256 x 256), a cluster per tile, its CTAs
+//             or pairs share the reduction and add up through each other's shared memory, in
+//             a fixed order
 // Up to 16 rows in all are ep_ffn_rows.cu's, if gated or a product on W's rows.
 //
 // What bounds it (times move by 8 % with the GPU and what it ran before: the power cap sets
@@ -73,7 +74,8 @@ constexpr int kJoin = 8;
 // 168: 128 * 88 + 256 * 208 are the 168 * 384 of the launch.  With 72 the copies' loop
 // spilt and took 690 cycles a block, whose products take 512.
 constexpr int kControlRegs = 88, kEpilogueRegs = 208;
-constexpr int kMaxSplit = 4;   // CTAs that share a tile's reduction
+constexpr int kMaxSplit = 4;   // CTAs, or pairs, that share a tile's reduction
+constexpr int kPairSplitBlocks = 24;  // of each pair; see launch_mode
 constexpr int kRaster = 16;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
@@ -89,7 +91,7 @@ __host__ __device__ constexpr bool weight_grad(int mode) {
 // 385 (all measured on the same GPU).
 template <int kMode, int kPair, bool kSplit>
 struct Ring_ {
-  static constexpr int kCols = kSplit ? 128 : 256;  // accumulator columns of a tile
+  static constexpr int kCols = kSplit && kPair == 1 ? 128 : 256;  // accumulator columns of a tile
   static constexpr int kABytes = kTileM * kBlockK * 2;
   static constexpr int kBBytes = kCols / kPair * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
@@ -605,6 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *cum = reinterpret_cast<int *>(smem + R::kSmem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair == 2 || kSplit ? (int)cluster_rank() : 0;
+  // of the CTAs of a pair, and the cluster's rank of its first; the part of a reduction
+  const int half_rank = kPair == 2 ? rank & 1 : 0, leader = rank - half_rank;
+  const int part_rank = kSplit ? rank >> (kPair - 1) : 0;
 
   if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
@@ -630,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tiles = (p.s.cnt_e == nullptr ? (int)((p.s.rows + kTileM * kPair - 1) / (kTileM * kPair))
                                   : cum[p.s.E]) * tiles_n;
   // a cluster of a split tile, or a pair, or a CTA, takes every step-th tile
-  const int first = (int)blockIdx.x >> (kSplit ? p.split >> 1 : kPair - 1);
+  const int first = (int)blockIdx.x >> (kSplit ? (p.split >> 1) + kPair - 1 : kPair - 1);
   const int step = (int)p.groups.of;
   // The tiles of the last round, where they are at most half as many as there are pairs,
   // are halved, so that the round takes half as long.
-  const int last = kPair == 2 ? tiles - (int)divide((uint32_t)tiles, p.groups) * step : 0;
+  const int last = kPair == 2 && !kSplit ? tiles - (int)divide((uint32_t)tiles, p.groups) * step : 0;
   const int whole_tiles = tiles - (2 * last <= step ? last : 0);
   const int items = whole_tiles + 2 * (tiles - whole_tiles);
   const auto tile_at = [&](int i) {
@@ -660,9 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   // this CTA's part of a tile's reduction
   const auto part = [&](int blocks, int r) {
-    return kSplit ? (int)((int64_t)blocks * r / p.split) : (r == 0 ? 0 : blocks);
+    return kSplit ? (int)((int64_t)blocks * r >> (p.split >> 1)) : (r == 0 ? 0 : blocks);
   };
-  const int part_rank = kSplit ? rank : 0;
   bool ok = true;
 
   if (warp < 4) {
@@ -675,8 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kStages> st;
     int issued = 0;  // stages filled, counted up to kStages
     int acquired = -1;  // the expert whose maps were last made visible
-    const uint32_t full0 = kPair == 2 ? cluster_map(&bar.full[0], 0) : smem_u32(&bar.full[0]);
-    const int half_rank = kPair == 2 ? rank : 0;
+    const uint32_t full0 = kPair == 2 ? cluster_map(&bar.full[0], leader) : smem_u32(&bar.full[0]);
     Tile next = tile0;
     for (int i = first; i < items && ok; i += step) {
       const Tile t = next;
@@ -711,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *a = smem + st.slot * R::kStageBytes, *b = a + R::kABytes;
         const uint32_t full = full0 + st.slot * 8;
         if (elect_one()) {
-          if (kPair == 1 || rank == 0) mbar_arrive_expect_tx(&bar.full[st.slot], bytes);
+          if (half_rank == 0) mbar_arrive_expect_tx(&bar.full[st.slot], bytes);
           if constexpr (kAMn) {
             const int y = (int)(t.k0 + (int64_t)k * kBlockK);
 #pragma unroll
@@ -762,14 +765,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
         // copies in flight: slots below st.slot in this round, the others in the
         // round before
-        if (kPair == 1 || rank == 0)
+        if (half_rank == 0)
           for (int s = 0; s < kStages; ++s)
             if (s < st.slot || issued == kStages)
               wait(&bar.full[s], s < st.slot ? st.phase : st.phase ^ 1);
       }
     }
     __syncwarp();
-   } else if (warp == 1 && (kPair == 1 || rank == 0)) {
+   } else if (warp == 1 && half_rank == 0) {
     // ---------------- products ----------------
     constexpr int kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
     Ring<kStages> st;
@@ -796,8 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < kBlockK / 16; ++q)
             mma_bf16<kPair>(tmem + acc.slot * kTileN, da + q * kAStep, db + q * kBStep, idesc,
                             q > 0 || !begins);
-          mma_commit_group<kPair>(&bar.empty[st.slot]);
-          if (ends) mma_commit_group<kPair>(&bar.acc_full[acc.slot]);
+          mma_commit_group<kPair>(&bar.empty[st.slot], (uint16_t)(3 << leader));
+          if (ends) mma_commit_group<kPair>(&bar.acc_full[acc.slot], (uint16_t)(3 << leader));
         }
         __syncwarp();
         st.next();
@@ -833,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = first; i < items; i += step) {
       const Tile t = i == first ? tile0 : tile_at(i);
       const int half = half_of<kMode, kPair>(t);
-      const int mine0 = kPair == 2 ? rank * half : 0;
+      const int mine0 = half_rank * half;
       const int used = kPair == 2 ? max(0, min(half, t.used - mine0)) : t.used;
       const int write = kPair == 2 ? max(0, min(half, t.write - mine0)) : t.write;
       const int64_t row = t.row0 + mine0 + m;
@@ -990,12 +993,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kMoreRegs) setmaxnreg_inc<kEpilogueRegs>();
     // Each CTA gets the sums of kTileN / split columns from all of them, in shared memory
     // over the stages: [source][4 columns][row][4], so that a warp writes 512 bytes in a row
-    // (rows apart, a tile of 128 rows took 25 us to change hands).
+    // (rows apart, a tile of 128 rows took 25 us to change hands).  Its own part it reads from
+    // TMEM again (in 32 bits, where it is in registers: from there too).
     const Tile t = tile0;
     const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
-    const int kb = part(t.blocks, rank), ke = part(t.blocks, rank + 1);
+    const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
+    const int half = half_of<kMode, kPair>(t), mine0 = half_rank * half;
+    const int used = kPair == 2 ? max(0, min(half, t.used - mine0)) : t.used;
+    const int write = kPair == 2 ? max(0, min(half, t.write - mine0)) : t.write;
+    const int64_t row0 = t.row0 + mine0;
     const int quarter = warp & 3, j = (warp - 4) >> 2, m = quarter * 32 + lane;
-    const bool work = quarter * 32 < t.used;  // any row of the warp
+    const bool work = quarter * 32 < used;  // any row of the warp
     const uint32_t ta = tmem + (uint32_t)(quarter * 32) * 65536u + j * (kTileN / 2);
     float sum[kF32 ? kTileN / 2 : 1];
     if constexpr (kF32) {
@@ -1015,10 +1023,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cc = kMode == kFfnGated ? c : j * (kTileN / 2) + c;
         const int per = kMode == kFfnGated ? wide / 2 : wide;
         const int to = cc / per;
+        if (!kF32 && to == part_rank) return;
         const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
         const uint32_t base =
-            cluster_map(smem, to) + (uint32_t)(((rank * (wide / 4) + piece) * kTileM + m) * 16);
-        if (m < t.used)
+            cluster_map(smem, to * kPair + half_rank) +
+            (uint32_t)(((part_rank * (wide / 4) + piece) * kTileM + m) * 16);
+        if (m < used)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             st_cluster_v4(base + (uint32_t)(x * kTileM * 16), v[4 * x], v[4 * x + 1],
@@ -1035,6 +1045,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
 #pragma unroll 1
         for (int c = 0; c < kTileN / 2; c += 32) {
+          const int cc = kMode == kFfnGated ? c : j * (kTileN / 2) + c;
+          const int per = kMode == kFfnGated ? wide / 2 : wide;
+          if (per >= 32 && cc / per == part_rank) continue;
           uint32_t d[32];
           tmem_load32(ta + c, d);
           tmem_load_wait(d);
@@ -1055,41 +1068,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait();
     const int per = kMode == kFfnGated ? wide / 2 : wide, groups = per / 16;
     const float4 *in = reinterpret_cast<const float4 *>(smem);
-    for (int i = threadIdx.x - 128; i < t.write * groups; i += 32 * kEpilogueWarps) {
-      const int g = i / t.write, r = i - g * t.write;
-      const int col = t.n0 + rank * per + g * 16;
-      if (col >= p.N) continue;
+    const uint32_t own = tmem + (uint32_t)(quarter * 32) * 65536u + part_rank * per;
+    // two warps to 32 rows, each with every second 16 columns
+    for (int g = j; g < groups && quarter * 32 < write; g += 2) {
+      const int col = t.n0 + part_rank * per + g * 16;
+      if (col >= p.N) break;
       float v[16], u[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x) v[x] = u[x] = 0.f;
+      if constexpr (!kF32) {
+        uint32_t d[16], d2[16];
+        tmem_load16(own + g * 16, d);
+        if constexpr (kMode == kFfnGated) tmem_load16(own + kTileN / 2 + g * 16, d2);
+        tmem_load_wait(d);
+        if constexpr (kMode == kFfnGated) tmem_load_wait(d2);
 #pragma unroll
-      for (int s = 0; s < kMaxSplit; ++s) {
-        if (s >= S) continue;
-        const float4 *from = in + (s * (wide / 4) + g * 4) * kTileM + r;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 a = from[x * kTileM];
-          v[4 * x] += a.x, v[4 * x + 1] += a.y, v[4 * x + 2] += a.z, v[4 * x + 3] += a.w;
-          if constexpr (kMode == kFfnGated) {
-            const float4 b = from[(per / 4 + x) * kTileM];
-            u[4 * x] += b.x, u[4 * x + 1] += b.y, u[4 * x + 2] += b.z, u[4 * x + 3] += b.w;
-          }
+        for (int x = 0; x < 16; ++x) {
+          v[x] = ok ? __uint_as_float(d[x]) : __uint_as_float(0x7fffffffu);
+          if constexpr (kMode == kFfnGated) u[x] = ok ? __uint_as_float(d2[x]) : v[x];
         }
       }
-      Pairs vp, up;
+      if (m < write) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        vp[x] = f32x2_pack(v[2 * x], v[2 * x + 1]);
-        up[x] = f32x2_pack(u[2 * x], u[2 * x + 1]);
+        for (int s = 0; s < kMaxSplit; ++s) {
+          if (s >= S || (!kF32 && s == part_rank)) continue;
+          const float4 *from = in + (s * (wide / 4) + g * 4) * kTileM + m;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 a = from[x * kTileM];
+            v[4 * x] += a.x, v[4 * x + 1] += a.y, v[4 * x + 2] += a.z, v[4 * x + 3] += a.w;
+            if constexpr (kMode == kFfnGated) {
+              const float4 b = from[(per / 4 + x) * kTileM];
+              u[4 * x] += b.x, u[4 * x + 1] += b.y, u[4 * x + 2] += b.z, u[4 * x + 3] += b.w;
+            }
+          }
+        }
+        Pairs vp, up;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          vp[x] = f32x2_pack(v[2 * x], v[2 * x + 1]);
+          up[x] = f32x2_pack(u[2 * x], u[2 * x + 1]);
+        }
+        Kept k{};
+        if constexpr (kMode == kFfnGatedGrad) {
+          const uint16_t *kept = p.kept + (row0 + m) * 2 * p.N + col;
+          load16<true>(kept, p.N - col, k.g[0], k.g[1]);
+          load16<true>(kept + p.N, p.N - col, k.u[0], k.u[1]);
+        }
+        finish16<kMode>(p, row0 + m, t.e, col, vp, up, k, p.accumulate);
       }
-      Kept k{};
-      if constexpr (kMode == kFfnGatedGrad) {
-        const uint16_t *kept = p.kept + (t.row0 + r) * 2 * p.N + col;
-        load16<true>(kept, p.N - col, k.g[0], k.g[1]);
-        load16<true>(kept + p.N, p.N - col, k.u[0], k.u[1]);
-      }
-      finish16<kMode>(p, t.row0 + r, t.e, col, vp, up, k, p.accumulate);
+      __syncwarp();
     }
+    tc_fence_before();
     if (!ok && lane == 0 && p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
   }
   __syncwarp();
@@ -1185,7 +1215,7 @@ cudaError_t launch_form(const Maps &maps, FfnParams p, int64_t tiles, int use, i
   lc.attrs = attr;
   lc.numAttrs = share > 1 ? 2 : 1;
   // (a pair's last tiles may be halved)
-  int64_t groups = std::min<int64_t>(use / share, kPair == 2 ? 2 * tiles : tiles);
+  int64_t groups = std::min<int64_t>(use / share, kPair == 2 && !kSplit ? 2 * tiles : tiles);
   if (share > 1) {
     int fit = 0;  // clusters that run at a time: no tile waits for one that does not
     e = max_clusters(reinterpret_cast<const void *>(kernel), dev, share, lc, &fit);
@@ -1254,22 +1284,44 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
     return r * tiles_n;
   };
   if (p.s.cnt_e == nullptr) {
-    // Few tiles: smaller ones, and clusters of 2 or 4 share each one's reduction, as long as
-    // all of them run at once.
-    const int64_t tiles = tiles_of(kTileM, 128);
+    // Few tiles: a cluster of 2 or 4 CTAs, or pairs of them, shares each one's reduction, as
+    // long as all run at once: CTAs on smaller tiles where there are enough, else pairs.  A
+    // block of either takes an SM 512 cycles, of a pair's half tile 384, but the sums that
+    // change hands cost 2,000 to 6,000 once, hence kPairSplitBlocks: 384 x 4096 x 7168 gated
+    // takes 24.3 us, unshared 30.7; 256 x 7168 x 2048 (32 blocks) 13.0 and 11.9.  Where CTAs
+    // share as often, pairs are no faster: 256 x 4096 x 7168 gated 23.2 and, by CTAs, 22.2.
+    const int64_t tiles = tiles_of(kTileM, 128), pairs = tiles_of(2 * kTileM, 256);
     const int64_t blocks = ((kAMn ? p.s.rows : p.K) + kBlockK - 1) / kBlockK;
     for (p.split = kMaxSplit; p.split > 1; p.split /= 2) {
-      if (tiles * p.split > use || blocks < p.split * 4) continue;
       bool fits = false;
-      e = launch_form<kMode, 1, true>(maps, p, tiles, use, p.split, s, &fits);
-      if (e != cudaSuccess || fits) return e;
+      if (tiles * p.split <= use && blocks >= p.split * 4) {
+        e = launch_form<kMode, 1, true>(maps, p, tiles, use, p.split, s, &fits);
+        if (e != cudaSuccess || fits) return e;
+      }
+      if constexpr (!kAMn)
+        if (p.s.rows > kTileM && 2 * pairs * p.split <= use &&
+            blocks >= p.split * kPairSplitBlocks) {
+          e = launch_form<kMode, 2, true>(maps, p, pairs, use, 2 * p.split, s, &fits);
+          if (e != cudaSuccess || fits) return e;
+        }
     }
   } else if constexpr (kAMn) {
     e = launch_pdl(ffn_segment_maps_kernel, (unsigned)std::min(2 * p.s.E, 8 * use), 32, 0, s,
                    maps, p.s, static_cast<CUtensorMap *>(p.seg_maps));
     if (e != cudaSuccess) return e;
   }
-  const bool pair = use > 1 && (p.s.cnt_e == nullptr || p.max_segments > kPairRows<kMode> * p.s.E);
+  bool pair = use > 1 && (p.s.cnt_e == nullptr || p.max_segments > kPairRows<kMode> * p.s.E);
+  if constexpr (!kAMn)
+    if (pair && p.s.cnt_e == nullptr) {
+      // By the rounds of tiles, in cycles of a block: a round of pairs' tiles 512, of their
+      // halves 384, of single CTAs' 600.  The latter have fewer empty rows: 640 x 7168 x 4096
+      // (84 tiles for 76 pairs, 140 for 152 CTAs) takes 28 us, by pairs 40; 1152 x 4096 x 4096
+      // 24 and 37; 1024 x 7168 x 2048 (two rounds of either) 21 by pairs.
+      const int64_t ones = tiles_of(kTileM, 256), twos = tiles_of(2 * kTileM, 256), at = use / 2;
+      const int64_t last = twos % at;
+      pair = 600 * ((ones + use - 1) / use) >=
+             512 * (twos / at) + (last == 0 ? 0 : 2 * last <= at ? 384 : 512);
+    }
   if constexpr (kMode == kFfnWeightGrad32)
     if (pair &&
         !make_map(&maps.out, p.out, p.N, p.M, p.s.E, p.N, (int64_t)p.N * p.M, 32, 32, true))

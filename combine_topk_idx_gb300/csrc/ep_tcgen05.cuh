@@ -67,6 +67,17 @@ __device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+
 // 64 columns of this warp's 32 lanes: lane l gets (l, column 0..63) from addr.
 __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t *r) {
   asm volatile(
@@ -181,14 +192,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 // Arrives on `bar`, for a pair on the barrier at that offset in both CTAs, when
 // the products issued so far by this thread are done.
 template <int kCtas>
-__device__ __forceinline__ void mma_commit_group(uint64_t *bar) {
+__device__ __forceinline__ void mma_commit_group(uint64_t *bar, uint16_t ctas = 3) {
   if constexpr (kCtas == 1)
     mma_commit(bar);
   else
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(ctas)
         : "memory");
 }
 
