@@ -35,8 +35,8 @@
 // library's product.  What an epilogue reads and writes competes with the operands for L2:
 // the gated gradient of that size moves 670 MB more and takes 353 us.  128 rows per expert,
 // the weights' bytes: 256 experts of 4096 x 7168, 2.46 ms for 15.9 GB, 6.5 TB/s.  Few rows
-// through one matrix, latency: 128 x 2048 x 7168 takes 10.3 us, of them 1.2 before the first
-// copy and 3 from the last product to the end.
+// through one matrix, latency: 128 x 2048 x 7168 takes 10.0 us, of them 1.2 before the first
+// copy and 2 from the last product to the end.
 //
 // Rows that are not an expert's own never reach its results: in the row products
 // they are other rows of the accumulator; in the weight gradient, where they
@@ -585,9 +585,9 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int col
 // ---- the kernel ---------------------------------------------------------------------------
 
 // kShifted: rows of the output (or of `kept`) may start in the middle of a sector.  A variant of
-// its own, as RowOut costs the others instructions: 8192 x 6784 x 256 gated takes 71 us, with
+// its own, as RowOut costs the others instructions: 8192 x 6784 x 256 gated took 71 us, with
 // it 82.  kAdds: a weight's gradient in BF16 is added to what is there (64 experts of 2048 x
-// 4096, 4096 tokens, top-8, 408 us without adding; with 512 tokens 198, with this code too 239).
+// 4096, 512 tokens, top-8, without adding: 198 us, with the code for it 239).
 template <int kMode, int kPair, bool kSplit, bool kShifted, bool kAdds>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnParams p) {
@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int step = (int)p.groups.of;
   // The tiles of the last round, where they are at most half as many as there are pairs,
   // are halved, so that the round takes half as long.
-  const int last = kPair == 2 && !kSplit ? tiles - (int)divide((uint32_t)tiles, p.groups) * step : 0;
+  const int last =
+      kPair == 2 && !kSplit ? tiles - (int)divide((uint32_t)tiles, p.groups) * step : 0;
   const int whole_tiles = tiles - (2 * last <= step ? last : 0);
   const int items = whole_tiles + 2 * (tiles - whole_tiles);
   const auto tile_at = [&](int i) {
@@ -884,7 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                      : p.kept + row * 2 * p.N + col_w;
       const bool loads = mine && (kMode == kFfnGatedGrad || kAdds);
       // gate and up 32 columns ahead; of the values that are added to, 64: every second 32
-      // each (see kAdds: 578 us, 32 ahead 655; 8192 x 8192 x 4104, shifted, 405 and 376)
+      // each (4096 tokens of kAdds' layout 578 us, 32 ahead 655; 8192 x 8192 x 4104, shifted,
+      // 405 and 376)
       constexpr bool kFar = kAdds && !kShifted;
       const auto ahead = [&](int c) {
         if (!loads || c >= left_w) return;
@@ -1239,12 +1241,13 @@ cudaError_t launch_form(const Maps &maps, FfnParams p, int64_t tiles, int use, i
 }
 
 // Rows per expert, on average, above which pairs of CTAs take the tiles of a layout.  With 64
-// experts of 4096 x 4096, a gated product of 128 rows each takes 366 us by single CTAs and 370
-// by pairs (half of their 256 rows are empty), of 192 rows 430 and 385, of 1024 1450 and 1310;
-// a weight gradient in BF16 of 128 rows 448 and 650 us (all of it stores, which two CTAs wait
-// for together), of 1024 1570 and 1415, in 32 bits 895 and 840.
+// experts of 4096 x 4096, a gated product of 128 rows each takes 365 us by single CTAs and 364
+// by pairs, of 160 rows 422 and 372, of 1024 1477 and 1300; the product on W as it lies of 128
+// rows 342 and 350, of 160 406 and 358; a weight gradient in BF16 of 128 rows 430 and 470 us
+// (all of it stores, which two CTAs wait for together), of 192 520 and 485, of 1024 1590 and
+// 1400, in 32 bits of 128 820 and 785.
 template <int kMode>
-constexpr int64_t kPairRows = kMode == kFfnWeightGrad ? 384 : kMode == kFfnWeightGrad32 ? 0 : 160;
+constexpr int64_t kPairRows = kMode == kFfnWeightGrad ? 176 : kMode == kFfnWeightGrad32 ? 0 : 128;
 
 template <int kMode>
 cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
