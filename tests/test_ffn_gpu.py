@@ -30,6 +30,41 @@ def test_one_matrix(ep, op, rows, n, k):
     check(ep, op, None, rows, n, k, seed=rows + n)
 
 
+# 129 to some 600 rows: a long reduction is shared by four pairs of CTAs, or two, with rows and
+# columns that end inside a tile; and tiles of single CTAs where those of pairs need a round more
+SOME_HUNDRED = [(250, 2568, 6200), (129, 3400, 3208), (300, 3400, 3208), (520, 2600, 3200),
+                (600, 6704, 200)]
+
+
+@pytest.mark.parametrize("rows,n,k", SOME_HUNDRED)
+@pytest.mark.parametrize("op", ["gated", "gated_bwd", "product", "product_t"])
+def test_some_hundred_rows(ep, op, rows, n, k):
+    # half as many columns for gate and up, which share a tile
+    check(ep, op, None, rows, n // 16 * 8 if op == "gated" else n, k, seed=rows)
+
+
+@pytest.mark.parametrize("op", ["gated", "gated_bwd", "product", "product_t"])
+def test_some_hundred_rows_in_graphs(ep, op):
+    """The shared reduction gives the same bits eagerly, on another stream and replayed."""
+    call, outputs = calls(ep, None, 300, 3400, 3208)[op]
+    want, side, again = (outputs() for _ in range(3))
+    call(want, None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    call(side, s)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(again, None)
+    for _ in range(2):
+        for t in again.values():
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for name, t in want.items():
+            assert torch.equal(side[name], t) and torch.equal(again[name], t)
+
+
 # name: (T, K, E, R, M, A, zero_pad, sync, fixed, drop, n, k)
 LAYOUTS = {
     "one_row": (1, 1, 1, 1, 1, 1, True, True, False, 0.0, 256, 128),
