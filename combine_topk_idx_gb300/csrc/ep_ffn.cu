@@ -808,6 +808,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ends) acc.next();
       }
     }
+    // The other CTA's last arrivals here: nothing else waits for them, and relaxed as they
+    // are, the cluster's barrier at the end does not either.
+    if constexpr (kPair == 2 && !kSplit)
+      for (int b = 0; b < 2 && ok; ++b, acc.next())
+        ok = __all_sync(0xffffffffu, wait(&bar.acc_empty[acc.slot], acc.phase ^ 1));
     if (!ok) {
       if (elect_one()) {
         if (p.err != nullptr) atomicOr(p.err, EP_ERRBIT_TIMEOUT);
