@@ -140,6 +140,7 @@ template <bool kGated, int kN, bool kLayout>
 cudaError_t launch(const FfnParams &p, int sms, cudaStream_t s) {
   constexpr int kOut = kGated ? kUnit / 2 : kUnit;
   const int64_t experts = std::min<int64_t>(p.max_segments, p.s.E);
+  if (experts == 0) return cudaSuccess;  // a layout of no tokens: rows, but none in use
   const int64_t grid = std::min<int64_t>(sms * kPerSm, experts * ((p.N + kOut - 1) / kOut));
   return launch_pdl(ffn_rows_kernel<kGated, kN, kLayout>, (unsigned)grid, kThreads, 0, s, p);
 }

@@ -97,6 +97,21 @@ def test_layouts(ep, op, name):
     h.free()
 
 
+# no tokens: rows are allocated (fixed slabs, an upper bound with alignment) and none is in use
+NO_TOKENS = {"fixed": (1, False, False, True), "bound": (8, True, False, False),
+             "bound_unpadded": (100, False, False, False), "no_rows": (8, True, True, False)}
+
+
+@pytest.mark.parametrize("name", sorted(NO_TOKENS))
+@pytest.mark.parametrize("op", OPS)
+def test_no_tokens(ep, op, name):
+    A, zp, sync, fixed = NO_TOKENS[name]
+    h = make_handle(ep, 0, 2, 4, 2, 16, A, zp, sync, fixed)
+    assert (h.rows_alloc == 0) == (name == "no_rows")
+    check(ep, op, h, h.rows_alloc, 136, 72)
+    h.free()
+
+
 # more rows per expert than a pair of CTAs takes alone, several tiles of each, a last round
 # of halved tiles, reductions over several joins
 WIDE = {"two_experts": (1300, 1, 2, 1, 1300, 16, 520, 200),
