@@ -49,8 +49,7 @@ cudaError_t launch_combine_weights(const CombineWeightsParams &p, cudaStream_t s
   const int64_t n = (int64_t)p.T * p.K;
   if (n == 0) return cudaSuccess;
   const int64_t blocks = (n + kWeightThreads - 1) / kWeightThreads;
-  combine_weights_kernel<<<(unsigned)blocks, kWeightThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_plain(combine_weights_kernel, (unsigned)blocks, kWeightThreads, 0, s, p);
 }
 
 }  // namespace ep

@@ -304,6 +304,19 @@ inline int sms_to_use(int device, int sm_cap) {
 cudaError_t launch_geometry(const void *func, int threads, size_t smem, int *device,
                             int *per_sm);
 
+// Launch that returns its own error.  (cudaGetLastError behind <<<>>> also returns one
+// that an earlier call has reported already.)
+template <typename... P, typename... A>
+cudaError_t launch_plain(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t s, A... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  return cudaLaunchKernelEx(&lc, kern, args...);
+}
+
 // Launch with programmatic dependent launch: the kernel may start while its
 // predecessor drains and calls griddep_wait() before it touches memory.
 template <typename... P, typename... A>

@@ -899,8 +899,7 @@ cudaError_t launch_layout(const LayoutParams &p, cudaStream_t s, int *kernels) {
   err = launch_geometry(reinterpret_cast<const void *>(layout_assign_kernel), NT, smem_assign,
                         &dev, nullptr);
   if (err != cudaSuccess) return err;
-  layout_count_kernel<<<p.num_blocks, NTC, smem_count, s>>>(p);
-  err = cudaGetLastError();
+  err = launch_plain(layout_count_kernel, p.num_blocks, NTC, smem_count, s, p);
   if (err != cudaSuccess) return err;
   // assign may launch while count drains (programmatic dependent launch); it
   // waits on griddepcontrol before touching count's outputs

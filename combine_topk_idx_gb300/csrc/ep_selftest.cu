@@ -29,8 +29,9 @@ extern "C" ep_status ep_selftest_bounded_wait(int32_t wait_us, int32_t signal,
       cudaSuccess)
     return EP_ERR_CUDA;
   // attempts of at most 1 us each
-  selftest_wait_kernel<<<1, 32, 0, s>>>(wait_us, 1000u, signal ? 1 : 0);
-  if (cudaGetLastError() != cudaSuccess) return EP_ERR_CUDA;
+  if (ep::launch_plain(selftest_wait_kernel, 1, 32, 0, s, wait_us, 1000u, signal ? 1 : 0) !=
+      cudaSuccess)
+    return EP_ERR_CUDA;
   unsigned bits = 0;
   if (cudaMemcpyFromSymbolAsync(&bits, g_selftest_err, sizeof(bits), 0, cudaMemcpyDeviceToHost, s) !=
       cudaSuccess)
