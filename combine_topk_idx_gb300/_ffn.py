@@ -118,12 +118,31 @@ def ep_ffn_weight_grad(handle: Optional[Handle], grad: torch.Tensor, a: torch.Te
     return grad_w
 
 
+class _Memory:
+    """The storages of tensors, each once, and where they were when they were listed.
+    Holding a storage keeps its memory unless someone resizes it, which gives the memory
+    back: :meth:`moved` says so."""
+
+    def __init__(self, tensors):
+        storages = (t.untyped_storage() for t in tensors)
+        self.storages = list({s._cdata: s for s in storages}.values())
+        self._at = list(map(torch.UntypedStorage.data_ptr, self.storages))
+        self._bytes = list(map(torch.UntypedStorage.nbytes, self.storages))
+
+    def moved(self) -> bool:
+        # 0.12 us a storage; both, as one emptied and filled again may be where it was
+        return (list(map(torch.UntypedStorage.data_ptr, self.storages)) != self._at
+                or list(map(torch.UntypedStorage.nbytes, self.storages)) != self._bytes)
+
+
 class GradPlan:
     """Gradients and where their clipped values go, listed once for many calls of
     :func:`ep_clip_grads`: a trainer's gradients stay where they are from step to
-    step.  Holds the tensors and their memory, and reads nothing of them but on the
-    GPU.  A tensor that is given other memory (``set_``, ``.data``, a storage that is
-    resized) needs a new plan: this one goes on with what it listed."""
+    step.  Holds the tensors and their storages, and reads nothing of them but on the
+    GPU.  A tensor that is given another storage (``set_``, ``.data``) needs a new plan:
+    this one goes on with the memory it listed.  A storage that is resized
+    (``untyped_storage().resize_``, ``resize_`` to more than it holds) has given that
+    memory back, and calls with the plan are refused."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
                  out: Optional[Sequence[torch.Tensor]] = None):
@@ -148,11 +167,12 @@ class GradPlan:
                 raise ValueError(f"output {i} is {o.dtype} {tuple(o.shape)}, its gradient "
                                  f"{g.dtype} {tuple(g.shape)}")
         n = len(self.grads)
-        self._memory = [t.untyped_storage() for t in self.grads + self.out]
         self._grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
         self._out = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
         self._numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
         self._f32 = (ctypes.c_uint8 * n)(*[t.dtype == torch.float32 for t in self.grads])
+        # behind the addresses: data_ptr() gives a lazy copy memory of its own
+        self._memory = _Memory(self.grads if out is None else self.grads + self.out)
         self._refuse_overlap()
 
     def _refuse_overlap(self):
@@ -184,6 +204,8 @@ def _clip(grads, max_norm, out, write, norm, stream):
         if out is not None:
             raise ValueError("a plan has its outputs")
         plan = grads
+        if plan._memory.moved():
+            raise ValueError("a storage of the plan was resized: its tensors need a new plan")
     else:
         plan = GradPlan(grads, out)
     max_norm = float(max_norm)

@@ -173,6 +173,28 @@ def test_plan_keeps_the_memory_it_listed(ep):
     assert float(ep.ep_grad_norm(fresh)) < want
 
 
+@pytest.mark.parametrize("which", ["grads", "out"])
+@pytest.mark.parametrize("how", ["emptied", "emptied_and_filled", "grown"])
+def test_plan_of_resized_storages_is_refused(ep, how, which):
+    """Their memory may be anybody's."""
+    grads = tensors([70000, 33], 15)
+    out = [torch.zeros_like(t) for t in grads]
+    plan, kept = ep.plan_grads(grads, out), ep.plan_grads(grads[1:])
+    want = float(ep.ep_clip_grads(plan, 0.5))
+    t = (grads if which == "grads" else out)[0]
+    if how == "grown":
+        t.resize_(200_000)
+    else:
+        t.untyped_storage().resize_(0)
+    if how == "emptied_and_filled":
+        t.untyped_storage().resize_(1000)
+    with pytest.raises(ValueError, match="resized"):
+        ep.ep_clip_grads(plan, 0.5)
+    with pytest.raises(ValueError, match="resized"):
+        ep.ep_grad_norm(plan)
+    assert want > 0.5 and float(ep.ep_clip_grads(kept, 0.5)) > 0.5
+
+
 def test_same_bits(ep):
     grads = tensors([123457, 1000, 7, 300000], 17)
     got = []

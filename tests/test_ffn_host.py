@@ -117,3 +117,26 @@ def test_global_norm():
     assert abs(O.global_norm(g) - np.sqrt((g[0] ** 2).sum() + (g[1] ** 2).sum())) < 1e-12
     assert O.global_norm([np.full(4, 1e300)]) == 2e300
     assert O.global_norm([]) == 0.0
+
+
+@pytest.mark.parametrize("how", ["emptied", "emptied_and_filled", "shrunk", "grown"])
+def test_memory_that_was_given_back(how):
+    """What a plan holds: a storage keeps its memory until it is resized, which is noticed."""
+    import torch
+    from combine_topk_idx_gb300._ffn import _Memory
+    a, b = torch.ones(1000), torch.ones(500)
+    m = _Memory([a, a[:3], b, b[7:], torch.empty(0)])
+    assert len(m.storages) == 3 and not m.moved()
+    a.mul_(2)
+    b.resize_(100)  # within the storage
+    at = a.data_ptr()
+    a.data = torch.zeros(1000)  # the storage of before is held
+    assert not m.moved() and m.storages[0].data_ptr() == at
+    s = b.untyped_storage()
+    if how == "grown":
+        b.resize_(100_000)
+    else:
+        s.resize_(1000 if how == "shrunk" else 0)
+    if how == "emptied_and_filled":
+        s.resize_(1200)
+    assert m.moved()
