@@ -134,6 +134,11 @@ class _Memory:
         return (list(map(torch.UntypedStorage.data_ptr, self.storages)) != self._at
                 or list(map(torch.UntypedStorage.nbytes, self.storages)) != self._bytes)
 
+    def record_stream(self, stream):
+        """The memory is in use on ``stream``."""
+        for s in self.storages:
+            torch.empty(0, dtype=torch.uint8, device=s.device).set_(s).record_stream(stream)
+
 
 class GradPlan:
     """Gradients and where their clipped values go, listed once for many calls of
@@ -216,8 +221,8 @@ def _clip(grads, max_norm, out, write, norm, stream):
         raise ValueError(f"the gradients are on cuda:{plan.device}, the call runs on "
                          f"cuda:{c.device}")
     if c.other is not None:
-        for t in plan.grads + (plan.out if write else []):
-            t.record_stream(c.other)
+        # the listed memory's, which the tensors may have left
+        plan._memory.record_stream(c.other)
     if norm is None:
         norm = c.empty(dtype=torch.float32)
     c(len(plan.grads), plan._grads, plan._out if write else None, plan._numels, plan._f32,

@@ -195,6 +195,26 @@ def test_plan_of_resized_storages_is_refused(ep, how, which):
     assert want > 0.5 and float(ep.ep_clip_grads(kept, 0.5)) > 0.5
 
 
+def test_memory_in_use_on_another_stream_is_kept(ep):
+    """A tensor leaves the listed memory, the plan is called on another stream and dropped:
+    the memory is nobody else's before that stream is done with it."""
+    grads = tensors([700_000, 33], 16)
+    plan = ep.plan_grads(grads)
+    size, at = grads[0].untyped_storage().nbytes(), grads[0].data_ptr()
+    grads[0].data = torch.zeros(700_000, device="cuda")
+    torch.cuda.synchronize()
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # some 0.2 s
+    ep.ep_clip_grads(plan, 0.5, stream=side)
+    done.record(side)
+    del plan
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert not done.query()
+    assert all(t.data_ptr() != at for t in others)
+    torch.cuda.synchronize()
+
+
 def test_same_bits(ep):
     grads = tensors([123457, 1000, 7, 300000], 17)
     got = []
