@@ -70,6 +70,12 @@ constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 // registers, rounded to nearest: the tensor cores cut off what does not fit, which
 // over 4096 rows is 4.4e-6 of the result, over 512 at a time 4.7e-7.
 constexpr int kJoin = 8;
+// The same of one in BF16, whose rounding is 2^-8.  The tensor cores add 16 rows at a time and
+// cut off at most 2^-23 of the sum so far: at most 2^-10 of sums of one sign after this many
+// blocks (131072 rows).  Without end, 2^20 positive products were off by 4e-3 beside the
+// rounding and 2^22 by 2e-2.
+constexpr int kLongBlocks = 2048;
+constexpr int kSumsBytes = kTileM * 256 * 4;  // of a CTA between two parts
 // registers of a control and of an epilogue thread where the latter need more than
 // 168: 128 * 88 + 256 * 208 are the 168 * 384 of the launch.  With 72 the copies' loop
 // spilt and took 690 cycles a block, whose products take 512.
@@ -80,8 +86,11 @@ constexpr int kRaster = 16;    // row tiles that pass over the columns together
 constexpr int kWaitIters = 4000;          // x kWaitHintNs: gives up after ~2 s
 constexpr uint32_t kWaitHintNs = 500000;
 
+__host__ __device__ constexpr bool weight_grad16(int mode) {
+  return mode == kFfnWeightGrad || mode == kFfnWeightGradLong;
+}
 __host__ __device__ constexpr bool weight_grad(int mode) {
-  return mode == kFfnWeightGrad || mode == kFfnWeightGrad32;
+  return weight_grad16(mode) || mode == kFfnWeightGrad32;
 }
 
 // A pair's weight gradients in 32 bits leave by TMA, through 8 KB of each epilogue warp: 256
@@ -478,7 +487,7 @@ __device__ __forceinline__ void finish16(const FfnParams &p, int64_t row, int e,
     Pairs s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = v[i];
-    if constexpr (kMode == kFfnWeightGrad)
+    if constexpr (weight_grad16(kMode))
       if (add) {
         const uint16_t *b = out_row<kMode>(p, 0, row, e) + col;
         const uint4 lo = ld_plain_v4(b);
@@ -582,6 +591,62 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int col
     for (int c = 0; c < kHalf; ++c) sum[c] = __uint_as_float(0x7fffffffu);
 }
 
+// A tile whose sum is of several accumulators, `apart` columns from one another: `cols` columns
+// from `taddr`.  Between them the sums are in memory, where no other thread looks at them (one
+// part is 2,048 blocks, a million cycles; held in registers they made every tile of such a call
+// 8 % slower).
+template <int kMode, int kPair>
+__device__ __forceinline__ void sum_parts(const FfnParams &p, Barriers &bar, const Tile &t,
+                                          uint32_t taddr, int apart, int cols, int col,
+                                          int64_t row, bool mine, bool work, Ring<2> &acc,
+                                          bool &ok) {
+  constexpr int kMine = 32 * kEpilogueWarps;
+  float4 *sums = p.sums + (int64_t)blockIdx.x * (kSumsBytes / 16) + (threadIdx.x - 128);
+  const int parts = (t.blocks + kLongBlocks - 1) / kLongBlocks;
+  for (int i = 0; i < parts; ++i) {
+    if (ok) ok = __all_sync(0xffffffffu, wait(&bar.acc_full[acc.slot], acc.phase));
+    tc_fence_after();
+    if (work) {
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t d[32];
+        tmem_load32(taddr + acc.slot * apart + c, d);
+        tmem_load_wait(d);
+        float4 *at = sums + (c >> 2) * kMine;
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          v[x] = make_float4(__uint_as_float(d[4 * x]), __uint_as_float(d[4 * x + 1]),
+                             __uint_as_float(d[4 * x + 2]), __uint_as_float(d[4 * x + 3]));
+          if (i > 0) {
+            const float4 b = at[x * kMine];
+            v[x].x += b.x, v[x].y += b.y, v[x].z += b.z, v[x].w += b.w;
+          }
+          if (!ok) v[x].x = v[x].y = v[x].z = v[x].w = __uint_as_float(0x7fffffffu);
+          if (i + 1 < parts) at[x * kMine] = v[x];
+        }
+        if (i + 1 == parts && mine)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (col + c + 16 * q >= p.N) break;
+            Pairs w;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              w[2 * x] = f32x2_pack(v[4 * q + x].x, v[4 * q + x].y);
+              w[2 * x + 1] = f32x2_pack(v[4 * q + x].z, v[4 * q + x].w);
+            }
+            finish16<kMode>(p, row, t.e, col + c + 16 * q, w, w, Kept{}, p.accumulate);
+          }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+    }
+    release<kPair>(&bar.acc_empty[acc.slot]);
+    acc.next();
+  }
+}
+
 // ---- the kernel ---------------------------------------------------------------------------
 
 // kShifted: rows of the output (or of `kept`) may start in the middle of a sector.  A variant of
@@ -596,8 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTmemColumns = 2 * kTileN;  // two accumulators
   constexpr bool kAMn = weight_grad(kMode);
   constexpr bool kBMn = kMode == kFfnGatedGrad || kMode == kFfnProductT || kAMn;
-  constexpr bool kF32 = kMode == kFfnWeightGrad32;
-  constexpr bool kMoreRegs = kF32 || (kMode == kFfnGatedGrad && !kSplit);
+  constexpr bool kF32 = kMode == kFfnWeightGrad32, kLong = kMode == kFfnWeightGradLong;
+  constexpr bool kJoins = kF32 || kLong;
+  constexpr int kPart = kF32 ? kJoin : kLongBlocks;  // blocks of an accumulator, where joined
+  constexpr bool kMoreRegs = kF32 || (kLong && kSplit) || (kMode == kFfnGatedGrad && !kSplit);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Barriers bar;
   __shared__ uint32_t tmem_slot;
@@ -785,9 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kb == ke) continue;
       const uint32_t idesc = idesc_bf16(kTileM * kPair, acc_columns<kMode>(t), kAMn, kBMn);
       for (int k = kb; k < ke && ok; ++k) {
-        // an accumulator takes the whole sum, or kJoin blocks of it
-        const bool begins = kF32 ? (k - kb) % kJoin == 0 : k == kb;
-        const bool ends = k + 1 == ke || (kF32 && (k + 1 - kb) % kJoin == 0);
+        // an accumulator takes the whole sum, or kPart blocks of it
+        const bool begins = kJoins ? (k - kb) % kPart == 0 : k == kb;
+        const bool ends = k + 1 == ke || (kJoins && (k + 1 - kb) % kPart == 0);
         if (begins) ok = __all_sync(0xffffffffu, wait(&bar.acc_empty[acc.slot], acc.phase ^ 1));
         if (ok) ok = __all_sync(0xffffffffu, wait(&bar.full[st.slot], st.phase));
         if (!ok) break;
@@ -855,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kF32) {
         if (!mma && p.accumulate) continue;
         float sum[kMostCols];
-        join_sums<kPair, kMostCols>(bar, taddr + j * cols, cols, (t.blocks + kJoin - 1) / kJoin,
+        join_sums<kPair, kMostCols>(bar, taddr + j * cols, cols, (t.blocks + kPart - 1) / kPart,
                                     work, acc, ok, sum);
         if (R::kTmaOut) {
 #pragma unroll
@@ -883,10 +950,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         continue;
       }
+      if constexpr (kLong)
+        if (t.blocks > kPart) {
+          sum_parts<kMode, kPair>(p, bar, t, taddr + j * cols, kTileN, cols, t.n0 + j * cols, row,
+                                  m < write, work, acc, ok);
+          continue;
+        }
       // the kept values of the next 32 columns are loaded while these are worked on
       const int col_w = t.n0 + j * cols, left_w = min(cols, p.N - col_w);
-      RowIn<kShifted, kMode != kFfnWeightGrad> gates, ups;
-      const uint16_t *kept = kMode == kFfnWeightGrad ? out_row<kMode>(p, 0, row, t.e) + col_w
+      RowIn<kShifted, !weight_grad(kMode)> gates, ups;
+      const uint16_t *kept = weight_grad(kMode) ? out_row<kMode>(p, 0, row, t.e) + col_w
                                                      : p.kept + row * 2 * p.N + col_w;
       const bool loads = mine && (kMode == kFfnGatedGrad || kAdds);
       // gate and up 32 columns ahead; of the values that are added to, 64: every second 32
@@ -1001,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each CTA gets the sums of kTileN / split columns from all of them, in shared memory
     // over the stages: [source][4 columns][row][4], so that a warp writes 512 bytes in a row
     // (rows apart, a tile of 128 rows took 25 us to change hands).  Its own part it reads from
-    // TMEM again (in 32 bits, where it is in registers: from there too).
+    // TMEM again (of joined sums, which are in registers: from there too).
     const Tile t = tile0;
     const int S = p.split, wide = kTileN / S;       // accumulator columns of a CTA
     const int kb = part(t.blocks, part_rank), ke = part(t.blocks, part_rank + 1);
@@ -1012,10 +1085,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, j = (warp - 4) >> 2, m = quarter * 32 + lane;
     const bool work = quarter * 32 < used;  // any row of the warp
     const uint32_t ta = tmem + (uint32_t)(quarter * 32) * 65536u + j * (kTileN / 2);
-    float sum[kF32 ? kTileN / 2 : 1];
-    if constexpr (kF32) {
+    float sum[kJoins ? kTileN / 2 : 1];
+    if constexpr (kJoins) {
       Ring<2> acc;
-      join_sums<1, kTileN / 2>(bar, ta, kTileN / 2, (ke - kb + kJoin - 1) / kJoin, work, acc, ok,
+      join_sums<1, kTileN / 2>(bar, ta, kTileN / 2, (ke - kb + kPart - 1) / kPart, work, acc, ok,
                                sum);
     } else {
       ok = __all_sync(0xffffffffu, wait(&bar.acc_full[0], 0));
@@ -1030,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cc = kMode == kFfnGated ? c : j * (kTileN / 2) + c;
         const int per = kMode == kFfnGated ? wide / 2 : wide;
         const int to = cc / per;
-        if (!kF32 && to == part_rank) return;
+        if (!kJoins && to == part_rank) return;
         const int piece = (cc - to * per + (kMode == kFfnGated ? j * per : 0)) / 4;
         const uint32_t base =
             cluster_map(smem, to * kPair + half_rank) +
@@ -1041,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_cluster_v4(base + (uint32_t)(x * kTileM * 16), v[4 * x], v[4 * x + 1],
                           v[4 * x + 2], v[4 * x + 3]);
       };
-      if constexpr (kF32) {
+      if constexpr (kJoins) {
 #pragma unroll
         for (int c = 0; c < kTileN / 2; c += 16) {
           float v[16];
@@ -1083,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v[16], u[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x) v[x] = u[x] = 0.f;
-      if constexpr (!kF32) {
+      if constexpr (!kJoins) {
         uint32_t d[16], d2[16];
         tmem_load16(own + g * 16, d);
         if constexpr (kMode == kFfnGated) tmem_load16(own + kTileN / 2 + g * 16, d2);
@@ -1098,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (m < write) {
 #pragma unroll
         for (int s = 0; s < kMaxSplit; ++s) {
-          if (s >= S || (!kF32 && s == part_rank)) continue;
+          if (s >= S || (!kJoins && s == part_rank)) continue;
           const float4 *from = in + (s * (wide / 4) + g * 4) * kTileM + m;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -1252,7 +1325,7 @@ cudaError_t launch_form(const Maps &maps, FfnParams p, int64_t tiles, int use, i
 // (all of it stores, which two CTAs wait for together), of 192 520 and 485, of 1024 1590 and
 // 1400, in 32 bits of 128 820 and 785.
 template <int kMode>
-constexpr int64_t kPairRows = kMode == kFfnWeightGrad ? 176 : kMode == kFfnWeightGrad32 ? 0 : 128;
+constexpr int64_t kPairRows = weight_grad16(kMode) ? 176 : weight_grad(kMode) ? 0 : 128;
 
 template <int kMode>
 cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
@@ -1346,17 +1419,36 @@ cudaError_t launch_mode(const FfnParams &p0, int sm_cap, cudaStream_t s) {
   if constexpr (kMode != kFfnWeightGrad32) {
     const auto on_32 = [](const void *x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
     const bool shifted = p.N % 16 != 0 || !on_32(p.out) || !on_32(p.out2) || !on_32(p.kept);
-    if constexpr (kMode == kFfnWeightGrad)
+    if constexpr (weight_grad(kMode))
       if (p.accumulate) return shifted ? launch(yes, yes) : launch(no, yes);
     if (shifted) return launch(yes, no);
   }
   return launch(no, no);
 }
 
+// Whether an expert may have more rows than one accumulator takes.
+bool long_sums(int mode, const FfnParams &p) {
+  int64_t most = p.s.rows;
+  if (p.s.cnt_e != nullptr)
+    most = std::min(p.max_segments, p.s.fixed_cap > 0 ? (int64_t)p.s.fixed_cap : p.s.rows);
+  return mode == kFfnWeightGrad && most > (int64_t)kLongBlocks * kBlockK;
+}
+
 }  // namespace
 
-size_t ffn_workspace(int mode, const FfnParams &p) {
-  return weight_grad(mode) && p.s.cnt_e != nullptr ? 2 * sizeof(CUtensorMap) * p.s.E : 0;
+size_t ffn_workspace(int mode, FfnParams *p, void *ws) {
+  if (!weight_grad(mode)) return 0;
+  const size_t maps = p->s.cnt_e != nullptr ? 2 * sizeof(CUtensorMap) * p->s.E : 0;
+  size_t sums = 0;
+  if (long_sums(mode, *p)) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess) sums = (size_t)kSumsBytes * device_sm_count(dev);
+  }
+  if (ws != nullptr) {
+    if (maps > 0) p->seg_maps = ws;
+    if (sums > 0) p->sums = reinterpret_cast<float4 *>(static_cast<char *>(ws) + maps);
+  }
+  return maps + sums;
 }
 
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s) {
@@ -1375,7 +1467,8 @@ cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s)
     case kFfnProductT:
       return launch_mode<kFfnProductT>(p, sm_cap, s);
     case kFfnWeightGrad:
-      return launch_mode<kFfnWeightGrad>(p, sm_cap, s);
+      return long_sums(mode, p) ? launch_mode<kFfnWeightGradLong>(p, sm_cap, s)
+                                : launch_mode<kFfnWeightGrad>(p, sm_cap, s);
     default:
       return launch_mode<kFfnWeightGrad32>(p, sm_cap, s);
   }

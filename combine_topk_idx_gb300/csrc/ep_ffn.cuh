@@ -5,9 +5,11 @@
 
 namespace ep {
 
-// Weight gradients: BF16, and in 32 bits.
+// Weight gradients: BF16, in 32 bits, and BF16 where an expert may have so many rows that
+// their sum is joined of parts (a form of the first that its launch chooses).
 enum FfnMode {
-  kFfnGated, kFfnGatedGrad, kFfnProduct, kFfnProductT, kFfnWeightGrad, kFfnWeightGrad32
+  kFfnGated, kFfnGatedGrad, kFfnProduct, kFfnProductT, kFfnWeightGrad, kFfnWeightGrad32,
+  kFfnWeightGradLong
 };
 
 // The rows of each expert: of an expanded layout, or (cnt_e NULL, E = 1) all rows.
@@ -58,11 +60,12 @@ struct FfnParams {
   // of tiles; weight gradient: of an expert's matrix
   Reciprocal groups, raster_tiles, expert_tiles;
   void *seg_maps;           // workspace: two tensor maps per expert
+  float4 *sums;             // workspace: sums between the parts of a long one
   unsigned *err;            // the handle's error word (EP_ERRBIT_TIMEOUT), or nullptr
 };
 
-// Bytes of workspace (FfnParams::seg_maps, 128-byte aligned); 0: none.
-size_t ffn_workspace(int mode, const FfnParams &p);
+// Bytes of workspace (128-byte aligned), which p is pointed into if it is given; 0: none.
+size_t ffn_workspace(int mode, FfnParams *p, void *ws);
 cudaError_t launch_ffn(int mode, const FfnParams &p, int sm_cap, cudaStream_t s);
 
 // Few rows, weights streamed into registers: whether a call is one of these, and its launch.

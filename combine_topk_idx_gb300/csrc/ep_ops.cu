@@ -108,12 +108,12 @@ FfnParams ffn_params(const ep_handle *h, int64_t rows) {
 
 ep_status run_ffn(int mode, FfnParams &p, const ep_handle *h, ep_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t bytes = ffn_workspace(mode, p);
+  const size_t bytes = ffn_workspace(mode, &p, nullptr);
   void *ws = nullptr;
   if (bytes > 0) {
     const cudaError_t e = workspace_alloc(bytes, s, &ws);
     if (e != cudaSuccess) return cuda_status(e);
-    p.seg_maps = ws;
+    ffn_workspace(mode, &p, ws);
   }
   cudaError_t e = launch_ffn(mode, p, h != nullptr ? h->cfg.num_sms : 0, s);
   if (ws != nullptr) {

@@ -564,7 +564,8 @@ EP_API ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int
  *   grad[r, i] * a[r, j]; with `accumulate` added to what grad_w holds (in fp32, then
  *   rounded; a subnormal value may count as zero).  An expert without rows has zeros, or
  *   is left as it is.
- * With a handle it uses a stream-ordered workspace of 256 bytes per expert.
+ * With a handle it uses a stream-ordered workspace of 256 bytes per expert; in BF16, if an
+ * expert may have more than 131072 rows, 128 KB per SM more.
  */
 EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n, int32_t k,
                                     const void *grad, int64_t grad_stride, const void *a,

@@ -151,6 +151,48 @@ def test_outputs_left_out(ep, rows, keep):
     assert torch.equal(act, ep.ep_ffn_gated(None, x, w, gate_up=gu))
 
 
+# sums of so many rows that they are joined of parts (131072 rows each): one matrix shared by a
+# cluster, by pairs; a layout's by pairs and by single CTAs (num_sms 1; few slots per expert).
+# name: (experts, rows, n, k, num_sms)
+LONG = {"cluster": (0, (1 << 22) + 37, 40, 24, 0), "just_more": (0, 131073, 72, 48, 0),
+        "tiles": (0, 300_001, 1160, 1160, 0), "pairs": (2, (1 << 21) + 5, 40, 264, 0),
+        "pairs_aligned": (3, (1 << 21) + 5, 136, 272, 0), "ctas": (2, (1 << 21) + 5, 40, 264, 1),
+        "ctas_aligned": (1, 1 << 21, 136, 272, 1), "many_experts": (1024, 140_001, 24, 40, 0)}
+
+
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_weight_gradient_of_very_many_rows(ep, name):
+    """Sums of one sign: what the tensor cores cut off adds up, at most two units (2^-23) of the
+    sum so far every 16 rows, half of that on average over a growing sum, so 2^-10 in a part."""
+    E, T, n, k, sms = LONG[name]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    h, rows, starts, counts = None, T, [0], [T]
+    if E:
+        idx = torch.full((T, 1), E // 2, dtype=torch.int64, device="cuda")
+        idx[:1000] = 0
+        h = ep.ep_layout(ep.make_config(T, 1, E, 1, 128, T, 1, do_expand=True, num_sms=sms), idx)
+        rows, starts = h.rows_alloc, h.tensor("psum_expert").tolist()[:-1]
+        counts = h.tensor("cnt_expert").tolist()
+    g, a = (torch.rand(rows, c, generator=gen, device="cuda").bfloat16() for c in (n, k))
+    for accumulate in (False, True):
+        lead = () if h is None else (E,)
+        got = torch.full((*lead, n, k), 64.0, dtype=torch.bfloat16, device="cuda")
+        ep.ep_ffn_weight_grad(h, g, a, got, accumulate=accumulate)
+        for e in {0, E // 2}:
+            s = slice(starts[e], starts[e] + counts[e])
+            want = sum(g[i:min(i + 65536, s.stop)].double().t() @ a[i:min(i + 65536, s.stop)].double()
+                       for i in range(s.start, s.stop, 65536))
+            want += 64.0 * accumulate
+            err = ((got if h is None else got[e]).double() - want).abs()
+            assert (err <= (2.0 ** -8 * (1 + 2.0 ** -9) + 2.0 ** -10 + 2.0 ** -18) * want).all(), (
+                e, float((err / want).max()))
+        if E > 3:
+            assert (got[3] == (64 if accumulate else 0)).all()  # no rows
+    if h is not None:
+        assert int(h.tensor("error_word")[0]) & ep.EP_ERRBIT_TIMEOUT == 0
+        h.free()
+
+
 def calls(ep, h, rows, n, k, seed=9):
     """{name: call of (outputs, stream)} and the outputs of each, for one set of inputs."""
     g = torch.Generator().manual_seed(seed)
