@@ -147,10 +147,12 @@ class GradPlan:
     GPU.  A tensor that is given another storage (``set_``, ``.data``) needs a new plan:
     this one goes on with the memory it listed.  A storage that is resized
     (``untyped_storage().resize_``, ``resize_`` to more than it holds) has given that
-    memory back, and calls with the plan are refused."""
+    memory back, and calls with the plan are refused.  With ``clips`` false it is for
+    :func:`ep_grad_norm` only, and the gradients may overlap."""
 
     def __init__(self, grads: Sequence[torch.Tensor],
-                 out: Optional[Sequence[torch.Tensor]] = None):
+                 out: Optional[Sequence[torch.Tensor]] = None, clips: bool = True):
+        self.clips = clips
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
@@ -178,7 +180,8 @@ class GradPlan:
         self._f32 = (ctypes.c_uint8 * n)(*[t.dtype == torch.float32 for t in self.grads])
         # behind the addresses: data_ptr() gives a lazy copy memory of its own
         self._memory = _Memory(self.grads if out is None else self.grads + self.out)
-        self._refuse_overlap()
+        if clips:
+            self._refuse_overlap()
 
     def _refuse_overlap(self):
         def spans(ts):
@@ -211,8 +214,10 @@ def _clip(grads, max_norm, out, write, norm, stream):
         plan = grads
         if plan._memory.moved():
             raise ValueError("a storage of the plan was resized: its tensors need a new plan")
+        if write and not plan.clips:
+            raise ValueError("the plan is for the norm only")
     else:
-        plan = GradPlan(grads, out)
+        plan = GradPlan(grads, out, write)
     max_norm = float(max_norm)
     if math.isnan(max_norm) or max_norm < 0:
         raise ValueError(f"max_norm = {max_norm}")
@@ -233,7 +238,7 @@ def _clip(grads, max_norm, out, write, norm, stream):
 def ep_grad_norm(grads: Union[GradPlan, Sequence[torch.Tensor]],
                  norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The 2-norm of all gradients together, an fp32 tensor without dimensions on the
-    GPU (``ep_clip_grads`` without outputs)."""
+    GPU (``ep_clip_grads`` without outputs).  The same values may be in it twice."""
     return _clip(grads, math.inf, None, False, norm, stream)
 
 

@@ -141,6 +141,19 @@ def test_norm_only(ep):
     assert all(torch.equal(a, b) for a, b in zip(grads, before))
 
 
+def test_norm_of_overlapping_gradients(ep):
+    """Nothing is written: each counts as often as it is listed."""
+    a, b = tensors([1000, 9000], 10, (torch.float32,))
+    grads = [a, a, b, b[500:], a[:7]]
+    want = P.global_norm([f64(t) for t in grads])
+    plan = ep.GradPlan(grads, clips=False)
+    for given in (grads, plan):
+        assert abs(float(ep.ep_grad_norm(given)) - want) <= NORM * want
+    for given in (grads, plan):
+        with pytest.raises(ValueError):
+            ep.ep_clip_grads(given, 1.0)
+
+
 def test_plan_is_used_again(ep):
     """A plan follows the values of its tensors."""
     grads = tensors([5000, 40, 8193], 11)
