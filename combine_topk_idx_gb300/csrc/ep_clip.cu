@@ -5,10 +5,11 @@
 // Two passes over the gradients with the norm between them: the first leaves a sum
 // per CTA, the second starts by adding all of these up, in the same fixed order in
 // every CTA, so neither a counter nor a third launch stands between them.  Few and
-// small tensors are one launch of a cluster, whose CTAs read each other's sums.  The
-// tensors' addresses travel as launch parameters (up to kMost per launch): nothing
-// is copied to the device first.  Both passes are bound by memory.  The second
-// goes through each CTA's part backwards: what the first read last is still in L2.
+// small tensors are one launch of a cluster, where the GPU holds it, whose CTAs read
+// each other's sums.  The tensors' addresses travel as launch parameters (up to kMost
+// per launch): nothing is copied to the device first.  Both passes are bound by memory.
+// The second goes through each CTA's part backwards: what the first read last is still
+// in L2.
 //
 // Sums.  A thread adds up the squares of at most 64 elements in fp32, then goes on in
 // fp64, so the error does not grow with the number of elements.  Squares that leave
@@ -409,34 +410,12 @@ Extent extent(const GradList &l) {
   }
   return x;
 }
-bool one_cluster(const Extent &x) { return x.tensors <= kFew && x.pieces <= kClusterPieces; }
 
-// Clusters of more than 8 CTAs are opted in to, once per device.
-cudaError_t allow_cluster() {
-  static std::mutex mu;
-  static std::vector<int> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  if (std::find(done.begin(), done.end(), dev) != done.end()) return cudaSuccess;
-  e = cudaFuncSetAttribute(grad_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) try {
-      done.push_back(dev);
-    } catch (...) {  // no memory: opted in again
-    }
-  return e;
-}
-
-cudaError_t launch_cluster(const Table<kFew> &t, bool write, float max_norm, float *norm,
-                           cudaStream_t s) {
-  const cudaError_t e = allow_cluster();
-  if (e != cudaSuccess) return e;
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], cudaStream_t s) {
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(kClusterCtas);
   lc.blockDim = dim3(kClusterThreads);
   lc.stream = s;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -444,6 +423,44 @@ cudaError_t launch_cluster(const Table<kFew> &t, bool write, float max_norm, flo
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 2;
+  return lc;
+}
+
+// Whether the current device takes the cluster (of more than 8 CTAs: opted in to; part of a
+// GPU may not hold it).  Looked up once per device.
+bool cluster_fits() {
+  struct Entry {
+    int device;
+    bool fits;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> known;
+  int dev = 0, clusters = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> g(mu);
+  for (const Entry &e : known)
+    if (e.device == dev) return e.fits;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc = cluster_config(attr, nullptr);
+  const bool fits =
+      cudaFuncSetAttribute(grad_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                           1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, grad_cluster_kernel, &lc) == cudaSuccess &&
+      clusters > 0;
+  try {
+    known.push_back({dev, fits});
+  } catch (...) {  // no memory: looked up again
+  }
+  return fits;
+}
+bool one_cluster(const Extent &x) {
+  return x.tensors <= kFew && x.pieces <= kClusterPieces && cluster_fits();
+}
+
+cudaError_t launch_cluster(const Table<kFew> &t, bool write, float max_norm, float *norm,
+                           cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc = cluster_config(attr, s);
   return cudaLaunchKernelEx(&lc, grad_cluster_kernel, t, write, max_norm, norm);
 }
 
@@ -460,7 +477,7 @@ size_t clip_workspace(const GradList &l, int sms) {
 cudaError_t launch_clip(const GradList &l, float max_norm, float *norm, void *workspace, int sms,
                         cudaStream_t s) {
   const Extent x = extent(l);
-  if (one_cluster(x)) {
+  if (workspace == nullptr) {
     Table<kFew> t;
     int at = 0;
     fill<32>(l, &at, &t);

@@ -14,6 +14,7 @@ struct GradList {
   const uint8_t *is_f32;
 };
 
+// Bytes of workspace; 0: one cluster does it all, and launch_clip's is NULL.
 size_t clip_workspace(const GradList &l, int sms);
 cudaError_t launch_clip(const GradList &l, float max_norm, float *norm, void *workspace, int sms,
                         cudaStream_t s);

@@ -69,6 +69,25 @@ def test_in_place_and_into_others(ep, name, max_norm):
     check(ep, grads, max_norm)
 
 
+# one launch of a cluster up to 64 tensors that are not empty and 1024 pieces of 4 KB, each
+# tensor rounded up to whole ones; else two launches
+FORMS = {"all_pieces": ([1024 * 1024], torch.float32, 1),
+         "a_value_more": ([1024 * 1024 + 1], torch.float32, 2),
+         "all_tensors": ([15 * 2048 + 1] * 64 + [0, 0], torch.bfloat16, 1),
+         "a_value_more_in_one": ([16 * 2048] * 63 + [16 * 2048 + 1], torch.bfloat16, 2),
+         "a_tensor_more": ([0, 1] * 65, torch.bfloat16, 2)}
+
+
+@pytest.mark.parametrize("name", sorted(FORMS))
+def test_where_the_forms_meet(ep, name):
+    from tests.test_ops_sm_cap_gpu import grids
+    sizes, kind, launches = FORMS[name]
+    grads = tensors(sizes, 21, (kind,))
+    out = [torch.full_like(t, 7.0) for t in grads]
+    check(ep, grads, 1.0, out)
+    assert len(grids(lambda: ep.ep_clip_grads(grads, 1.0, out=out))) == launches
+
+
 @pytest.mark.parametrize("shift", range(8))
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
 def test_alignments(ep, kind, shift):
