@@ -537,3 +537,29 @@ def test_num_sms(ep, op, cap):
             h.free()
         for k, t in got[0].items():
             assert torch.equal(t, got[1][k]), k
+
+
+@pytest.mark.parametrize("cap", [1, 2, 5])
+@pytest.mark.parametrize("op", OPS)
+def test_num_sms_by_residency(ep, op, cap):
+    """What a capped call launches fits that many SMs at once: of the tensor cores' kernel one
+    CTA an SM (its shared memory), of few rows' two, of the small kernel before a weight
+    gradient eight.  Uncapped the same calls take more."""
+    from tests.test_ops_sm_cap_gpu import grids
+    for T, K, E in ((200, 2, 32), (1500, 2, 2), (7, 2, 32)):
+        most = {}
+        for c in (0, cap):
+            h = make_handle(ep, T, K, E, 1, T, 1, num_sms=c)
+            call, outputs = calls(ep, h, h.rows_alloc, 1032, 200)[op]
+            o = outputs()
+            launched = grids(lambda: call(o, None))
+            most[c] = launched[-1]
+            if op.startswith("wgrad"):
+                assert len(launched) == 2
+                if c:
+                    assert launched[0] <= 8 * c
+            else:
+                assert len(launched) == 1
+            h.free()
+        per_sm = 2 if T * K <= 16 and op in ("gated", "product") else 1
+        assert most[cap] <= per_sm * cap < most[0]
