@@ -59,7 +59,8 @@ def ep_ffn_gated_backward(handle: Optional[Handle], grad_out: torch.Tensor, w: t
     """Gradient of ``gate_up`` through the down projection (``ep_ffn_gated_backward``):
     ``grad_out`` BF16 [rows, n] (may be row-strided), ``w`` BF16 [E, n, ffn] ([n, ffn]
     without a handle).  Returns ``grad_gate_up`` BF16 [rows, 2 * ffn]; ``act`` BF16
-    [rows, ffn], the forward's activation once more, is written if given."""
+    [rows, ffn], the activation of gate and up as kept (rounded: not the forward's bits),
+    is written if given."""
     c = _Call("ep_ffn_gated_backward", stream)
     hp, rows = _rows(handle, grad_out, "grad_out")
     wp, n, ffn = _matrix(c, handle, w, "w")

@@ -199,7 +199,8 @@ __device__ __forceinline__ void scale_piece(const void *from, void *to, int len,
     else
       reinterpret_cast<float *>(o)[i] = reinterpret_cast<const float *>(p)[i] * by;
   }
-  constexpr int kBatch = 4;  // in flight: more would not fit the registers
+  // in flight; with the 64 registers of four CTAs to an SM 52 bytes spill
+  constexpr int kBatch = 4;
 #pragma unroll 1
   for (int u0 = 0; u0 < kLoads; u0 += kBatch) {
     // kBatch * 32 vectors of a warp in a row

@@ -4,10 +4,11 @@
 //   gated        h = x W^T, W [2F, K] gate rows then up rows;
 //                act = silu(h_gate) * h_up, and h itself for the backward pass
 //   gated grad   d = g W, W [K, F] the down projection; with the forward's h:
-//                dh = (d h_up silu'(h_gate), d silu(h_gate)), act once more
+//                dh = (d h_up silu'(h_gate), d silu(h_gate)), and act of h as kept
 //   product      out = a W^T, W [N, K], or a W, W [K, N] (transposed)
 //   weight grad  W'[e] = sum over e's rows of g[r]^T a[r]
-// Sums in fp32 (TMEM), each output rounded once.
+// Sums in fp32 (TMEM; long ones of a weight gradient joined of parts), each output rounded
+// once.
 //
 // A tile is 128 rows x 256 columns of a CTA's TMEM (gated: 128 gate columns and
 // the 128 up columns beside them).  Warps of a CTA:
@@ -30,12 +31,13 @@
 // Up to 16 rows in all are ep_ffn_rows.cu's, if gated or a product on W's rows.
 //
 // What bounds it (times move by 8 % with the GPU and what it ran before: the power cap sets
-// its clock).  Large tiles, the tensor cores: a block of a 256 x 256 tile takes 521 cycles
-// where its products need 512; 8192 x 8192 x 4096 takes 276 us, 2.0 PFLOP/s, and 264 as a
-// library's product.  What an epilogue reads and writes competes with the operands for L2:
+// its clock; sizes are rows x n x k as the calls name them, n of a gated product gate and up
+// together).  Large tiles, the tensor cores: a block of a 256 x 256 tile takes 521 cycles
+// where its products need 512; 8192 x 8192 x 4096 takes 268 to 290 us, up to 2.05 PFLOP/s, and
+// as torch.matmul, timed in turn with it, 266 to 290.  What an epilogue reads and writes competes with the operands for L2:
 // the gated gradient of that size moves 670 MB more and takes 353 us.  128 rows per expert,
 // the weights' bytes: 256 experts of 4096 x 7168, 2.46 ms for 15.9 GB, 6.5 TB/s.  Few rows
-// through one matrix, latency: 128 x 2048 x 7168 takes 10.0 us, of them 1.2 before the first
+// through one matrix, latency: 128 x 7168 x 2048 takes 10.0 us, of them 1.2 before the first
 // copy and 2 from the last product to the end.
 //
 // Rows that are not an expert's own never reach its results: in the row products
@@ -650,8 +652,8 @@ __device__ __forceinline__ void sum_parts(const FfnParams &p, Barriers &bar, con
 // ---- the kernel ---------------------------------------------------------------------------
 
 // kShifted: rows of the output (or of `kept`) may start in the middle of a sector.  A variant of
-// its own, as RowOut costs the others instructions: 8192 x 6784 x 256 gated took 71 us, with
-// it 82.  kAdds: a weight's gradient in BF16 is added to what is there (64 experts of 2048 x
+// its own, as RowOut costs the others instructions: 8192 x 13568 x 256 gated takes 50 us, with
+// it 61.  kAdds: a weight's gradient in BF16 is added to what is there (64 experts of 2048 x
 // 4096, 512 tokens, top-8, without adding: 198 us, with the code for it 239).
 template <int kMode, int kPair, bool kSplit, bool kShifted, bool kAdds>
 __global__ void __launch_bounds__(kThreads, 1)

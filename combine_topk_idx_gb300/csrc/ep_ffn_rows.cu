@@ -9,12 +9,12 @@
 // and of x, and a sum has no order.  The warps' sums meet in shared memory, in a fixed order.
 //
 // No stages, no cluster, no TMEM: what the tcgen05 form does around its products is a third of
-// so short a call.  Weights read from HBM, 7168 x 4096 gated (58.7 MB, 8.8 us at what a copy
-// reaches): 10.5 us for 1 row, 10.9 for 8, 12.3 for 16, where that form takes 14.5; 2048 x
-// 7168 as a product 6.6, 6.8 and 8.9 us for 10.4.  What a row more costs is reading x in every
+// so short a call.  Weights read from HBM, 4096 x 7168 gated (58.7 MB, 8.8 us at what a copy
+// reaches): 10.5 us for 1 row, 10.9 for 8, 12.3 for 16, where that form takes 14.5; 7168 x
+// 2048 as a product 6.6, 6.8 and 8.9 us for 10.4.  What a row more costs is reading x in every
 // CTA.  Half or twice as many warps, CTAs per SM or loads ahead change nothing.  One token
-// through 2 of 8 experts (4096 x 4096 gated): 14.4 us, by tcgen05 27; through 8 of 256 (7168 x
-// 4096) 76 and 79.
+// through 2 of 8 experts (4096 x 4096 gated): 14.4 us, by tcgen05 27; through 8 of 256 (4096 x
+// 7168) 76 and 79.
 #include <algorithm>
 
 #include "ep_ffn.cuh"

@@ -513,8 +513,9 @@ EP_API ep_status ep_expert_gemm(const ep_handle *h, int32_t n, int32_t k, const 
  * grad) may be row-strided (elements, a multiple of 8, at least the row's length).
  * Outputs overlap neither each other nor an input.
  * Sizes n, k, ffn: multiples of 8, at most EP_MAX_GEMM (ffn: half of that).
- * 16-byte aligned.  Sums are fp32, each output is rounded once.  The same call gives
- * the same bits each time.  A device-side wait that gives up leaves NaN in the tiles
+ * 16-byte aligned.  Sums are fp32 (the tensor cores cut off what does not fit, at most
+ * 2^-23 of the sum so far every 16 terms), each output is rounded once.  The same call
+ * gives the same bits each time.  A device-side wait that gives up leaves NaN in the tiles
  * it was for and, with a handle, sets EP_ERRBIT_TIMEOUT.
  */
 
@@ -538,7 +539,8 @@ EP_API ep_status ep_ffn_gated(const ep_handle *h, int64_t rows, int32_t ffn, int
  * With d = grad_out W (fp32), g, u of gate_up, s = sigmoid(g):
  *   grad_gate_up BF16 [rows, 2 * ffn]: d * u * s * (1 + g * (1 - s)), then d * g * s;
  *   act BF16 [rows, ffn], or NULL: g * s * u, which the down projection's
- *     ep_ffn_weight_grad takes (so that the forward need not keep it).
+ *     ep_ffn_weight_grad takes (so that the forward need not keep its own, whose g and u
+ *     were not rounded).
  */
 EP_API ep_status ep_ffn_gated_backward(const ep_handle *h, int64_t rows, int32_t ffn, int32_t n,
                                        const void *grad_out, int64_t grad_out_stride,
@@ -562,7 +564,8 @@ EP_API ep_status ep_ffn_product(const ep_handle *h, int64_t rows, int32_t n, int
  * grad: BF16 [rows, n], gradient of the projection's output; a: BF16 [rows, k], its input.
  * grad_w: fp32 or BF16 [E, n, k]: sum over the rows r of expert e of
  *   grad[r, i] * a[r, j]; with `accumulate` added to what grad_w holds (in fp32, then
- *   rounded; a subnormal value may count as zero).  An expert without rows has zeros, or
+ *   rounded; a subnormal value may count as zero).  Sums are joined of parts, rounded to
+ *   nearest: fp32 of 512 rows, BF16 of 131072.  An expert without rows has zeros, or
  *   is left as it is.
  * With a handle it uses a stream-ordered workspace of 256 bytes per expert; in BF16, if an
  * expert may have more than 131072 rows, 128 KB per SM more.
@@ -578,16 +581,18 @@ EP_API ep_status ep_ffn_weight_grad(const ep_handle *h, int64_t rows, int32_t n,
  * count: tensors; grads, numels, is_fp32 and outs are HOST arrays of that length,
  *   read before the call returns.  Tensor i: numels[i] elements, fp32 or BF16,
  *   contiguous, aligned to its element's size; empty ones are skipped.
- *   norm = sqrt(sum of all squares), fp32 sums of at most 66 squares joined in fp64;
+ *   norm = sqrt(sum of all squares), fp32 sums of at most 65 squares joined in fp64;
  *     finite whenever fp32 holds it, though the squares may not be.
  *   c = 1 if norm + 1e-6 <= max_norm, else max_norm / (norm + 1e-6): a norm that is
  *     infinite makes c zero, one that is NaN makes it NaN.
  * outs[i]: c * grads[i] in fp32, rounded to the tensor's type; may be grads[i] itself
  *   (and is then not written if c = 1), else overlaps no gradient and no other
  *   output.  outs NULL: the norm only.
- * norm: device fp32, or NULL if outs is given.  max_norm: >= 0, or infinite.
- * More than 2 MB, or 64 tensors, use a stream-ordered workspace of 8 bytes per CTA.  The
- * same bits each time.
+ * norm: device fp32, or NULL if outs is given; overlaps no gradient and no output.
+ * max_norm: >= 0, or infinite.
+ * More than 4 MB (each tensor rounded up to 4 KB) or 64 tensors that are not empty use a
+ * stream-ordered workspace of 8 bytes per CTA, and so do fewer on a GPU (or part of one) that
+ * holds no cluster of 16 CTAs.  The same bits each time.
  */
 EP_API ep_status ep_clip_grads(int32_t count, const void *const *grads, void *const *outs,
                                const int64_t *numels, const uint8_t *is_fp32, float max_norm,
