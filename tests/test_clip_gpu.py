@@ -237,7 +237,7 @@ def test_memory_in_use_on_another_stream_is_kept(ep):
     torch.cuda.synchronize()
     side, done = torch.cuda.Stream(), torch.cuda.Event()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(400_000_000)  # some 0.2 s
+        torch.cuda._sleep(1_000_000_000)  # some 0.5 s
     ep.ep_clip_grads(plan, 0.5, stream=side)
     done.record(side)
     del plan
