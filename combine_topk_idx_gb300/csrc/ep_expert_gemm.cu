@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < kWarpC / kChunk; ++c) {
                 uint32_t d[kChunk];
                 tmem_load64(ta + c * kChunk, d);
-                tmem_load_wait64(d);
+                tmem_load_wait(d);
                 if (c + 1 == kWarpC / kChunk) {  // read: a later block may overwrite it
                   tc_fence_before();
                   __syncwarp();

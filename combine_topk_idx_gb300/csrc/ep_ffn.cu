@@ -578,7 +578,7 @@ __device__ __forceinline__ void join_sums(Barriers &bar, uint32_t taddr, int col
         if (c >= cols) break;
         uint32_t d[64];
         tmem_load64(taddr + acc.slot * 2 * kHalf + c, d);
-        tmem_load_wait64(d);
+        tmem_load_wait(d);
 #pragma unroll
         for (int x = 0; x < 64; ++x) sum[c + x] += __uint_as_float(d[x]);
       }

@@ -99,12 +99,6 @@ __device__ __forceinline__ void tmem_load64(uint32_t addr, uint32_t *r) {
         "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(addr));
 }
-// Waits for this thread's TMEM loads and orders the uses of r after them.
-__device__ __forceinline__ void tmem_load_wait64(uint32_t *r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
-}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
